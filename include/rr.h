@@ -378,6 +378,159 @@ rr_status rr_plan_end(int32_t *launches);
 rr_status rr_plan_append(void *plan, size_t bytes, const void *other);
 rr_status rr_plan_launch(const void *plan, void *stream);
 
+/*
+ * Sharded losses -- the local work of one rank in the last stage of a training
+ * or scoring step whose vocabulary is split over ranks, and in the routing of
+ * tokens to experts.  Between the calls the caller exchanges small arrays
+ * through its collectives: the statistics and picked logits of every shard
+ * (rr_vocab_stats -> rr_vocab_cross_entropy / rr_vocab_distill), the partial
+ * input gradients (rr_vocab_grad -> an all-reduce sum of dx), the experts'
+ * counts and probability sums (rr_route -> rr_balance_loss).
+ *
+ * All matrices are contiguous and row-major; x, w, dx, dw, the teacher's and
+ * the router's logits have the call's dtype, statistics, losses, weights and
+ * probabilities are float, indices int64_t.  Products, softmax statistics and
+ * sums are accumulated in 32 bits.  A call's outputs must not overlap its
+ * inputs, each other or its workspace (RR_EALIAS).  Results do not depend on
+ * the launch's timing: the same call on the same inputs gives the same bits.
+ * rows == 0 (and vocab == 0 for a shard) is valid.
+ *
+ * `workspace` is device memory of at least the bytes that the matching query
+ * returns, aligned to 256 bytes.  It carries nothing from one call to the
+ * next, so calls on one stream may share it.
+ */
+
+/* One rank's shard [first, first + vocab) of a head over `total` vocabulary
+ * entries: logits z = scale * (x . w) with x [rows][dim] and w [vocab][dim].
+ * topk index entries belong to every row (1 for cross entropy). */
+typedef struct {
+    int64_t vocab, first, total;  /* 0 <= first, 0 <= vocab, first + vocab <= total < 2^31, total >= 1 */
+    int32_t dim;                  /* 1 .. RR_MAX_DIM */
+    int32_t topk;                 /* 1 .. RR_MAX_TOPK */
+    float scale;                  /* finite; 1, or one over the temperature */
+    int32_t reserved;
+} rr_vocab;
+
+#define RR_MAX_DIM 65536
+#define RR_MAX_TOPK 1024
+#define RR_MAX_SHARDS 16
+#define RR_MAX_ROWS (INT64_C(1) << 30)
+
+/*
+ * rr_vocab_workspace -- bytes of workspace that rr_vocab_stats (grad == 0) or
+ * rr_vocab_grad (grad != 0; enough for rr_vocab_stats too) needs; -1 for
+ * arguments that those calls reject (see rr_last_error).
+ */
+int64_t rr_vocab_workspace(const rr_vocab *v, int dtype, int64_t rows, int grad);
+
+/*
+ * rr_vocab_stats -- softmax statistics of this shard's logits, without keeping
+ * the logits.
+ *   index [rows][topk]: vocabulary entries over all shards.  An entry that is
+ *     negative, or not below total, does not count.
+ *   stats [rows][2]: the shard's largest logit m and sum exp(z - m); (-inf, 0)
+ *     for an empty shard or a row whose logits are all -inf.
+ *   picked [rows][topk]: the logits at the entries that this shard holds, 0 at
+ *     every other entry, so that a sum over shards gives them all.
+ */
+rr_status rr_vocab_stats(const rr_vocab *v, int dtype, int64_t rows, const void *x, const void *w,
+                         const int64_t *index, float *stats, float *picked, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
+/*
+ * rr_vocab_cross_entropy -- combines the shards' statistics (topk must be 1;
+ * 1 <= nShards <= RR_MAX_SHARDS arrays each, in the same order; of `v` only
+ * total and topk are used).
+ *   lse [rows] = log sum exp over all shards; logit [rows] = sum of picked;
+ *   loss [rows] = lse - logit, and 0 for a row whose entry does not count.
+ */
+rr_status rr_vocab_cross_entropy(const rr_vocab *v, int64_t rows, const int64_t *index,
+                                 const float *const *stats, const float *const *picked, int nShards,
+                                 float *lse, float *logit, float *loss, void *stream);
+
+/*
+ * rr_vocab_distill -- the divergence of the head from a teacher's top logits.
+ *   teacher [rows][topk]: the teacher's logits of the index entries, in the
+ *     call's dtype; those of entries that do not count are not used.
+ *   prob [rows][topk]: p = softmax of scale * teacher over the entries that
+ *     count; 0 elsewhere, and in a row with no such entry (or whose teacher
+ *     logits are all -inf).
+ *   lse [rows], logit [rows][topk]: as above.
+ *   loss [rows] = sum p (log p - logit + lse) over the entries with p > 0.
+ */
+rr_status rr_vocab_distill(const rr_vocab *v, int dtype, int64_t rows, const int64_t *index,
+                           const void *teacher, const float *const *stats, const float *const *picked,
+                           int nShards, float *lse, float *logit, float *prob, float *loss, void *stream);
+
+/*
+ * rr_vocab_grad -- the gradients of sum_r grad[r] * loss[r] with respect to x
+ * (this shard's part: the sum over shards is the gradient) and w.  The logits
+ * are recomputed in pieces of the vocabulary.
+ *   lse, logit: as written by the combining call; prob: its probabilities, or
+ *     null for cross entropy (topk must be 1 then).
+ *   dz[r][v] = grad[r] * scale * (exp(z - lse) - p), p the summed probability
+ *     of the row's entries equal to v; a row with no target has dz = 0.  For
+ *     bf16, dz is rounded to bf16 before the two products.
+ *   dx [rows][dim] = dz w, dw [vocab][dim] = dz^T x, rounded once.
+ */
+rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *x, const void *w,
+                        const int64_t *index, const float *lse, const float *logit, const float *prob,
+                        const float *grad, void *dx, void *dw, void *workspace, int64_t workspace_bytes,
+                        void *stream);
+
+/* A router of tokens to the topk most likely of `experts` experts. */
+typedef struct {
+    int32_t experts;      /* 1 .. RR_MAX_EXPERTS */
+    int32_t topk;         /* 1 .. min(experts, RR_MAX_ROUTE_TOPK) */
+    int32_t renormalize;  /* weights divided by their sum over the chosen experts */
+    int32_t reserved;
+} rr_router;
+
+#define RR_MAX_EXPERTS 1024
+#define RR_MAX_ROUTE_TOPK 32
+
+/* rr_route_workspace -- bytes of workspace for rr_route (may be 0); -1 for
+ * arguments that it rejects. */
+int64_t rr_route_workspace(const rr_router *r, int64_t rows);
+
+/*
+ * rr_route -- choices, weights and this rank's statistics.
+ *   logits [rows][experts]; keep [rows] bytes, 0 leaves a token out (null: all
+ *     are kept).
+ *   choice [rows][topk]: the experts of the largest logits, largest first, the
+ *     lower index first among equals, NaN above every number; -1 for a token
+ *     left out.
+ *   weight [rows][topk]: p = softmax(logits) of the choices (renormalize: over
+ *     their sum); 0 for a token left out, and where every logit (renormalize:
+ *     every chosen one) is -inf.
+ *   lse [rows]: log sum exp of the logits; 0 for a token left out.
+ *   counts [experts + 1]: tokens per expert, then the tokens kept.
+ *   prob_sum [experts]: the sum of p over the tokens kept.
+ */
+rr_status rr_route(const rr_router *r, int dtype, int64_t rows, const void *logits, const uint8_t *keep,
+                   int32_t *choice, float *weight, float *lse, int32_t *counts, float *prob_sum,
+                   void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * rr_balance_loss -- experts * sum_e f_e P_e over all ranks: with n tokens
+ * kept in all, f_e = counts_e / (n * topk) and P_e = prob_sum_e / n.
+ *   counts, prob_sum: nRanks arrays as rr_route writes them (1 .. RR_MAX_SHARDS).
+ *   loss [1]; slope [experts] = d loss / d p_e of one token = experts * f_e / n.
+ *   Both are 0 when no token is kept.  f is taken as constant.
+ */
+rr_status rr_balance_loss(const rr_router *r, const int32_t *const *counts, const float *const *prob_sum,
+                          int nRanks, float *loss, float *slope, void *stream);
+
+/*
+ * rr_route_grad -- the gradient of grad_loss * loss + sum grad_weight * weight
+ * with respect to this rank's logits, given what rr_route and rr_balance_loss
+ * wrote.  grad_loss [1], grad_weight [rows][topk]; dlogits [rows][experts] in
+ * the call's dtype, 0 for a token left out.
+ */
+rr_status rr_route_grad(const rr_router *r, int dtype, int64_t rows, const void *logits, const uint8_t *keep,
+                        const int32_t *choice, const float *weight, const float *lse, const float *slope,
+                        const float *grad_loss, const float *grad_weight, void *dlogits, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

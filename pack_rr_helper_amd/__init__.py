@@ -493,3 +493,9 @@ def rr_a2a_pack_many(dtype, jobs, stream=None, prepare=False):
 def rr_a2a_unpack_many(dtype, jobs, stream=None, prepare=False):
     """jobs: [(relay, helper, recv, out), ...]"""
     return _a2a_many(load().rr_a2a_unpack_many, dtype, jobs, True, stream, prepare)
+
+
+from . import losses  # noqa: E402  (uses the helpers above)
+from .losses import *  # noqa: E402,F401,F403
+
+__all__ += losses.__all__

@@ -14,7 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "librr.so")
-SOURCES = [os.path.join(CSRC, "rr_kernels.hip"), os.path.join(CSRC, "rr_api.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("rr_kernels.hip", "rr_api.cpp", "rr_loss.cpp", "rr_vocab.hip",
+                                           "rr_route.hip")]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

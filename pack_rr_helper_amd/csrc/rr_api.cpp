@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "rr_internal.h"
+#include "rr_loss.h"
 
 namespace {
 
@@ -98,6 +99,10 @@ hipError_t emit_copy(const rr::CopyBatch &b, int64_t tiles, bool shifted, hipStr
     }
     return hipSuccess;
 }
+
+// A loss operator's launch takes the place of a batch in its record.
+enum : int32_t { kPlanOp = 3 };
+static_assert(sizeof(rr::Op) <= sizeof(rr::RedBatch), "an op is stored in a batch's bytes");
 
 rr_status launch_failed(hipError_t e)
 {
@@ -893,6 +898,43 @@ LaunchShape copy_shape(const CopyBatch &b, int64_t total_tiles)
 
 }  // namespace rr
 
+// ---------------------------------------------------------------------------
+// Operator launches and the error state (declared in rr_loss.h)
+// ---------------------------------------------------------------------------
+
+namespace rr {
+
+hipError_t emit_op(const Op &op, hipStream_t stream)
+{
+    if (!g_plan)
+        return op.launch(op, stream);
+    if (g_plan->count >= g_plan->capacity) {
+        g_plan->broken = 1;
+        return hipErrorOutOfMemory;
+    }
+    PlanRec &r = plan_records(g_plan)[g_plan->count++];
+    r.kind = kPlanOp;
+    r.shifted = 0;
+    r.tiles = 0;
+    memcpy(static_cast<void *>(&r.red), &op, sizeof op);
+    return hipSuccess;
+}
+
+rr_status op_failed(hipError_t e) { return launch_failed(e); }
+
+rr_status set_error(rr_status st, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return st;
+}
+
+rr_status set_ok() { return ok(); }
+
+}  // namespace rr
+
 // ===========================================================================
 // Exported entry points
 // ===========================================================================
@@ -1166,8 +1208,15 @@ rr_status rr_plan_launch(const void *plan, void *stream)
     const hipStream_t st = static_cast<hipStream_t>(stream);
     for (int i = 0; i < h->count; ++i) {
         const rr::PlanRec &r = rec[i];
-        const hipError_t e = r.kind == rr::kPlanReduce ? rr::launch_reduce(r.red, r.tiles, r.shifted != 0, st)
-                                                       : rr::launch_copy(r.copy, r.tiles, r.shifted != 0, st);
+        hipError_t e;
+        if (r.kind == kPlanOp) {
+            rr::Op op;
+            memcpy(&op, static_cast<const void *>(&r.red), sizeof op);
+            e = op.launch(op, st);
+        } else {
+            e = r.kind == rr::kPlanReduce ? rr::launch_reduce(r.red, r.tiles, r.shifted != 0, st)
+                                          : rr::launch_copy(r.copy, r.tiles, r.shifted != 0, st);
+        }
         if (e != hipSuccess)
             return fail(RR_EHIP, "kernel launch %d of the plan failed: %s", i, hipGetErrorString(e));
     }

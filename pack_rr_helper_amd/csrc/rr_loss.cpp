@@ -1,0 +1,498 @@
+// rr_loss.cpp -- the C ABI of the sharded losses (rr.h): argument validation,
+// the division of the workspace, and the launches of each call.  Everything is
+// rejected before any HIP call; nothing is allocated on the device.
+#include "rr_loss.h"
+
+#include <math.h>
+
+#include <algorithm>
+
+namespace {
+
+using namespace rr;
+
+int64_t elem_size(int dtype) { return dtype == RR_F32 ? 4 : 2; }
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+rr_status check_dtype(int dtype)
+{
+    if (dtype != RR_F32 && dtype != RR_BF16)
+        return set_error(RR_EINVAL, "unknown dtype %d", dtype);
+    return RR_OK;
+}
+
+rr_status check_rows(int64_t rows)
+{
+    if (rows < 0 || rows > RR_MAX_ROWS)
+        return set_error(RR_EINVAL, "rows=%lld outside [0, RR_MAX_ROWS]", (long long)rows);
+    return RR_OK;
+}
+
+rr_status check_vocab(const rr_vocab *v)
+{
+    if (!v)
+        return set_error(RR_EINVAL, "vocabulary descriptor is null");
+    if (v->total < 1 || v->total > INT32_MAX)
+        return set_error(RR_EINVAL, "total=%lld outside [1, 2^31)", (long long)v->total);
+    if (v->vocab < 0 || v->first < 0 || v->first > v->total || v->vocab > v->total - v->first)
+        return set_error(RR_EINVAL, "shard [first=%lld, + vocab=%lld) outside [0, total=%lld)",
+                         (long long)v->first, (long long)v->vocab, (long long)v->total);
+    if (v->dim < 1 || v->dim > RR_MAX_DIM)
+        return set_error(RR_EINVAL, "dim=%d outside [1, RR_MAX_DIM]", v->dim);
+    if (v->topk < 1 || v->topk > RR_MAX_TOPK)
+        return set_error(RR_EINVAL, "topk=%d outside [1, RR_MAX_TOPK]", v->topk);
+    if (!isfinite(v->scale))
+        return set_error(RR_EINVAL, "scale is not finite");
+    return RR_OK;
+}
+
+// The buffers of one call: each checked for null and alignment, the written
+// ones against every other.
+class Buffers {
+public:
+    Buffers &in(const void *p, int64_t bytes, int64_t align, const char *what) { return add(p, bytes, align, what, false); }
+    Buffers &out(const void *p, int64_t bytes, int64_t align, const char *what) { return add(p, bytes, align, what, true); }
+
+    rr_status check()
+    {
+        if (st_ != RR_OK)
+            return st_;
+        for (int i = 0; i < n_; ++i)
+            for (int j = 0; j < i; ++j)
+                if ((b_[i].written || b_[j].written) && b_[i].lo < b_[j].hi && b_[j].lo < b_[i].hi)
+                    return set_error(RR_EALIAS, "%s overlaps %s", b_[i].what, b_[j].what);
+        return RR_OK;
+    }
+
+private:
+    struct Buf {
+        uintptr_t lo, hi;
+        const char *what;
+        bool written;
+    };
+    Buffers &add(const void *p, int64_t bytes, int64_t align, const char *what, bool written)
+    {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        if (st_ != RR_OK || bytes <= 0)
+            return *this;
+        if (!p)
+            st_ = set_error(RR_EINVAL, "%s is null", what);
+        else if (lo % uintptr_t(align))
+            st_ = set_error(RR_EINVAL, "%s=%p is not aligned to %lld bytes", what, p, (long long)align);
+        else
+            b_[n_++] = Buf{lo, lo + uintptr_t(bytes), what, written};
+        return *this;
+    }
+    Buf b_[2 * RR_MAX_SHARDS + 16];
+    int n_ = 0;
+    rr_status st_ = RR_OK;
+};
+
+// The launches of one call, up to the first that fails.
+class Launches {
+public:
+    explicit Launches(void *stream) : st_(static_cast<hipStream_t>(stream)) {}
+    template <typename A>
+    void add(hipError_t (*launch)(const Op &, hipStream_t), const A &a)
+    {
+        if (err_ == hipSuccess)
+            err_ = emit_op(Op::make(launch, a), st_);
+    }
+    rr_status finish() const { return err_ == hipSuccess ? set_ok() : op_failed(err_); }
+
+private:
+    hipStream_t st_;
+    hipError_t err_ = hipSuccess;
+};
+
+Product logits_product(const rr_vocab *v, int dtype, int64_t rows, const void *x, const void *w)
+{
+    return Product{w, x, v->dim, v->dim, int32_t(v->vocab), int32_t(rows), v->dim, dtype == RR_BF16};
+}
+
+// Parts of a workspace, one after the other at 256-byte boundaries.
+class Carver {
+public:
+    explicit Carver(void *base) : base_(static_cast<char *>(base)) {}
+    void *take(int64_t bytes)
+    {
+        void *p = base_ + used_;
+        used_ += round_up(bytes, 256);
+        return p;
+    }
+    int64_t used() const { return used_; }
+
+private:
+    char *base_;
+    int64_t used_ = 0;
+};
+
+// The workspace of rr_vocab_grad.  dz is held for one piece of the vocabulary
+// at a time, in both layouts.
+struct GradSpace {
+    int64_t piece, ldr, ldv;
+    int32_t splits;
+    float2 *row;
+    char *xt, *wt, *dz, *dzt;
+    float *acc;
+    int64_t bytes;
+};
+
+// Bytes of one piece of dz in one layout.
+constexpr int64_t kPieceBytes = int64_t(1) << 28;
+
+GradSpace grad_space(const rr_vocab *v, int dtype, int64_t rows, void *base)
+{
+    const int64_t es = elem_size(dtype);
+    GradSpace s{};
+    s.ldr = round_up(std::max<int64_t>(rows, 1), 64);
+    const int64_t most = std::max<int64_t>(kPieceBytes / (s.ldr * es) / 256 * 256, 256);
+    const int64_t pieces = (v->vocab + most - 1) / most;
+    s.piece = pieces ? std::min(round_up((v->vocab + pieces - 1) / pieces, 256), v->vocab) : 0;
+    s.ldv = round_up(s.piece, 64);
+    s.splits = 1;
+    Carver c(base);
+    s.row = static_cast<float2 *>(c.take(rows * 8));
+    s.xt = static_cast<char *>(c.take(v->dim * s.ldr * es));
+    s.wt = static_cast<char *>(c.take(v->dim * s.ldv * es));
+    s.dz = static_cast<char *>(c.take(rows * s.ldv * es));
+    s.dzt = static_cast<char *>(c.take(s.piece * s.ldr * es));
+    s.acc = static_cast<float *>(c.take(s.splits * rows * v->dim * 4));
+    s.bytes = c.used();
+    return s;
+}
+
+int64_t stats_bytes(const rr_vocab *v, int dtype, int64_t rows)
+{
+    const Product p = logits_product(v, dtype, rows, nullptr, nullptr);
+    const int64_t tile = stats_tile(p);
+    return round_up((v->vocab + tile - 1) / tile * rows * 8, 256);
+}
+
+rr_status check_workspace(int64_t have, int64_t need)
+{
+    if (have < need)
+        return set_error(RR_EINVAL, "workspace of %lld bytes, needs %lld", (long long)have, (long long)need);
+    return RR_OK;
+}
+
+rr_status check_router(const rr_router *r)
+{
+    if (!r)
+        return set_error(RR_EINVAL, "router descriptor is null");
+    if (r->experts < 1 || r->experts > RR_MAX_EXPERTS)
+        return set_error(RR_EINVAL, "experts=%d outside [1, RR_MAX_EXPERTS]", r->experts);
+    if (r->topk < 1 || r->topk > std::min(r->experts, RR_MAX_ROUTE_TOPK))
+        return set_error(RR_EINVAL, "topk=%d outside [1, min(experts, RR_MAX_ROUTE_TOPK)]", r->topk);
+    return RR_OK;
+}
+
+int64_t route_bytes(const rr_router *r, int64_t rows)
+{
+    const int32_t blocks = route_blocks(rows, r->experts);
+    return blocks > 1 ? round_up(int64_t(blocks) * (r->experts + 1) * 4, 256) + int64_t(blocks) * r->experts * 4 : 0;
+}
+
+// The arguments both combining calls share.
+rr_status check_combine(const rr_vocab *v, int64_t rows, const int64_t *index, const float *const *stats,
+                        const float *const *picked, int nShards, Buffers &b)
+{
+    rr_status st = check_vocab(v);
+    if (st == RR_OK)
+        st = check_rows(rows);
+    if (st != RR_OK)
+        return st;
+    if (nShards < 1 || nShards > RR_MAX_SHARDS)
+        return set_error(RR_EINVAL, "nShards=%d outside [1, RR_MAX_SHARDS]", nShards);
+    if (!stats || !picked)
+        return set_error(RR_EINVAL, "an array of shard pointers is null");
+    b.in(index, rows * v->topk * 8, 8, "index");
+    for (int i = 0; i < nShards; ++i)
+        b.in(stats[i], rows * 8, 8, "stats").in(picked[i], rows * v->topk * 4, 4, "picked");
+    return RR_OK;
+}
+
+CombineArgs combine_args(const rr_vocab *v, int64_t rows, const int64_t *index, const float *const *stats,
+                         const float *const *picked, int nShards, float *lse, float *logit, float *loss)
+{
+    CombineArgs a{};
+    for (int i = 0; i < nShards; ++i) {
+        a.stats[i] = reinterpret_cast<const float2 *>(stats[i]);
+        a.picked[i] = picked[i];
+    }
+    a.shards = nShards;
+    a.rows = int32_t(rows);
+    a.topk = v->topk;
+    a.total = v->total;
+    a.scale = v->scale;
+    a.index = index;
+    a.lse = lse;
+    a.logit = logit;
+    a.loss = loss;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t rr_vocab_workspace(const rr_vocab *v, int dtype, int64_t rows, int grad)
+{
+    if (check_vocab(v) != RR_OK || check_dtype(dtype) != RR_OK || check_rows(rows) != RR_OK)
+        return -1;
+    set_ok();
+    const int64_t n = stats_bytes(v, dtype, rows);
+    return grad ? std::max(n, grad_space(v, dtype, rows, nullptr).bytes) : n;
+}
+
+rr_status rr_vocab_stats(const rr_vocab *v, int dtype, int64_t rows, const void *x, const void *w,
+                         const int64_t *index, float *stats, float *picked, void *workspace,
+                         int64_t workspace_bytes, void *stream)
+{
+    rr_status st = check_vocab(v);
+    if (st == RR_OK)
+        st = check_dtype(dtype);
+    if (st == RR_OK)
+        st = check_rows(rows);
+    if (st != RR_OK)
+        return st;
+    const int64_t es = elem_size(dtype), need = stats_bytes(v, dtype, rows);
+    if ((st = check_workspace(workspace_bytes, need)) != RR_OK)
+        return st;
+    Buffers b;
+    b.in(x, rows * v->dim * es, es, "x").in(w, v->vocab * v->dim * es, es, "w");
+    b.in(index, rows * v->topk * 8, 8, "index");
+    b.out(stats, rows * 8, 8, "stats").out(picked, rows * v->topk * 4, 4, "picked");
+    b.out(workspace, need, 256, "workspace");
+    if ((st = b.check()) != RR_OK)
+        return st;
+    if (rows == 0)
+        return set_ok();
+
+    Launches l(stream);
+    StatsArgs a{};
+    a.p = logits_product(v, dtype, rows, x, w);
+    a.scale = v->scale;
+    a.topk = v->topk;
+    a.first = v->first;
+    a.total = v->total;
+    a.index = index;
+    a.part = static_cast<float2 *>(workspace);
+    a.picked = picked;
+    if (v->vocab > 0)
+        l.add(launch_stats, a);
+    const int32_t tile = stats_tile(a.p);
+    l.add(launch_stats_done, StatsDoneArgs{a.part, int32_t((v->vocab + tile - 1) / tile), int32_t(rows), v->topk,
+                                           v->first, v->vocab, index, reinterpret_cast<float2 *>(stats), picked});
+    return l.finish();
+}
+
+rr_status rr_vocab_cross_entropy(const rr_vocab *v, int64_t rows, const int64_t *index,
+                                 const float *const *stats, const float *const *picked, int nShards,
+                                 float *lse, float *logit, float *loss, void *stream)
+{
+    Buffers b;
+    rr_status st = check_combine(v, rows, index, stats, picked, nShards, b);
+    if (st != RR_OK)
+        return st;
+    if (v->topk != 1)
+        return set_error(RR_EINVAL, "topk=%d: cross entropy has one target per row", v->topk);
+    b.out(lse, rows * 4, 4, "lse").out(logit, rows * 4, 4, "logit").out(loss, rows * 4, 4, "loss");
+    if ((st = b.check()) != RR_OK)
+        return st;
+    if (rows == 0)
+        return set_ok();
+    Launches l(stream);
+    l.add(launch_cross_entropy, combine_args(v, rows, index, stats, picked, nShards, lse, logit, loss));
+    return l.finish();
+}
+
+rr_status rr_vocab_distill(const rr_vocab *v, int dtype, int64_t rows, const int64_t *index,
+                           const void *teacher, const float *const *stats, const float *const *picked,
+                           int nShards, float *lse, float *logit, float *prob, float *loss, void *stream)
+{
+    rr_status st = check_dtype(dtype);
+    if (st != RR_OK)
+        return st;
+    Buffers b;
+    if ((st = check_combine(v, rows, index, stats, picked, nShards, b)) != RR_OK)
+        return st;
+    const int64_t es = elem_size(dtype), n = rows * v->topk;
+    b.in(teacher, n * es, es, "teacher");
+    b.out(lse, rows * 4, 4, "lse").out(logit, n * 4, 4, "logit").out(prob, n * 4, 4, "prob");
+    b.out(loss, rows * 4, 4, "loss");
+    if ((st = b.check()) != RR_OK)
+        return st;
+    if (rows == 0)
+        return set_ok();
+    CombineArgs a = combine_args(v, rows, index, stats, picked, nShards, lse, logit, loss);
+    a.teacher = teacher;
+    a.prob = prob;
+    a.bf16 = dtype == RR_BF16;
+    Launches l(stream);
+    l.add(launch_distill, a);
+    return l.finish();
+}
+
+rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *x, const void *w,
+                        const int64_t *index, const float *lse, const float *logit, const float *prob,
+                        const float *grad, void *dx, void *dw, void *workspace, int64_t workspace_bytes,
+                        void *stream)
+{
+    rr_status st = check_vocab(v);
+    if (st == RR_OK)
+        st = check_dtype(dtype);
+    if (st == RR_OK)
+        st = check_rows(rows);
+    if (st != RR_OK)
+        return st;
+    if (!prob && v->topk != 1)
+        return set_error(RR_EINVAL, "topk=%d: cross entropy (prob is null) has one target per row", v->topk);
+    const int64_t es = elem_size(dtype), wbytes = v->vocab * v->dim * es, xbytes = rows * v->dim * es;
+    const GradSpace s = grad_space(v, dtype, rows, workspace);
+    if ((st = check_workspace(workspace_bytes, s.bytes)) != RR_OK)
+        return st;
+    Buffers b;
+    b.in(x, xbytes, es, "x").in(w, wbytes, es, "w").in(index, rows * v->topk * 8, 8, "index");
+    b.in(lse, rows * 4, 4, "lse").in(logit, rows * v->topk * 4, 4, "logit").in(grad, rows * 4, 4, "grad");
+    if (prob)
+        b.in(prob, rows * v->topk * 4, 4, "prob");
+    b.out(dx, xbytes, es, "dx").out(dw, wbytes, es, "dw").out(workspace, s.bytes, 256, "workspace");
+    if ((st = b.check()) != RR_OK)
+        return st;
+
+    const int32_t bf16 = dtype == RR_BF16, dim = v->dim, n = int32_t(rows);
+    Launches l(stream);
+    if (rows == 0) {
+        // no row contributes: dw is zero
+        if (v->vocab > 0)
+            l.add(launch_gather, GatherArgs{nullptr, dw, v->vocab * dim, 0, bf16});
+        return l.finish();
+    }
+    if (v->vocab > 0) {
+        l.add(launch_rows, RowsArgs{index, lse, prob, grad, n, v->topk, v->total, v->scale, s.row});
+        l.add(launch_transpose, TransposeArgs{x, s.xt, dim, s.ldr, n, dim, bf16});
+    }
+    for (int64_t v0 = 0; v0 < v->vocab; v0 += s.piece) {
+        const int32_t c = int32_t(std::min(s.piece, v->vocab - v0));
+        const char *wp = static_cast<const char *>(w) + v0 * dim * es;
+        char *dwp = static_cast<char *>(dw) + v0 * dim * es;
+        l.add(launch_dz, DzArgs{Product{wp, x, dim, dim, c, n, dim, bf16}, v->scale, s.row, s.dz, s.dzt, s.ldv, s.ldr});
+        l.add(launch_targets, TargetArgs{index, logit, prob, s.row, n, v->topk, c, bf16, v->first + v0,
+                                         s.dz, s.dzt, s.ldv, s.ldr});
+        l.add(launch_transpose, TransposeArgs{wp, s.wt, dim, s.ldv, c, dim, bf16});
+        l.add(launch_store, StoreArgs{Product{s.xt, s.dzt, s.ldr, s.ldr, dim, c, n, bf16}, dwp, dim, nullptr, 1, 0});
+        l.add(launch_store, StoreArgs{Product{s.wt, s.dz, s.ldv, s.ldv, dim, n, c, bf16}, nullptr, 0, s.acc,
+                                      s.splits, v0 > 0});
+    }
+    l.add(launch_gather, GatherArgs{s.acc, dx, rows * dim, v->vocab > 0 ? s.splits : 0, bf16});
+    return l.finish();
+}
+
+int64_t rr_route_workspace(const rr_router *r, int64_t rows)
+{
+    if (check_router(r) != RR_OK || check_rows(rows) != RR_OK)
+        return -1;
+    set_ok();
+    return route_bytes(r, rows);
+}
+
+rr_status rr_route(const rr_router *r, int dtype, int64_t rows, const void *logits, const uint8_t *keep,
+                   int32_t *choice, float *weight, float *lse, int32_t *counts, float *prob_sum,
+                   void *workspace, int64_t workspace_bytes, void *stream)
+{
+    rr_status st = check_router(r);
+    if (st == RR_OK)
+        st = check_dtype(dtype);
+    if (st == RR_OK)
+        st = check_rows(rows);
+    if (st != RR_OK)
+        return st;
+    const int64_t es = elem_size(dtype), need = route_bytes(r, rows), e = r->experts;
+    if ((st = check_workspace(workspace_bytes, need)) != RR_OK)
+        return st;
+    Buffers b;
+    b.in(logits, rows * e * es, es, "logits");
+    if (keep)
+        b.in(keep, rows, 1, "keep");
+    b.out(choice, rows * r->topk * 4, 4, "choice").out(weight, rows * r->topk * 4, 4, "weight");
+    b.out(lse, rows * 4, 4, "lse").out(counts, (e + 1) * 4, 4, "counts").out(prob_sum, e * 4, 4, "prob_sum");
+    b.out(workspace, need, 256, "workspace");
+    if ((st = b.check()) != RR_OK)
+        return st;
+    const int32_t blocks = route_blocks(rows, r->experts);
+    RouteArgs a{logits, keep, choice, weight, lse, counts, prob_sum, rows,
+                r->experts, r->topk, r->renormalize ? 1 : 0, dtype == RR_BF16, blocks};
+    Launches l(stream);
+    if (blocks <= 1) {
+        l.add(launch_route, a);
+        return l.finish();
+    }
+    a.counts = static_cast<int32_t *>(workspace);
+    a.prob_sum = reinterpret_cast<float *>(static_cast<char *>(workspace) + round_up(int64_t(blocks) * (e + 1) * 4, 256));
+    l.add(launch_route, a);
+    l.add(launch_route_sum, RouteSumArgs{a.counts, a.prob_sum, counts, prob_sum, blocks, r->experts});
+    return l.finish();
+}
+
+rr_status rr_balance_loss(const rr_router *r, const int32_t *const *counts, const float *const *prob_sum,
+                          int nRanks, float *loss, float *slope, void *stream)
+{
+    rr_status st = check_router(r);
+    if (st != RR_OK)
+        return st;
+    if (nRanks < 1 || nRanks > RR_MAX_SHARDS)
+        return set_error(RR_EINVAL, "nRanks=%d outside [1, RR_MAX_SHARDS]", nRanks);
+    if (!counts || !prob_sum)
+        return set_error(RR_EINVAL, "an array of rank pointers is null");
+    const int64_t e = r->experts;
+    Buffers b;
+    BalanceArgs a{};
+    for (int i = 0; i < nRanks; ++i) {
+        b.in(counts[i], (e + 1) * 4, 4, "counts").in(prob_sum[i], e * 4, 4, "prob_sum");
+        a.counts[i] = counts[i];
+        a.prob_sum[i] = prob_sum[i];
+    }
+    b.out(loss, 4, 4, "loss").out(slope, e * 4, 4, "slope");
+    if ((st = b.check()) != RR_OK)
+        return st;
+    a.ranks = nRanks;
+    a.experts = r->experts;
+    a.topk = r->topk;
+    a.loss = loss;
+    a.slope = slope;
+    Launches l(stream);
+    l.add(launch_balance, a);
+    return l.finish();
+}
+
+rr_status rr_route_grad(const rr_router *r, int dtype, int64_t rows, const void *logits, const uint8_t *keep,
+                        const int32_t *choice, const float *weight, const float *lse, const float *slope,
+                        const float *grad_loss, const float *grad_weight, void *dlogits, void *stream)
+{
+    rr_status st = check_router(r);
+    if (st == RR_OK)
+        st = check_dtype(dtype);
+    if (st == RR_OK)
+        st = check_rows(rows);
+    if (st != RR_OK)
+        return st;
+    const int64_t es = elem_size(dtype), e = r->experts, n = rows * r->topk;
+    Buffers b;
+    b.in(logits, rows * e * es, es, "logits");
+    if (keep)
+        b.in(keep, rows, 1, "keep");
+    b.in(choice, n * 4, 4, "choice").in(weight, n * 4, 4, "weight").in(lse, rows * 4, 4, "lse");
+    b.in(slope, e * 4, 4, "slope").in(grad_loss, 4, 4, "grad_loss").in(grad_weight, n * 4, 4, "grad_weight");
+    b.out(dlogits, rows * e * es, es, "dlogits");
+    if ((st = b.check()) != RR_OK)
+        return st;
+    if (rows == 0)
+        return set_ok();
+    Launches l(stream);
+    l.add(launch_route_grad, RouteGradArgs{logits, keep, choice, weight, lse, slope, grad_loss, grad_weight, dlogits,
+                                           rows, r->experts, r->topk, r->renormalize ? 1 : 0, dtype == RR_BF16});
+    return l.finish();
+}
+
+}  // extern "C"

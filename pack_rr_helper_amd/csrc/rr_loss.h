@@ -1,0 +1,206 @@
+// rr_loss.h -- what the host layer of the sharded losses (rr_loss.cpp) shares
+// with their kernels (rr_vocab.hip, rr_route.hip) and with the plans of
+// rr_api.cpp.  Not part of the public ABI.
+#pragma once
+
+#include <stdint.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include <hip/hip_runtime.h>
+
+#include "rr.h"
+
+namespace rr {
+
+// One launch of a loss operator: the function that enqueues it and its
+// arguments by value.  A plan records it as it is.
+struct Op {
+    hipError_t (*launch)(const Op &, hipStream_t);
+    alignas(16) char args[496];
+
+    template <typename A>
+    static Op make(hipError_t (*launch)(const Op &, hipStream_t), const A &a)
+    {
+        static_assert(sizeof(A) <= sizeof(Op::args) && std::is_trivially_copyable<A>::value, "");
+        Op op{};
+        op.launch = launch;
+        memcpy(op.args, &a, sizeof a);
+        return op;
+    }
+    template <typename A>
+    A get() const
+    {
+        A a;
+        memcpy(&a, args, sizeof a);
+        return a;
+    }
+};
+
+// In rr_api.cpp: enqueue an op, or append it to the plan that this thread
+// records; the error state of the calling thread.
+hipError_t emit_op(const Op &op, hipStream_t stream);
+rr_status op_failed(hipError_t e);
+rr_status set_error(rr_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+rr_status set_ok();
+
+// ---------------------------------------------------------------------------
+// Vocabulary head.  Every product is C[j][i] = sum_k A[i][k] * B[j][k], both
+// operands with contiguous k: "i" (the fast axis of C) runs over the
+// vocabulary for the logits and over dim for dw and dx.
+// ---------------------------------------------------------------------------
+
+struct Product {
+    const void *a, *b;   // [ni][lda], [nj][ldb]
+    int64_t lda, ldb;    // elements
+    int32_t ni, nj, nk;
+    int32_t bf16;        // element type of a and b
+};
+
+// The logits' softmax statistics per tile of the vocabulary, and the picked ones.
+struct StatsArgs {
+    Product p;           // a = w, b = x
+    float scale;
+    int32_t topk;
+    int64_t first, total;
+    const int64_t *index;
+    float2 *part;        // [tiles of i][nj]
+    float *picked;
+};
+// Vocabulary entries of one partial statistic.
+int32_t stats_tile(const Product &p);
+hipError_t launch_stats(const Op &, hipStream_t);
+
+// stats[row] from its partials; picked entries of other shards to zero.
+struct StatsDoneArgs {
+    const float2 *part;
+    int32_t tiles, rows, topk;
+    int64_t first, vocab;
+    const int64_t *index;
+    float2 *stats;
+    float *picked;
+};
+hipError_t launch_stats_done(const Op &, hipStream_t);
+
+struct CombineArgs {
+    const float2 *stats[RR_MAX_SHARDS];
+    const float *picked[RR_MAX_SHARDS];
+    int32_t shards, rows, topk, bf16;
+    int64_t total;
+    float scale;
+    const int64_t *index;
+    const void *teacher;
+    float *lse, *logit, *prob, *loss;
+};
+hipError_t launch_cross_entropy(const Op &, hipStream_t);
+hipError_t launch_distill(const Op &, hipStream_t);
+
+// Per row: lse and grad * scale, or zeros for a row without a target.
+struct RowsArgs {
+    const int64_t *index;
+    const float *lse, *prob, *grad;
+    int32_t rows, topk;
+    int64_t total;
+    float scale;
+    float2 *row;         // (lse, coefficient)
+};
+hipError_t launch_rows(const Op &, hipStream_t);
+
+// dz of one piece of the vocabulary without its targets, in both layouts.
+struct DzArgs {
+    Product p;           // a = the piece of w, b = x
+    float scale;
+    const float2 *row;
+    void *dz, *dzt;      // [nj][ldz], [ni][ldt]
+    int64_t ldz, ldt;
+};
+hipError_t launch_dz(const Op &, hipStream_t);
+
+// dz at the targets of one piece.
+struct TargetArgs {
+    const int64_t *index;
+    const float *logit, *prob;
+    const float2 *row;
+    int32_t rows, topk, count, bf16;  // entries [first, first + count) of the vocabulary
+    int64_t first;
+    void *dz, *dzt;
+    int64_t ldz, ldt;
+};
+hipError_t launch_targets(const Op &, hipStream_t);
+
+// out[c][r] = in[r][c] for r < rows, c < cols; out rows end in zeros up to
+// the next multiple of 64 of rows.
+struct TransposeArgs {
+    const void *in;
+    void *out;
+    int64_t ldi, ldo;
+    int32_t rows, cols, bf16;
+};
+hipError_t launch_transpose(const Op &, hipStream_t);
+
+// A product stored as the element type, or into partial sums in fp32.
+struct StoreArgs {
+    Product p;
+    void *out;           // [nj][ldo]
+    int64_t ldo;
+    float *acc;          // not null: [splits][nj][ni] instead of out
+    int32_t splits, add; // add: to what acc holds
+};
+hipError_t launch_store(const Op &, hipStream_t);
+
+// out = the sum of the partial sums (none: zero).
+struct GatherArgs {
+    const float *acc;
+    void *out;
+    int64_t n;
+    int32_t splits, bf16;
+};
+hipError_t launch_gather(const Op &, hipStream_t);
+
+// ---------------------------------------------------------------------------
+// Router
+// ---------------------------------------------------------------------------
+
+struct RouteArgs {
+    const void *logits;
+    const uint8_t *keep;
+    int32_t *choice;
+    float *weight, *lse;
+    int32_t *counts;     // of one workgroup: the results; else [blocks][experts + 1]
+    float *prob_sum;     //                             else [blocks][experts]
+    int64_t rows;
+    int32_t experts, topk, renormalize, bf16, blocks;
+};
+int32_t route_blocks(int64_t rows, int32_t experts);
+hipError_t launch_route(const Op &, hipStream_t);
+
+struct RouteSumArgs {
+    const int32_t *part_counts;
+    const float *part_sum;
+    int32_t *counts;
+    float *prob_sum;
+    int32_t blocks, experts;
+};
+hipError_t launch_route_sum(const Op &, hipStream_t);
+
+struct BalanceArgs {
+    const int32_t *counts[RR_MAX_SHARDS];
+    const float *prob_sum[RR_MAX_SHARDS];
+    int32_t ranks, experts, topk;
+    float *loss, *slope;
+};
+hipError_t launch_balance(const Op &, hipStream_t);
+
+struct RouteGradArgs {
+    const void *logits;
+    const uint8_t *keep;
+    const int32_t *choice;
+    const float *weight, *lse, *slope, *grad_loss, *grad_weight;
+    void *dlogits;
+    int64_t rows;
+    int32_t experts, topk, renormalize, bf16;
+};
+hipError_t launch_route_grad(const Op &, hipStream_t);
+
+}  // namespace rr
