@@ -404,7 +404,8 @@ rr_status rr_plan_launch(const void *plan, void *stream);
  * entries: logits z = scale * (x . w) with x [rows][dim] and w [vocab][dim].
  * topk index entries belong to every row (1 for cross entropy). */
 typedef struct {
-    int64_t vocab, first, total;  /* 0 <= first, 0 <= vocab, first + vocab <= total < 2^31, total >= 1 */
+    int64_t vocab, first, total;  /* 0 <= first, 0 <= vocab <= RR_MAX_VOCAB, first + vocab <= total < 2^31,
+                                     total >= 1; vocab * dim and rows * vocab <= RR_MAX_PLANE */
     int32_t dim;                  /* 1 .. RR_MAX_DIM */
     int32_t topk;                 /* 1 .. RR_MAX_TOPK */
     float scale;                  /* finite; 1, or one over the temperature */
@@ -412,9 +413,11 @@ typedef struct {
 } rr_vocab;
 
 #define RR_MAX_DIM 65536
+#define RR_MAX_VOCAB (INT64_C(1) << 24)
+#define RR_MAX_PLANE (INT64_C(1) << 36)
 #define RR_MAX_TOPK 1024
 #define RR_MAX_SHARDS 16
-#define RR_MAX_ROWS (INT64_C(1) << 30)
+#define RR_MAX_ROWS (INT64_C(1) << 20)   /* of a head */
 
 /*
  * rr_vocab_workspace -- bytes of workspace that rr_vocab_stats (grad == 0) or
@@ -488,6 +491,7 @@ typedef struct {
 
 #define RR_MAX_EXPERTS 1024
 #define RR_MAX_ROUTE_TOPK 32
+#define RR_MAX_ROUTE_ROWS (INT64_C(1) << 30)
 
 /* rr_route_workspace -- bytes of workspace for rr_route (may be 0); -1 for
  * arguments that it rejects. */

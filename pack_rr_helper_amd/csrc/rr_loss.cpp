@@ -21,14 +21,14 @@ rr_status check_dtype(int dtype)
     return RR_OK;
 }
 
-rr_status check_rows(int64_t rows)
+rr_status check_tokens(int64_t rows)
 {
-    if (rows < 0 || rows > RR_MAX_ROWS)
-        return set_error(RR_EINVAL, "rows=%lld outside [0, RR_MAX_ROWS]", (long long)rows);
+    if (rows < 0 || rows > RR_MAX_ROUTE_ROWS)
+        return set_error(RR_EINVAL, "rows=%lld outside [0, RR_MAX_ROUTE_ROWS]", (long long)rows);
     return RR_OK;
 }
 
-rr_status check_vocab(const rr_vocab *v)
+rr_status check_vocab(const rr_vocab *v, int64_t rows)
 {
     if (!v)
         return set_error(RR_EINVAL, "vocabulary descriptor is null");
@@ -37,12 +37,19 @@ rr_status check_vocab(const rr_vocab *v)
     if (v->vocab < 0 || v->first < 0 || v->first > v->total || v->vocab > v->total - v->first)
         return set_error(RR_EINVAL, "shard [first=%lld, + vocab=%lld) outside [0, total=%lld)",
                          (long long)v->first, (long long)v->vocab, (long long)v->total);
+    if (v->vocab > RR_MAX_VOCAB)
+        return set_error(RR_EINVAL, "vocab=%lld above RR_MAX_VOCAB", (long long)v->vocab);
     if (v->dim < 1 || v->dim > RR_MAX_DIM)
         return set_error(RR_EINVAL, "dim=%d outside [1, RR_MAX_DIM]", v->dim);
     if (v->topk < 1 || v->topk > RR_MAX_TOPK)
         return set_error(RR_EINVAL, "topk=%d outside [1, RR_MAX_TOPK]", v->topk);
     if (!isfinite(v->scale))
         return set_error(RR_EINVAL, "scale is not finite");
+    if (rows < 0 || rows > RR_MAX_ROWS)
+        return set_error(RR_EINVAL, "rows=%lld outside [0, RR_MAX_ROWS]", (long long)rows);
+    if (v->vocab * v->dim > RR_MAX_PLANE || rows * v->vocab > RR_MAX_PLANE)
+        return set_error(RR_EINVAL, "rows=%lld, vocab=%lld, dim=%d: vocab * dim or rows * vocab above RR_MAX_PLANE",
+                         (long long)rows, (long long)v->vocab, v->dim);
     return RR_OK;
 }
 
@@ -130,7 +137,7 @@ private:
 // The workspace of rr_vocab_grad.  dz is held for one piece of the vocabulary
 // at a time, in both layouts.
 struct GradSpace {
-    int64_t piece, ldr, ldv;
+    int64_t piece, ldr, ldv, lda;
     int32_t splits;
     float2 *row;
     char *xt, *wt, *dz, *dzt;
@@ -150,23 +157,24 @@ GradSpace grad_space(const rr_vocab *v, int dtype, int64_t rows, void *base)
     const int64_t pieces = (v->vocab + most - 1) / most;
     s.piece = pieces ? std::min(round_up((v->vocab + pieces - 1) / pieces, 256), v->vocab) : 0;
     s.ldv = round_up(s.piece, 64);
-    s.splits = 1;
+    s.lda = round_up(v->dim, 4);
+    // one number of parts for every piece, as the sums go on from piece to piece
+    s.splits = product_splits(Product{nullptr, nullptr, s.ldv, s.ldv, v->dim, int32_t(rows), int32_t(s.piece),
+                                      dtype == RR_BF16});
     Carver c(base);
     s.row = static_cast<float2 *>(c.take(rows * 8));
     s.xt = static_cast<char *>(c.take(v->dim * s.ldr * es));
     s.wt = static_cast<char *>(c.take(v->dim * s.ldv * es));
     s.dz = static_cast<char *>(c.take(rows * s.ldv * es));
     s.dzt = static_cast<char *>(c.take(s.piece * s.ldr * es));
-    s.acc = static_cast<float *>(c.take(s.splits * rows * v->dim * 4));
+    s.acc = static_cast<float *>(c.take(s.splits * rows * s.lda * 4));
     s.bytes = c.used();
     return s;
 }
 
 int64_t stats_bytes(const rr_vocab *v, int dtype, int64_t rows)
 {
-    const Product p = logits_product(v, dtype, rows, nullptr, nullptr);
-    const int64_t tile = stats_tile(p);
-    return round_up((v->vocab + tile - 1) / tile * rows * 8, 256);
+    return round_up(stats_parts(logits_product(v, dtype, rows, nullptr, nullptr)) * rows * 8, 256);
 }
 
 rr_status check_workspace(int64_t have, int64_t need)
@@ -197,9 +205,7 @@ int64_t route_bytes(const rr_router *r, int64_t rows)
 rr_status check_combine(const rr_vocab *v, int64_t rows, const int64_t *index, const float *const *stats,
                         const float *const *picked, int nShards, Buffers &b)
 {
-    rr_status st = check_vocab(v);
-    if (st == RR_OK)
-        st = check_rows(rows);
+    const rr_status st = check_vocab(v, rows);
     if (st != RR_OK)
         return st;
     if (nShards < 1 || nShards > RR_MAX_SHARDS)
@@ -238,7 +244,7 @@ extern "C" {
 
 int64_t rr_vocab_workspace(const rr_vocab *v, int dtype, int64_t rows, int grad)
 {
-    if (check_vocab(v) != RR_OK || check_dtype(dtype) != RR_OK || check_rows(rows) != RR_OK)
+    if (check_vocab(v, rows) != RR_OK || check_dtype(dtype) != RR_OK)
         return -1;
     set_ok();
     const int64_t n = stats_bytes(v, dtype, rows);
@@ -249,11 +255,9 @@ rr_status rr_vocab_stats(const rr_vocab *v, int dtype, int64_t rows, const void 
                          const int64_t *index, float *stats, float *picked, void *workspace,
                          int64_t workspace_bytes, void *stream)
 {
-    rr_status st = check_vocab(v);
+    rr_status st = check_vocab(v, rows);
     if (st == RR_OK)
         st = check_dtype(dtype);
-    if (st == RR_OK)
-        st = check_rows(rows);
     if (st != RR_OK)
         return st;
     const int64_t es = elem_size(dtype), need = stats_bytes(v, dtype, rows);
@@ -273,17 +277,12 @@ rr_status rr_vocab_stats(const rr_vocab *v, int dtype, int64_t rows, const void 
     StatsArgs a{};
     a.p = logits_product(v, dtype, rows, x, w);
     a.scale = v->scale;
-    a.topk = v->topk;
-    a.first = v->first;
-    a.total = v->total;
-    a.index = index;
     a.part = static_cast<float2 *>(workspace);
-    a.picked = picked;
     if (v->vocab > 0)
         l.add(launch_stats, a);
-    const int32_t tile = stats_tile(a.p);
-    l.add(launch_stats_done, StatsDoneArgs{a.part, int32_t((v->vocab + tile - 1) / tile), int32_t(rows), v->topk,
-                                           v->first, v->vocab, index, reinterpret_cast<float2 *>(stats), picked});
+    l.add(launch_stats_done, StatsDoneArgs{a.part, x, w, index, reinterpret_cast<float2 *>(stats), picked, v->first,
+                                           int32_t(stats_parts(a.p)), a.p.nj, v->topk, a.p.ni, v->dim, a.p.bf16,
+                                           v->scale});
     return l.finish();
 }
 
@@ -339,11 +338,9 @@ rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *
                         const float *grad, void *dx, void *dw, void *workspace, int64_t workspace_bytes,
                         void *stream)
 {
-    rr_status st = check_vocab(v);
+    rr_status st = check_vocab(v, rows);
     if (st == RR_OK)
         st = check_dtype(dtype);
-    if (st == RR_OK)
-        st = check_rows(rows);
     if (st != RR_OK)
         return st;
     if (!prob && v->topk != 1)
@@ -366,7 +363,7 @@ rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *
     if (rows == 0) {
         // no row contributes: dw is zero
         if (v->vocab > 0)
-            l.add(launch_gather, GatherArgs{nullptr, dw, v->vocab * dim, 0, bf16});
+            l.add(launch_gather, GatherArgs{nullptr, dw, v->vocab, 0, dim, 0, bf16});
         return l.finish();
     }
     if (v->vocab > 0) {
@@ -381,17 +378,17 @@ rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *
         l.add(launch_targets, TargetArgs{index, logit, prob, s.row, n, v->topk, c, bf16, v->first + v0,
                                          s.dz, s.dzt, s.ldv, s.ldr});
         l.add(launch_transpose, TransposeArgs{wp, s.wt, dim, s.ldv, c, dim, bf16});
-        l.add(launch_store, StoreArgs{Product{s.xt, s.dzt, s.ldr, s.ldr, dim, c, n, bf16}, dwp, dim, nullptr, 1, 0});
+        l.add(launch_store, StoreArgs{Product{s.xt, s.dzt, s.ldr, s.ldr, dim, c, n, bf16}, dwp, dim, nullptr, 0, 1, 0});
         l.add(launch_store, StoreArgs{Product{s.wt, s.dz, s.ldv, s.ldv, dim, n, c, bf16}, nullptr, 0, s.acc,
-                                      s.splits, v0 > 0});
+                                      s.lda, s.splits, v0 > 0});
     }
-    l.add(launch_gather, GatherArgs{s.acc, dx, rows * dim, v->vocab > 0 ? s.splits : 0, bf16});
+    l.add(launch_gather, GatherArgs{s.acc, dx, rows, s.lda, dim, v->vocab > 0 ? s.splits : 0, bf16});
     return l.finish();
 }
 
 int64_t rr_route_workspace(const rr_router *r, int64_t rows)
 {
-    if (check_router(r) != RR_OK || check_rows(rows) != RR_OK)
+    if (check_router(r) != RR_OK || check_tokens(rows) != RR_OK)
         return -1;
     set_ok();
     return route_bytes(r, rows);
@@ -405,7 +402,7 @@ rr_status rr_route(const rr_router *r, int dtype, int64_t rows, const void *logi
     if (st == RR_OK)
         st = check_dtype(dtype);
     if (st == RR_OK)
-        st = check_rows(rows);
+        st = check_tokens(rows);
     if (st != RR_OK)
         return st;
     const int64_t es = elem_size(dtype), need = route_bytes(r, rows), e = r->experts;
@@ -474,7 +471,7 @@ rr_status rr_route_grad(const rr_router *r, int dtype, int64_t rows, const void 
     if (st == RR_OK)
         st = check_dtype(dtype);
     if (st == RR_OK)
-        st = check_rows(rows);
+        st = check_tokens(rows);
     if (st != RR_OK)
         return st;
     const int64_t es = elem_size(dtype), e = r->experts, n = rows * r->topk;

@@ -58,28 +58,26 @@ struct Product {
     int32_t bf16;        // element type of a and b
 };
 
-// The logits' softmax statistics per tile of the vocabulary, and the picked ones.
+// The logits' softmax statistics per part of the vocabulary.
 struct StatsArgs {
     Product p;           // a = w, b = x
     float scale;
-    int32_t topk;
-    int64_t first, total;
-    const int64_t *index;
-    float2 *part;        // [tiles of i][nj]
-    float *picked;
+    float2 *part;        // [parts][nj]
 };
-// Vocabulary entries of one partial statistic.
-int32_t stats_tile(const Product &p);
+// Partial statistics of one row.
+int64_t stats_parts(const Product &p);
 hipError_t launch_stats(const Op &, hipStream_t);
 
-// stats[row] from its partials; picked entries of other shards to zero.
+// stats[row] from its parts, and the logits of the entries of this shard.
 struct StatsDoneArgs {
     const float2 *part;
-    int32_t tiles, rows, topk;
-    int64_t first, vocab;
+    const void *x, *w;
     const int64_t *index;
     float2 *stats;
     float *picked;
+    int64_t first;
+    int32_t parts, rows, topk, vocab, dim, bf16;
+    float scale;
 };
 hipError_t launch_stats_done(const Op &, hipStream_t);
 
@@ -96,7 +94,7 @@ struct CombineArgs {
 hipError_t launch_cross_entropy(const Op &, hipStream_t);
 hipError_t launch_distill(const Op &, hipStream_t);
 
-// Per row: lse and grad * scale, or zeros for a row without a target.
+// Per row: lse in units of ln 2 and grad * scale, or zeros for a row without a target.
 struct RowsArgs {
     const int64_t *index;
     const float *lse, *prob, *grad;
@@ -139,22 +137,25 @@ struct TransposeArgs {
 };
 hipError_t launch_transpose(const Op &, hipStream_t);
 
-// A product stored as the element type, or into partial sums in fp32.
+// A product stored as the element type, or in fp32 as one sum for each of the
+// `splits` parts of k.
 struct StoreArgs {
     Product p;
     void *out;           // [nj][ldo]
     int64_t ldo;
-    float *acc;          // not null: [splits][nj][ni] instead of out
+    float *acc;          // not null: [splits][nj][lda] instead of out
+    int64_t lda;         // a multiple of 4
     int32_t splits, add; // add: to what acc holds
 };
+int32_t product_splits(const Product &p);
 hipError_t launch_store(const Op &, hipStream_t);
 
 // out = the sum of the partial sums (none: zero).
 struct GatherArgs {
-    const float *acc;
-    void *out;
-    int64_t n;
-    int32_t splits, bf16;
+    const float *acc;    // [splits][rows][lda]
+    void *out;           // [rows][dim]
+    int64_t rows, lda;
+    int32_t dim, splits, bf16;
 };
 hipError_t launch_gather(const Op &, hipStream_t);
 

@@ -1,14 +1,18 @@
 // rr_vocab.hip -- gfx950 kernels of the sharded vocabulary head: the logits'
 // softmax statistics and their gradient, without keeping the logits.
 //
-// Simplest form: every product is computed in 64 x 64 tiles staged through
-// LDS, each thread accumulating 4 x 4 results in fp32.
-#include "rr_loss.h"
+// The four products of a training step (logits for the statistics, logits
+// again for dz, dw = dz^T x, dx = dz w) are tiles on the matrix cores
+// (rr_product.h) with different ends.  The vocabulary runs along the registers
+// of a tile, so a row's maximum and sum over the tile are taken within a lane
+// and over the four lane groups of a wave.
+#include "rr_product.h"
 
 namespace rr {
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
+constexpr int kThreads = 256;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 template <bool BF16>
 __device__ __forceinline__ float load(const void *p, int64_t i)
@@ -28,75 +32,58 @@ __device__ __forceinline__ void store(void *p, int64_t i, float v)
         static_cast<float *>(p)[i] = v;
 }
 
-// c[y][x] = sum over k of A[i0 + 4 tx + x][k] B[j0 + 4 ty + y][k].
-template <bool BF16>
-__device__ void product_tile(const Product &p, int64_t i0, int64_t j0, float (&c)[4][4])
-{
-    __shared__ float sa[kStep][kTile + 4], sb[kStep][kTile + 4];
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    for (int y = 0; y < 4; ++y)
-        for (int x = 0; x < 4; ++x)
-            c[y][x] = 0.0f;
-    for (int k0 = 0; k0 < p.nk; k0 += kStep) {
-        for (int t = threadIdx.x; t < kTile * kStep; t += kThreads) {
-            const int k = t % kStep, r = t / kStep;
-            const bool in = k0 + k < p.nk;
-            sa[k][r] = in && i0 + r < p.ni ? load<BF16>(p.a, (i0 + r) * p.lda + k0 + k) : 0.0f;
-            sb[k][r] = in && j0 + r < p.nj ? load<BF16>(p.b, (j0 + r) * p.ldb + k0 + k) : 0.0f;
-        }
-        __syncthreads();
-        for (int k = 0; k < kStep; ++k)
-            for (int y = 0; y < 4; ++y)
-                for (int x = 0; x < 4; ++x)
-                    c[y][x] = __builtin_fmaf(sa[k][4 * tx + x], sb[k][4 * ty + y], c[y][x]);
-        __syncthreads();
-    }
-}
-
 // exp(x - top) where top may be infinite: -inf - -inf counts as nothing.
 __device__ __forceinline__ float exp_below(float x, float top)
 {
     return x == -INFINITY ? 0.0f : expf(x - top);
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(kThreads) void stats_kernel(StatsArgs a)
+__device__ __forceinline__ unsigned pack_bf16(float lo, float hi)
 {
-    const int64_t i0 = int64_t(blockIdx.x) * kTile, j0 = int64_t(blockIdx.y) * kTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float c[4][4];
-    product_tile<BF16>(a.p, i0, j0, c);
-    for (int y = 0; y < 4; ++y) {
-        const int64_t j = j0 + 4 * ty + y;
-        float top = -INFINITY, sum = 0.0f;
-        bool nan = false;
-        for (int x = 0; x < 4; ++x) {
-            const int64_t i = i0 + 4 * tx + x;
-            c[y][x] *= a.scale;
-            if (i < a.p.ni) {
-                top = fmaxf(top, c[y][x]);
-                nan |= c[y][x] != c[y][x];
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+// One wave's rows of a tile: part = the logits' maximum and sum of exponentials.
+template <typename T>
+__global__ __launch_bounds__(T::kThreads) void stats_kernel(StatsArgs a, int tiles_i, int tiles_j)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[T::kLdsBytes];
+    int ti, tj;
+    tile_at(blockIdx.x, gridDim.x, tiles_i, tiles_j, ti, tj);
+    const int i0 = ti * T::TI, j0 = tj * T::TJ;
+    typename T::Acc acc;
+    T::run(a.p, i0, j0, 0, (a.p.nk + T::kStep - 1) / T::kStep, lds, acc);
+    const bool full = i0 + T::TI <= a.p.ni;
+    const int part = ti * (T::TI / (T::FI * 16)) + T::wave_i() / (T::FI * 16);
+#pragma unroll
+    for (int j = 0; j < T::FJ; ++j) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < T::FI; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float z = acc.c[i][j][e] * a.scale;
+                if (!full && i0 + T::lane_i(i) + e >= a.p.ni)
+                    z = -INFINITY;
+                acc.c[i][j][e] = z;
+                top = fmaxf(top, z);
             }
-        }
-        for (int d = 1; d < 16; d *= 2)
-            top = fmaxf(top, __shfl_xor(top, d));
-        for (int x = 0; x < 4; ++x)
-            if (i0 + 4 * tx + x < a.p.ni)
-                sum += exp_below(c[y][x], top);
-        if (nan)
-            sum = NAN;
-        for (int d = 1; d < 16; d *= 2)
-            sum += __shfl_xor(sum, d);
-        if (j >= a.p.nj)
-            continue;
-        if (tx == 0)
-            a.part[int64_t(blockIdx.x) * a.p.nj + j] = float2{top, sum};
-        for (int e = 0; e < a.topk; ++e) {
-            const int64_t i = a.index[j * a.topk + e] - a.first;
-            for (int x = 0; x < 4; ++x)
-                if (i == i0 + 4 * tx + x && i < a.p.ni)
-                    a.picked[j * a.topk + e] = c[y][x];
-        }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float base = top == -INFINITY ? 0.0f : top * -kLog2e;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < T::FI; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc.c[i][j][e], kLog2e, base));
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        const int row = j0 + T::lane_j(j);
+        if (threadIdx.x % 64 < 16 && row < a.p.nj)
+            a.part[int64_t(part) * a.p.nj + row] = float2{top, sum};
     }
 }
 
@@ -108,19 +95,68 @@ __device__ __forceinline__ float2 join(float2 a, float2 b)
     return float2{top, a.y * fa + b.y * fb};
 }
 
-__global__ __launch_bounds__(kThreads) void stats_done_kernel(StatsDoneArgs a)
+__device__ __forceinline__ float wave_max(float v)
 {
-    const int64_t j = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    if (j >= a.rows)
+    for (int d = 1; d < 64; d *= 2)
+        v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+    for (int d = 1; d < 64; d *= 2)
+        v += __shfl_xor(v, d);
+    return v;
+}
+
+// The first `joins` workgroups join the parts of `wide` rows each (a power of
+// two up to 64), the others compute the logits of one entry per wave.
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void stats_done_kernel(StatsDoneArgs a, int joins, int wide)
+{
+    __shared__ float2 sums[kThreads];
+    if (int(blockIdx.x) < joins) {
+        const int r = threadIdx.x % wide, t0 = threadIdx.x / wide, step = kThreads / wide;
+        const int64_t row = int64_t(blockIdx.x) * wide + r;
+        float2 s{-INFINITY, 0.0f};
+        if (row < a.rows)
+            for (int t = t0; t < a.parts; t += step)
+                s = join(s, a.part[int64_t(t) * a.rows + row]);
+        sums[threadIdx.x] = s;
+        for (int n = kThreads / 2; n >= wide; n /= 2) {
+            __syncthreads();
+            if (int(threadIdx.x) < n)
+                sums[threadIdx.x] = join(sums[threadIdx.x], sums[threadIdx.x + n]);
+        }
+        if (t0 == 0 && row < a.rows)
+            a.stats[row] = sums[threadIdx.x];
         return;
-    float2 s{-INFINITY, 0.0f};
-    for (int t = 0; t < a.tiles; ++t)
-        s = join(s, a.part[int64_t(t) * a.rows + j]);
-    a.stats[j] = s;
-    for (int e = 0; e < a.topk; ++e) {
-        const int64_t i = a.index[j * a.topk + e] - a.first;
-        if (i < 0 || i >= a.vocab)
-            a.picked[j * a.topk + e] = 0.0f;
+    }
+    const int lane = threadIdx.x % 64;
+    const int64_t entries = int64_t(a.rows) * a.topk, waves = int64_t(gridDim.x - joins) * (kThreads / 64);
+    for (int64_t n = (int64_t(blockIdx.x) - joins) * (kThreads / 64) + threadIdx.x / 64; n < entries; n += waves) {
+        const int64_t i = a.index[n] - a.first;
+        float z = 0.0f;
+        if (i >= 0 && i < a.vocab) {
+            constexpr int kEs = BF16 ? 2 : 4, kPer = 16 / kEs;
+            const char *x = static_cast<const char *>(a.x) + n / a.topk * a.dim * kEs;
+            const char *w = static_cast<const char *>(a.w) + i * a.dim * kEs;
+            for (int k = lane * kPer; k < a.dim; k += 64 * kPer) {
+                const u32x4 u = load_chunk<kEs>(x + k * kEs, (a.dim - k) * kEs), v = load_chunk<kEs>(w + k * kEs, (a.dim - k) * kEs);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (BF16) {
+                        z = __builtin_fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), z);
+                        z = __builtin_fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(v[e] & 0xffff0000u), z);
+                    } else {
+                        z = __builtin_fmaf(__uint_as_float(u[e]), __uint_as_float(v[e]), z);
+                    }
+                }
+            }
+            z = wave_sum(z) * a.scale;
+        }
+        if (lane == 0)
+            a.picked[n] = z;
     }
 }
 
@@ -154,20 +190,6 @@ __global__ __launch_bounds__(kThreads) void cross_entropy_kernel(CombineArgs a)
     a.lse[j] = lse;
     a.logit[j] = z;
     a.loss[j] = counts(a.index[j], a.total) ? lse - z : 0.0f;
-}
-
-__device__ __forceinline__ float wave_max(float v)
-{
-    for (int d = 1; d < 64; d *= 2)
-        v = fmaxf(v, __shfl_xor(v, d));
-    return v;
-}
-
-__device__ __forceinline__ float wave_sum(float v)
-{
-    for (int d = 1; d < 64; d *= 2)
-        v += __shfl_xor(v, d);
-    return v;
 }
 
 // One wave per row.
@@ -219,30 +241,108 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a)
     bool used = false;
     for (int e = 0; e < a.topk; ++e)
         used |= a.prob ? a.prob[j * a.topk + e] != 0.0f : counts(a.index[j * a.topk + e], a.total);
-    a.row[j] = used ? float2{a.lse[j], a.grad[j] * a.scale} : float2{0.0f, 0.0f};
+    a.row[j] = used ? float2{a.lse[j] * kLog2e, a.grad[j] * a.scale} : float2{0.0f, 0.0f};
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(kThreads) void dz_kernel(DzArgs a)
-{
-    const int64_t i0 = int64_t(blockIdx.x) * kTile, j0 = int64_t(blockIdx.y) * kTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float c[4][4];
-    product_tile<BF16>(a.p, i0, j0, c);
-    for (int y = 0; y < 4; ++y) {
-        const int64_t j = j0 + 4 * ty + y;
-        if (j >= a.p.nj)
-            continue;
-        const float2 row = a.row[j];
-        for (int x = 0; x < 4; ++x) {
-            const int64_t i = i0 + 4 * tx + x;
-            if (i >= a.p.ni)
-                continue;
-            const float d = row.y == 0.0f ? 0.0f : row.y * expf(a.scale * c[y][x] - row.x);
-            store<BF16>(a.dz, j * a.ldz + i, d);
-            store<BF16>(a.dzt, i * a.ldt + j, d);
+// A tile in the element type, [TJ][TI] with 4 bytes after each row: column
+// reads of eight rows at a time then fall on different banks.
+template <typename T>
+struct Staged {
+    static constexpr int kStride = T::TI * T::kEs + 4;
+    static constexpr int kBytes = T::TJ * kStride;
+
+    // Four results of one row of the tile.
+    __device__ static void put(char *lds, int j, int i, f32x4 v)
+    {
+        unsigned *to = reinterpret_cast<unsigned *>(lds + j * kStride + i * T::kEs);
+        if constexpr (T::kEs == 2) {
+            to[0] = pack_bf16(v[0], v[1]);
+            to[1] = pack_bf16(v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                to[e] = __float_as_uint(v[e]);
         }
     }
+
+    // Rows j < nj, results i < ni to out[j][i].
+    __device__ static void store_rows(const char *lds, char *out, int64_t stride, int nj, int ni)
+    {
+        constexpr int kChunks = T::TI * T::kEs / 16;
+        for (int t = threadIdx.x; t < T::TJ * kChunks; t += T::kThreads) {
+            const int j = t / kChunks, c = t % kChunks, left = ni * T::kEs - c * 16;
+            if (j >= nj || left <= 0)
+                continue;
+            const unsigned *from = reinterpret_cast<const unsigned *>(lds + j * kStride + c * 16);
+            store_chunk<T::kEs>(out + j * stride + c * 16, u32x4{from[0], from[1], from[2], from[3]}, left);
+        }
+    }
+
+    // Transposed: results i < ni, rows j < nj (a multiple of 16 bytes) to out[i][j].
+    __device__ static void store_columns(const char *lds, char *out, int64_t stride, int nj, int ni)
+    {
+        constexpr int kPer = 16 / T::kEs, kChunks = T::TJ / kPer, kWide = kChunks < 8 ? kChunks : 8;
+        // eight chunks of j by eight i at a time: whole 128-byte lines, all banks
+        for (int t = threadIdx.x; t < T::TI * kChunks; t += T::kThreads) {
+            const int i = t / kWide % T::TI, c = t % kWide + t / (kWide * T::TI) * kWide;
+            if (i >= ni || c * kPer >= nj)
+                continue;
+            u32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const char *from = lds + c * kPer * kStride + i * T::kEs;
+                if constexpr (T::kEs == 2)
+                    v[e] = *reinterpret_cast<const unsigned short *>(from + 2 * e * kStride) |
+                           unsigned(*reinterpret_cast<const unsigned short *>(from + (2 * e + 1) * kStride)) << 16;
+                else
+                    v[e] = *reinterpret_cast<const unsigned *>(from + e * kStride);
+            }
+            *reinterpret_cast<u32x4 *>(out + i * stride + c * 16) = v;
+        }
+    }
+};
+
+template <typename T>
+constexpr int staged_lds = T::kLdsBytes > Staged<T>::kBytes ? T::kLdsBytes : Staged<T>::kBytes;
+
+__device__ __forceinline__ int round64(int n) { return (n + 63) / 64 * 64; }
+
+// dz = coefficient * exp(z - lse), zero past the piece and past the rows up to
+// the next multiple of 64.  bf16 keeps dz at 8 bits for the products: each
+// gradient sums many of these roundings, which leaves it within its own.
+template <typename T>
+__global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, int tiles_j)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[staged_lds<T>];
+    int ti, tj;
+    tile_at(blockIdx.x, gridDim.x, tiles_i, tiles_j, ti, tj);
+    const int i0 = ti * T::TI, j0 = tj * T::TJ;
+    typename T::Acc acc;
+    T::run(a.p, i0, j0, 0, (a.p.nk + T::kStep - 1) / T::kStep, lds, acc);
+    const bool full = i0 + T::TI <= a.p.ni;
+    const float c = a.scale * kLog2e;
+#pragma unroll
+    for (int j = 0; j < T::FJ; ++j) {
+        const int row = j0 + T::lane_j(j);
+        const float2 r = row < a.p.nj ? a.row[row] : float2{0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < T::FI; ++i) {
+            f32x4 d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                d[e] = r.y * __builtin_amdgcn_exp2f(__builtin_fmaf(acc.c[i][j][e], c, -r.x));
+                if (r.y == 0.0f || (!full && i0 + T::lane_i(i) + e >= a.p.ni))
+                    d[e] = 0.0f;
+            }
+            Staged<T>::put(lds, T::lane_j(j), T::lane_i(i), d);
+        }
+    }
+    __syncthreads();
+    const int left_i = round64(a.p.ni) - i0, left_j = round64(a.p.nj) - j0;
+    Staged<T>::store_rows(lds, static_cast<char *>(a.dz) + (j0 * a.ldz + i0) * T::kEs, a.ldz * T::kEs,
+                          a.p.nj - j0 < T::TJ ? a.p.nj - j0 : T::TJ, left_i < T::TI ? left_i : T::TI);
+    Staged<T>::store_columns(lds, static_cast<char *>(a.dzt) + (i0 * a.ldt + j0) * T::kEs, a.ldt * T::kEs,
+                             left_j < T::TJ ? left_j : T::TJ, a.p.ni - i0 < T::TI ? a.p.ni - i0 : T::TI);
 }
 
 // One thread per entry.  Equal entries of a row write the same value.
@@ -263,7 +363,7 @@ __global__ __launch_bounds__(kThreads) void targets_kernel(TargetArgs a)
             if (a.index[j * a.topk + e] == at)
                 p += a.prob[j * a.topk + e];
     }
-    const float d = row.y == 0.0f ? 0.0f : row.y * (expf(a.logit[n] - row.x) - p);
+    const float d = row.y == 0.0f ? 0.0f : row.y * (__builtin_amdgcn_exp2f(__builtin_fmaf(a.logit[n], kLog2e, -row.x)) - p);
     store<BF16>(a.dz, j * a.ldz + i, d);
     store<BF16>(a.dzt, i * a.ldt + j, d);
 }
@@ -272,7 +372,9 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void transpose_kernel(TransposeArgs a)
 {
     __shared__ T tile[64][65];
-    const int64_t r0 = int64_t(blockIdx.x) * 64, c0 = int64_t(blockIdx.y) * 64;
+    const int64_t tall = (a.rows + 63) / 64, all = tall * ((a.cols + 63) / 64);
+    for (int64_t b = blockIdx.x; b < all; b += gridDim.x) {
+    const int64_t r0 = b % tall * 64, c0 = b / tall * 64;
     for (int t = threadIdx.x; t < 64 * 64; t += kThreads) {
         const int r = t / 64, c = t % 64;
         tile[r][c] = r0 + r < a.rows && c0 + c < a.cols ? static_cast<const T *>(a.in)[(r0 + r) * a.ldi + c0 + c] : T(0);
@@ -283,37 +385,56 @@ __global__ __launch_bounds__(kThreads) void transpose_kernel(TransposeArgs a)
         if (c0 + c < a.cols)
             static_cast<T *>(a.out)[(c0 + c) * a.ldo + r0 + r] = tile[r][c];
     }
+    __syncthreads();
+    }
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(kThreads) void store_kernel(StoreArgs a)
+template <typename T>
+__global__ __launch_bounds__(T::kThreads) void store_kernel(StoreArgs a, int tiles_i, int tiles_j)
 {
-    const int64_t i0 = int64_t(blockIdx.x) * kTile, j0 = int64_t(blockIdx.y) * kTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float c[4][4];
-    product_tile<BF16>(a.p, i0, j0, c);
-    for (int y = 0; y < 4; ++y)
-        for (int x = 0; x < 4; ++x) {
-            const int64_t i = i0 + 4 * tx + x, j = j0 + 4 * ty + y;
-            if (i >= a.p.ni || j >= a.p.nj)
-                continue;
-            if (a.acc) {
-                float *s = a.acc + j * a.p.ni + i;
-                *s = a.add ? *s + c[y][x] : c[y][x];
-            } else {
-                store<BF16>(a.out, j * a.ldo + i, c[y][x]);
+    __shared__ __attribute__((aligned(1024))) char lds[staged_lds<T>];
+    const int tiles = tiles_i * tiles_j, split = blockIdx.x / tiles;
+    int ti, tj;
+    tile_at(blockIdx.x - split * tiles, tiles, tiles_i, tiles_j, ti, tj);
+    const int i0 = ti * T::TI, j0 = tj * T::TJ;
+    const int steps = (a.p.nk + T::kStep - 1) / T::kStep, per = (steps + a.splits - 1) / a.splits;
+    const int s0 = split * per < steps ? split * per : steps, s1 = s0 + per < steps ? s0 + per : steps;
+    typename T::Acc acc;
+    T::run(a.p, i0, j0, s0, s1, lds, acc);
+    if (a.acc) {
+        float *out = a.acc + int64_t(split) * a.p.nj * a.lda;
+#pragma unroll
+        for (int j = 0; j < T::FJ; ++j)
+#pragma unroll
+            for (int i = 0; i < T::FI; ++i) {
+                const int row = j0 + T::lane_j(j), col = i0 + T::lane_i(i);
+                if (row >= a.p.nj || col >= a.lda)
+                    continue;
+                f32x4 *to = reinterpret_cast<f32x4 *>(out + row * a.lda + col);
+                *to = a.add ? *to + acc.c[i][j] : acc.c[i][j];
             }
-        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < T::FJ; ++j)
+#pragma unroll
+        for (int i = 0; i < T::FI; ++i)
+            Staged<T>::put(lds, T::lane_j(j), T::lane_i(i), acc.c[i][j]);
+    __syncthreads();
+    Staged<T>::store_rows(lds, static_cast<char *>(a.out) + (j0 * a.ldo + i0) * T::kEs, a.ldo * T::kEs,
+                          a.p.nj - j0 < T::TJ ? a.p.nj - j0 : T::TJ, a.p.ni - i0 < T::TI ? a.p.ni - i0 : T::TI);
 }
 
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a)
 {
-    for (int64_t n = int64_t(blockIdx.x) * kThreads + threadIdx.x; n < a.n; n += int64_t(gridDim.x) * kThreads) {
+    const int64_t n = a.rows * a.dim;
+    for (int64_t t = int64_t(blockIdx.x) * kThreads + threadIdx.x; t < n; t += int64_t(gridDim.x) * kThreads) {
+        const int64_t row = t / a.dim, at = row * a.lda + (t - row * a.dim);
         float s = 0.0f;
         for (int i = 0; i < a.splits; ++i)
-            s += a.acc[i * a.n + n];
-        store<BF16>(a.out, n, s);
+            s += a.acc[i * a.rows * a.lda + at];
+        store<BF16>(a.out, t, s);
     }
 }
 
@@ -328,21 +449,105 @@ unsigned blocks(int64_t n, int64_t per) { return unsigned((n + per - 1) / per); 
         return hipGetLastError();                                    \
     } while (0)
 
-int32_t stats_tile(const Product &) { return kTile; }
+namespace {
+
+// Tiles of a product, by its rows j (the rows of x, mostly).  Up to 64 rows
+// the vocabulary streams past them and a narrow tile wastes least; 256 x 256
+// tiles reuse an operand most, but need enough of them for the 256 compute
+// units; fp32 tiles of that size would not fit LDS when staged.
+enum Shape { kRows16, kRows32, kRows64, kMid, kBig };
+
+Shape shape_of(const Product &p)
+{
+    if (p.nj <= 16)
+        return kRows16;
+    if (p.nj <= 32)
+        return kRows32;
+    if (p.nj <= 64)
+        return kRows64;
+    const int64_t big = ((p.ni + 255) / 256) * int64_t((p.nj + 255) / 256);
+    return p.bf16 && big >= 192 ? kBig : kMid;
+}
+
+// Both operands in 16-byte chunks.
+bool direct(const Product &p)
+{
+    const int64_t es = p.bf16 ? 2 : 4;
+    return (reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.b) | uintptr_t(p.lda * es) |
+            uintptr_t(p.ldb * es) | uintptr_t(p.nk * es)) % 16 == 0;
+}
+
+template <bool BF16, bool DIRECT> using Rows16 = Tile<BF16, 128, 16, 4, 1, DIRECT ? 4 : 2, DIRECT>;
+template <bool BF16, bool DIRECT> using Rows32 = Tile<BF16, 128, 32, 4, 1, DIRECT ? 4 : 2, DIRECT>;
+template <bool BF16, bool DIRECT> using Rows64 = Tile<BF16, 128, 64, 4, 1, DIRECT ? 3 : 2, DIRECT>;
+template <bool BF16, bool DIRECT> using Mid = Tile<BF16, 128, 128, 2, 2, 2, DIRECT>;
+template <bool BF16, bool DIRECT> using Big = Tile<BF16, 256, 256, 2, 4, 2, DIRECT>;
+
+int tiles(int n, int per) { return n / per + (n % per != 0); }
+
+// f(tile type) for the product's tile.
+template <bool BF16, bool DIRECT, typename F>
+hipError_t with_shape(Shape s, F f)
+{
+    switch (s) {
+    case kRows16: return f(Rows16<BF16, DIRECT>{});
+    case kRows32: return f(Rows32<BF16, DIRECT>{});
+    case kRows64: return f(Rows64<BF16, DIRECT>{});
+    case kBig:
+        if constexpr (BF16)
+            return f(Big<BF16, DIRECT>{});
+    default: return f(Mid<BF16, DIRECT>{});
+    }
+}
+
+template <bool ALWAYS_DIRECT, typename F>
+hipError_t with_tile(const Product &p, F f)
+{
+    const Shape s = shape_of(p);
+    if (ALWAYS_DIRECT || direct(p))
+        return p.bf16 ? with_shape<true, true>(s, f) : with_shape<false, true>(s, f);
+    if constexpr (!ALWAYS_DIRECT)
+        return p.bf16 ? with_shape<true, false>(s, f) : with_shape<false, false>(s, f);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+int64_t stats_parts(const Product &p)
+{
+    switch (shape_of(p)) {
+    case kRows16: case kRows32: case kRows64: return int64_t(tiles(p.ni, 128)) * 4;
+    case kMid: return int64_t(tiles(p.ni, 128)) * 2;
+    default: return int64_t(tiles(p.ni, 256)) * 2;
+    }
+}
 
 hipError_t launch_stats(const Op &op, hipStream_t stream)
 {
     const StatsArgs a = op.get<StatsArgs>();
-    const dim3 grid(blocks(a.p.ni, kTile), blocks(a.p.nj, kTile));
-    if (a.p.bf16)
-        RR_LAUNCH(stats_kernel<true>, grid, a);
-    RR_LAUNCH(stats_kernel<false>, grid, a);
+    (void)hipGetLastError();
+    return with_tile<false>(a.p, [&](auto t) {
+        using T = decltype(t);
+        const int ti = tiles(a.p.ni, T::TI), tj = tiles(a.p.nj, T::TJ);
+        stats_kernel<T><<<dim3(unsigned(ti) * unsigned(tj)), dim3(T::kThreads), 0, stream>>>(a, ti, tj);
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_stats_done(const Op &op, hipStream_t stream)
 {
     const StatsDoneArgs a = op.get<StatsDoneArgs>();
-    RR_LAUNCH(stats_done_kernel, dim3(blocks(a.rows, kThreads)), a);
+    int wide = 1;
+    while (wide < 64 && wide < a.rows)
+        wide *= 2;
+    const unsigned joins = blocks(a.rows, wide), entries = blocks(int64_t(a.rows) * a.topk, kThreads / 64),
+                   grid = joins + (entries < 65536u ? entries : 65536u);
+    (void)hipGetLastError();
+    if (a.bf16)
+        stats_done_kernel<true><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
+    else
+        stats_done_kernel<false><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
+    return hipGetLastError();
 }
 
 hipError_t launch_cross_entropy(const Op &op, hipStream_t stream)
@@ -369,10 +574,13 @@ hipError_t launch_rows(const Op &op, hipStream_t stream)
 hipError_t launch_dz(const Op &op, hipStream_t stream)
 {
     const DzArgs a = op.get<DzArgs>();
-    const dim3 grid(blocks(a.p.ni, kTile), blocks(a.p.nj, kTile));
-    if (a.p.bf16)
-        RR_LAUNCH(dz_kernel<true>, grid, a);
-    RR_LAUNCH(dz_kernel<false>, grid, a);
+    (void)hipGetLastError();
+    return with_tile<false>(a.p, [&](auto t) {
+        using T = decltype(t);
+        const int ti = tiles(a.p.ni, T::TI), tj = tiles(a.p.nj, T::TJ);
+        dz_kernel<T><<<dim3(unsigned(ti) * unsigned(tj)), dim3(T::kThreads), 0, stream>>>(a, ti, tj);
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_targets(const Op &op, hipStream_t stream)
@@ -387,25 +595,40 @@ hipError_t launch_targets(const Op &op, hipStream_t stream)
 hipError_t launch_transpose(const Op &op, hipStream_t stream)
 {
     const TransposeArgs a = op.get<TransposeArgs>();
-    const dim3 grid(blocks(a.rows, 64), blocks(a.cols, 64));
+    const int64_t all = ((a.rows + 63) / 64) * int64_t((a.cols + 63) / 64);
+    const dim3 grid(unsigned(all < 65536 ? all : 65536));
     if (a.bf16)
         RR_LAUNCH(transpose_kernel<unsigned short>, grid, a);
     RR_LAUNCH(transpose_kernel<unsigned>, grid, a);
 }
 
+// Parts of k, so that a product of few tiles still fills the compute units.
+int32_t product_splits(const Product &p)
+{
+    const Shape s = shape_of(p);
+    const int64_t all = s == kBig ? int64_t(tiles(p.ni, 256)) * tiles(p.nj, 256)
+                                  : int64_t(tiles(p.ni, 128)) * tiles(p.nj, s == kMid ? 128 : 64);
+    const int64_t steps = tiles(p.nk, p.bf16 ? 64 : 32), fill = (s == kBig ? 256 : 512) / (all ? all : 1);
+    return int32_t(fill < 1 ? 1 : fill > steps / 4 ? (steps / 4 ? steps / 4 : 1) : fill);
+}
+
 hipError_t launch_store(const Op &op, hipStream_t stream)
 {
     const StoreArgs a = op.get<StoreArgs>();
-    const dim3 grid(blocks(a.p.ni, kTile), blocks(a.p.nj, kTile));
-    if (a.p.bf16)
-        RR_LAUNCH(store_kernel<true>, grid, a);
-    RR_LAUNCH(store_kernel<false>, grid, a);
+    (void)hipGetLastError();
+    return with_tile<true>(a.p, [&](auto t) {
+        using T = decltype(t);
+        const int ti = tiles(a.p.ni, T::TI), tj = tiles(a.p.nj, T::TJ);
+        store_kernel<T><<<dim3(unsigned(ti) * unsigned(tj) * unsigned(a.splits)), dim3(T::kThreads), 0, stream>>>(a, ti, tj);
+        return hipGetLastError();
+    });
 }
 
 hipError_t launch_gather(const Op &op, hipStream_t stream)
 {
     const GatherArgs a = op.get<GatherArgs>();
-    const dim3 grid(blocks(a.n, kThreads) < 4096u ? blocks(a.n, kThreads) : 4096u);
+    const unsigned all = blocks(a.rows * a.dim, kThreads);
+    const dim3 grid(all < 4096u ? all : 4096u);
     if (a.bf16)
         RR_LAUNCH(gather_kernel<true>, grid, a);
     RR_LAUNCH(gather_kernel<false>, grid, a);

@@ -184,13 +184,17 @@ def test_workspace_too_small(L):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_workspace_sizes(dtype):
-    for rows in (0, 1, 17, 4096, 1 << 30):
-        for v in (rr.Vocab(1, 1), rr.Vocab(64, 0, 10, 10), rr.Vocab(65536, (1 << 31) - 1), rr.Vocab(4096, 128000)):
+    for rows in (0, 1, 17, 4096, 1 << 20):
+        for v in (rr.Vocab(1, 1), rr.Vocab(64, 0, 10, 10), rr.Vocab(65536, 1 << 20), rr.Vocab(4096, 1 << 16), rr.Vocab(4096, 128000)):
+            if rows * v.vocab > 1 << 36:
+                continue
             n, g = rr.rr_vocab_workspace(v, dtype, rows), rr.rr_vocab_workspace(v, dtype, rows, grad=True)
             assert 0 <= n <= g < 1 << 62
     assert rr.rr_vocab_workspace(rr.Vocab(4096, 128000), BF16, 8192, grad=True) < 4 << 30
-    with pytest.raises(ValueError):
-        rr.rr_vocab_workspace(rr.Vocab(0, 10), dtype, 4)
+    for v, rows in ((rr.Vocab(0, 10), 4), (rr.Vocab(8, (1 << 24) + 1), 4), (rr.Vocab(65536, (1 << 20) + 1), 4),
+                    (rr.Vocab(8, (1 << 16) + 1), 1 << 20), (rr.Vocab(8, 10), (1 << 20) + 1)):
+        with pytest.raises(ValueError):
+            rr.rr_vocab_workspace(v, dtype, rows)
     with pytest.raises(ValueError):
         rr.rr_route_workspace(rr.Router(8, 9), 4)
 
