@@ -119,9 +119,18 @@ __global__ __launch_bounds__(kThreads) void stats_done_kernel(StatsDoneArgs a, i
         const int r = threadIdx.x % wide, t0 = threadIdx.x / wide, step = kThreads / wide;
         const int64_t row = int64_t(blockIdx.x) * wide + r;
         float2 s{-INFINITY, 0.0f};
-        if (row < a.rows)
-            for (int t = t0; t < a.parts; t += step)
+        if (row < a.rows) {
+            int t = t0;
+            for (; t + 3 * step < a.parts; t += 4 * step) {
+                float2 v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    v[u] = a.part[int64_t(t + u * step) * a.rows + row];
+                s = join(s, join(join(v[0], v[1]), join(v[2], v[3])));
+            }
+            for (; t < a.parts; t += step)
                 s = join(s, a.part[int64_t(t) * a.rows + row]);
+        }
         sums[threadIdx.x] = s;
         for (int n = kThreads / 2; n >= wide; n /= 2) {
             __syncthreads();
@@ -537,8 +546,9 @@ hipError_t launch_stats(const Op &op, hipStream_t stream)
 hipError_t launch_stats_done(const Op &op, hipStream_t stream)
 {
     const StatsDoneArgs a = op.get<StatsDoneArgs>();
+    // rows per workgroup: few, so that there are workgroups for all compute units
     int wide = 1;
-    while (wide < 64 && wide < a.rows)
+    while (wide < 64 && a.rows / wide > 512)
         wide *= 2;
     const unsigned joins = blocks(a.rows, wide), entries = blocks(int64_t(a.rows) * a.topk, kThreads / 64),
                    grid = joins + (entries < 65536u ? entries : 65536u);
