@@ -1,58 +1,73 @@
 // rr_route.hip -- gfx950 kernels of the router: the topk choice, the weights,
 // the experts' counts and probability sums, the balance loss and its gradient.
 //
-// A row is held by G lanes in registers, PER experts each: 16 lanes up to 256
-// experts, so that a wave works on four rows at once and every exchange stays
-// within a DPP row, a whole wave above.  The choice takes the largest key topk
-// times; a key orders as its logit does and is taken out once chosen.  Per row
-// that is about topk * (3 * PER + 12) vector instructions, which is what bounds
-// rr_route; rr_route_grad is bound by its bytes.
+// A row is held by G lanes in registers, PER experts each, so that one wave
+// works on 64 / G rows and up to 256 experts every exchange stays within a DPP
+// row.  Up to 8 choices, each lane sorts its own experts' keys and sorted lists
+// are merged across the lanes; more choices are taken one largest key at a
+// time.  rr_route is bound by these vector instructions, rr_route_grad by its
+// bytes.  Loads are unconditional, at clamped places: a load under a condition
+// is waited for where the condition ends.
 #include "rr_loss.h"
 
 namespace rr {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kRouteThreads = 512, kRouteWaves = kRouteThreads / 64;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
-// Lane exchange within rows of 16: rotation by N.
-template <int N>
-__device__ __forceinline__ unsigned rotate(unsigned v)
+template <int CTRL>
+__device__ __forceinline__ unsigned dpp(unsigned v)
 {
-    return unsigned(__builtin_amdgcn_update_dpp(0, int(v), 0x120 + N, 0xf, 0xf, false));
+    return unsigned(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, false));
+}
+
+// The value of the lane that step STEP of an exchange over G lanes pairs this
+// one with: its neighbour, the other pair, the mirror lane of 8, of 16, and
+// the lanes 16 and 32 away.
+template <int STEP>
+__device__ __forceinline__ unsigned other(unsigned v)
+{
+    if constexpr (STEP == 0)
+        return dpp<0xb1>(v);
+    else if constexpr (STEP == 1)
+        return dpp<0x4e>(v);
+    else if constexpr (STEP == 2)
+        return dpp<0x141>(v);
+    else if constexpr (STEP == 3)
+        return dpp<0x140>(v);
+    else
+        return unsigned(__shfl_xor(int(v), 1 << STEP));
+}
+template <int STEP>
+__device__ __forceinline__ float other(float v)
+{
+    return __uint_as_float(other<STEP>(__float_as_uint(v)));
+}
+template <int STEP>
+__device__ __forceinline__ double other(double v)
+{
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+    return __builtin_bit_cast(double, (unsigned long long)other<STEP>(unsigned(u >> 32)) << 32 | other<STEP>(unsigned(u)));
 }
 
 // f over the G lanes of a row, the result in every lane.  f commutes, and both
 // sides of each exchange combine the same two values, so all lanes get the
 // same bits.
-template <int G, typename F>
-__device__ __forceinline__ unsigned across(unsigned v, F f)
+template <int G, int STEP = 0, typename T, typename F>
+__device__ __forceinline__ T across(T v, F f)
 {
-    v = f(v, rotate<8>(v));
-    v = f(v, rotate<4>(v));
-    v = f(v, rotate<2>(v));
-    v = f(v, rotate<1>(v));
-    if constexpr (G == 64) {
-        v = f(v, unsigned(__shfl_xor(int(v), 16)));
-        v = f(v, unsigned(__shfl_xor(int(v), 32)));
-    }
-    return v;
+    if constexpr (1 << STEP == G)
+        return v;
+    else
+        return across<G, STEP + 1>(f(v, other<STEP>(v)), f);
 }
 
 template <int G>
 __device__ __forceinline__ float row_sum(float v)
 {
-    return __uint_as_float(across<G>(__float_as_uint(v), [](unsigned a, unsigned b) {
-        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-    }));
-}
-
-template <int G>
-__device__ __forceinline__ float row_max(float v)
-{
-    return __uint_as_float(across<G>(__float_as_uint(v), [](unsigned a, unsigned b) {
-        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-    }));
+    return across<G>(v, [](float a, float b) { return a + b; });
 }
 
 __device__ __forceinline__ float wave_sum(float v)
@@ -62,18 +77,147 @@ __device__ __forceinline__ float wave_sum(float v)
     return v;
 }
 
-// Unsigned keys in the order of the floats, NaN on top, above 0.
+// Unsigned keys above 0 in the order of the floats: a positive number's bits
+// above all others, a negative one's negated, which makes both zeros equal.
 __device__ __forceinline__ unsigned order_key(float v)
 {
-    const unsigned u = __float_as_uint(v + 0.0f);  // -0 is 0
-    return v != v ? 0xffffffffu : u ^ (unsigned(int(u) >> 31) | 0x80000000u);
+    const unsigned u = __float_as_uint(v), m = unsigned(int(u) >> 31);
+    return (u ^ (m | 0x80000000u)) - m;
 }
+// of every NaN
+constexpr unsigned kNanKey = 0xffff0000u;
 
-template <bool BF16>
 __device__ __forceinline__ float key_value(unsigned key)
 {
-    const unsigned u = key & 0x80000000u ? key ^ 0x80000000u : ~key;
-    return __uint_as_float(BF16 ? u & 0xffff0000u : u);
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : 0u - key);
+}
+
+// A logit and its expert as one number, larger for the larger logit and for
+// the lower index among equals.  bf16 leaves 16 bits of a word for the index;
+// fp32 takes a double in [1, 2), whose order is that of its bits and whose
+// minimum and maximum are single instructions.
+template <bool BF16>
+struct Key;
+
+template <>
+struct Key<true> {
+    typedef unsigned T;
+    __device__ static T make(unsigned k, int e) { return (k & 0xffff0000u) | unsigned(0xffff - e); }
+    __device__ static int expert(T k) { return 0xffff - int(k & 0xffffu); }
+    __device__ static float value(T k) { return key_value(k & 0xffff0000u); }
+    __device__ static T larger(T a, T b) { return a > b ? a : b; }
+    __device__ static T smaller(T a, T b) { return a < b ? a : b; }
+};
+
+template <>
+struct Key<false> {
+    typedef double T;
+    static_assert(RR_MAX_EXPERTS <= 1024, "the index has ten bits");
+    __device__ static T make(unsigned k, int e)
+    {
+        return __builtin_bit_cast(double, (unsigned long long)(0x3ff00000u | k >> 22) << 32 | (k << 10 | unsigned(1023 - e)));
+    }
+    __device__ static unsigned long long bits(T k) { return __builtin_bit_cast(unsigned long long, k); }
+    __device__ static int expert(T k) { return 1023 - int(bits(k) & 1023u); }
+    __device__ static float value(T k) { return key_value(unsigned(bits(k) >> 10)); }
+    __device__ static T larger(T a, T b) { return fmax(a, b); }
+    __device__ static T smaller(T a, T b) { return fmin(a, b); }
+};
+
+// Descending order of a sequence that falls and then rises, or the other way.
+template <typename K, int N>
+__device__ __forceinline__ void sort_bitonic(typename K::T *v)
+{
+    if constexpr (N > 1) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const auto a = v[i], b = v[i + N / 2];
+            v[i] = K::larger(a, b);
+            v[i + N / 2] = K::smaller(a, b);
+        }
+        sort_bitonic<K, N / 2>(v);
+        sort_bitonic<K, N / 2>(v + N / 2);
+    }
+}
+
+// v = the L largest of v (N, falling) and w (N, falling), falling; their count
+// is min(2 N, L).
+template <typename K, int N, int L>
+__device__ __forceinline__ void merge(typename K::T *v, const typename K::T *w)
+{
+    if constexpr (2 * N <= L) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[N + i] = w[N - 1 - i];
+        sort_bitonic<K, 2 * N>(v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = K::larger(v[i], w[N - 1 - i]);
+        sort_bitonic<K, N>(v);
+    }
+}
+
+template <typename K>
+__device__ __forceinline__ void order(typename K::T &a, typename K::T &b)
+{
+    const auto l = K::larger(a, b);
+    b = K::smaller(a, b);
+    a = l;
+}
+
+// Batcher's networks: 1, 5 and 19 exchanges.
+template <typename K, int N>
+__device__ __forceinline__ void sort(typename K::T *v)
+{
+    static_assert(N <= 8, "");
+    if constexpr (N == 2) {
+        order<K>(v[0], v[1]);
+    } else if constexpr (N > 2) {
+        sort<K, N / 2>(v);
+        sort<K, N / 2>(v + N / 2);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            order<K>(v[i], v[i + N / 2]);
+        if constexpr (N == 8) {
+            order<K>(v[2], v[4]);
+            order<K>(v[3], v[5]);
+        }
+#pragma unroll
+        for (int i = 1; i < N - 1; i += 2)
+            order<K>(v[i], v[i + 1]);
+    }
+}
+
+// The min(N, L) largest of v[N], falling, in out.
+template <typename K, int N, int L>
+__device__ __forceinline__ void sort_top(const typename K::T *v, typename K::T *out)
+{
+    if constexpr (N <= L) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            out[i] = v[i];
+        sort<K, N>(out);
+    } else {
+        typename K::T w[L];
+        sort_top<K, N / 2, L>(v, out);
+        sort_top<K, N / 2, L>(v + N / 2, w);
+        merge<K, L, L>(out, w);
+    }
+}
+
+// The same over the lanes of a row, N values in each.
+template <typename K, int G, int N, int L, int STEP = 0>
+__device__ __forceinline__ void merge_lanes(typename K::T *v)
+{
+    if constexpr (1 << STEP < G) {
+        typename K::T w[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            w[i] = other<STEP>(v[i]);
+        merge<K, N, L>(v, w);
+        merge_lanes<K, G, (2 * N < L ? 2 * N : L), L, STEP + 1>(v);
+    }
 }
 
 // exp(x - base).  The product's rounding is |x - base| 2^-24 of the result.
@@ -87,29 +231,41 @@ __device__ __forceinline__ float finite_base(float top) { return top == -INFINIT
 
 // The part of a row of `experts` elements that one lane holds: PER of them in
 // chunks of V, chunk c of lane l at element (c * G + l) * V.  V divides
-// `experts`, so a chunk lies in the row or past it.
+// `experts`, so a chunk lies in the row or past it and moves as a whole.
 template <bool BF16, int G_, int PER_, int V_>
 struct Row {
-    static constexpr int G = G_, PER = PER_, V = V_, kGroups = kThreads / G, kChunks = PER / V;
-    static constexpr int kKeep = (RR_MAX_ROUTE_TOPK + G - 1) / G;  // choices of a row per lane
+    static constexpr int G = G_, PER = PER_, V = V_, kChunks = PER / V;
+    static constexpr int kEs = BF16 ? 2 : 4;
+    static constexpr bool kPairs = BF16 && V > 1;    // two elements to a word
+    static constexpr int kWords = kPairs ? V / 2 : V;  // of a chunk
     using Raw = std::conditional_t<BF16, unsigned short, unsigned>;
     struct Chunk {
-        Raw v[V];
+        std::conditional_t<kPairs || !BF16, unsigned, unsigned short> w[kWords];
     };
-    Chunk c[kChunks];
+    unsigned w[kChunks * kWords];
 
     __device__ static int expert(int lane, int s) { return (s / V * G + lane) * V + s % V; }
 
-    __device__ void load(const void *p, int lane, int experts, Raw pad)
+    // Elements past the row are anything until pad().
+    __device__ void load(const void *p, int lane, int experts)
     {
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                c[i].v[e] = pad;
             const int at = (i * G + lane) * V;
-            if (at < experts)
-                __builtin_memcpy(&c[i], static_cast<const Raw *>(p) + at, sizeof(Chunk));
+            Chunk c;
+            __builtin_memcpy(&c, static_cast<const Raw *>(p) + (at < experts ? at : 0), sizeof c);
+#pragma unroll
+            for (int n = 0; n < kWords; ++n)
+                w[i * kWords + n] = c.w[n];
+        }
+    }
+    // -inf past the row
+    __device__ void pad(int lane, int experts)
+    {
+        if (experts < G * PER) {
+#pragma unroll
+            for (int i = 0; i < kChunks * kWords; ++i)
+                w[i] = (i / kWords * G + lane) * V < experts ? w[i] : BF16 ? 0xff80ff80u : 0xff800000u;
         }
     }
     __device__ void store(void *p, int lane, int experts) const
@@ -117,36 +273,49 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
             const int at = (i * G + lane) * V;
+            Chunk c;
+#pragma unroll
+            for (int n = 0; n < kWords; ++n)
+                c.w[n] = w[i * kWords + n];
             if (at < experts)
-                __builtin_memcpy(static_cast<Raw *>(p) + at, &c[i], sizeof(Chunk));
+                __builtin_memcpy(static_cast<Raw *>(p) + at, &c, sizeof c);
         }
     }
     __device__ float get(int s) const
     {
-        if constexpr (BF16)
-            return __uint_as_float(unsigned(c[s / V].v[s % V]) << 16);
+        if constexpr (kPairs)
+            return __uint_as_float(s % 2 ? w[s / 2] & 0xffff0000u : w[s / 2] << 16);
         else
-            return __uint_as_float(c[s / V].v[s % V]);
+            return __uint_as_float(BF16 ? w[s] << 16 : w[s]);
     }
-    __device__ void set(int s, float f)
+    __device__ void set(const float *f)
     {
-        if constexpr (BF16)
-            c[s / V].v[s % V] = __builtin_bit_cast(unsigned short, (__bf16)f);
-        else
-            c[s / V].v[s % V] = __float_as_uint(f);
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < kChunks * kWords; ++i)
+            if constexpr (kPairs)
+                w[i] = __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{f[2 * i], f[2 * i + 1]}, bf16x2));
+            else if constexpr (BF16)
+                w[i] = __builtin_bit_cast(unsigned short, (__bf16)f[i]);
+            else
+                w[i] = __float_as_uint(f[i]);
     }
-    static constexpr Raw kNothing = BF16 ? Raw(0xff80) : Raw(0xff800000u);  // -inf
 };
 
-template <bool BF16, typename R>
-__global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a)
+// L: at least topk and merged as lists, or 0.
+template <bool BF16, typename R, int L>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a)
 {
-    constexpr int G = R::G, PER = R::PER;
+    using K = Key<BF16>;
+    using T = typename K::T;
+    constexpr int G = R::G, PER = R::PER, kGroups = kRouteThreads / G;
+    constexpr int kKeep = ((L ? L : RR_MAX_ROUTE_TOPK) + G - 1) / G;  // choices per lane
     __shared__ int count[G * PER + 1];
-    __shared__ float sums[kWaves][G * PER];
+    __shared__ float sums[kRouteWaves][G * PER];
     const int lane = threadIdx.x % G, group = threadIdx.x / G;
-    const int64_t es = BF16 ? 2 : 4, step = int64_t(gridDim.x) * R::kGroups;
-    for (int i = threadIdx.x; i <= a.experts; i += kThreads)
+    const int64_t step = int64_t(gridDim.x) * kGroups, bytes = step * a.experts * R::kEs;
+    for (int i = threadIdx.x; i <= a.experts; i += kRouteThreads)
         count[i] = 0;
     __syncthreads();
     float sum[PER];
@@ -154,108 +323,117 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a)
     for (int s = 0; s < PER; ++s)
         sum[s] = 0.0f;
     int kept = 0;
-    int64_t r = int64_t(blockIdx.x) * R::kGroups + group;
-    const char *from = static_cast<const char *>(a.logits) + r * a.experts * es;
+    int64_t r = int64_t(blockIdx.x) * kGroups + group;
+    const char *from = static_cast<const char *>(a.logits) + r * a.experts * R::kEs;
     R row;
-    bool keep = true;
+    unsigned char keep = 1;
     if (r < a.rows) {
-        row.load(from, lane, a.experts, R::kNothing);
-        keep = !a.keep || a.keep[r];
+        row.load(from, lane, a.experts);
+        if (a.keep)
+            keep = a.keep[r];
     }
     for (; r < a.rows; r += step) {
-        // the next row is on its way while this one is worked on
+        // the next row is on its way meanwhile
         R next = row;
-        bool next_keep = true;
-        from += step * a.experts * es;
+        unsigned char next_keep = 1;
+        from += bytes;
         if (r + step < a.rows) {
-            next.load(from, lane, a.experts, R::kNothing);
-            next_keep = !a.keep || a.keep[r + step];
+            next.load(from, lane, a.experts);
+            if (a.keep)
+                next_keep = a.keep[r + step];
         }
-        int mine[R::kKeep];
-        float w[R::kKeep], top = -INFINITY, lse = 0.0f;
+        int mine[kKeep];
+        float w[kKeep], lse = 0.0f;
 #pragma unroll
-        for (int i = 0; i < R::kKeep; ++i)
+        for (int i = 0; i < kKeep; ++i)
             mine[i] = -1, w[i] = 0.0f;
         if (keep) {
-            float z[PER], total = 0.0f;
-            unsigned key[PER];
+            row.pad(lane, a.experts);
+            float z[PER], total, base;
+            T top_key;
+            T key[PER];
+            bool nan = false;
 #pragma unroll
             for (int s = 0; s < PER; ++s) {
-                z[s] = row.get(s);
-                key[s] = order_key(z[s]);
-                // bf16 leaves 16 bits free for the index, the lowest on top
-                if constexpr (BF16)
-                    key[s] = (key[s] & 0xffff0000u) | unsigned(0xffff - R::expert(lane, s));
-                if (R::expert(lane, s) >= a.experts)
-                    key[s] = 0;
-                top = fmaxf(top, z[s]);
+                key[s] = K::make(order_key(row.get(s)), R::expert(lane, s));
+                if (s % 2)
+                    nan |= __builtin_isunordered(row.get(s - 1), row.get(s));
             }
-            top = row_max<G>(top);
-            const float base = finite_base(top);
+            if (nan) {
+#pragma unroll
+                for (int s = 0; s < PER; ++s)
+                    if (row.get(s) != row.get(s))
+                        key[s] = K::make(kNanKey, R::expert(lane, s));
+            }
+            if constexpr (L > 0) {
+                T best[L];
+                sort_top<K, PER, L>(key, best);
+                merge_lanes<K, G, (PER < L ? PER : L), L>(best);
+                top_key = best[0];
+                constexpr int kHave = PER * G < L ? PER * G : L;
+#pragma unroll
+                for (int i = 0; i < kKeep; ++i) {
+                    T k = best[0];
+#pragma unroll
+                    for (int n = 1; n < kHave; ++n)
+                        k = i * G + lane == n ? best[n] : k;
+                    mine[i] = K::expert(k);
+                    w[i] = K::value(k);
+                }
+            } else {
+                top_key = key[0];
+                for (int k = 0; k < a.topk; ++k) {
+                    T best = key[0];
+#pragma unroll
+                    for (int s = 1; s < PER; ++s)
+                        best = K::larger(best, key[s]);
+                    best = across<G>(best, [](T x, T y) { return K::larger(x, y); });
+                    top_key = k == 0 ? best : top_key;
+#pragma unroll
+                    for (int s = 0; s < PER; ++s)
+                        key[s] = key[s] == best ? T(0) : key[s];
+#pragma unroll
+                    for (int i = 0; i < kKeep; ++i)
+                        if (k == i * G + lane) {
+                            mine[i] = K::expert(best);
+                            w[i] = K::value(best);
+                        }
+                }
+            }
+            base = finite_base(K::value(top_key));
+            total = 0.0f;
 #pragma unroll
             for (int s = 0; s < PER; ++s) {
-                z[s] = exp_from(z[s], base);
+                z[s] = exp_from(row.get(s), base);
                 total += z[s];
             }
             total = row_sum<G>(total);
-            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+            float chosen = 0.0f;
+            const float inv = total == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(total);
 #pragma unroll
             for (int s = 0; s < PER; ++s)
                 sum[s] = __builtin_fmaf(z[s], inv, sum[s]);
-            for (int k = 0; k < a.topk; ++k) {
-                unsigned best = 0;
-                int e = 0;
-                if constexpr (BF16) {
 #pragma unroll
-                    for (int s = 0; s < PER; ++s)
-                        best = key[s] > best ? key[s] : best;
-                    best = across<G>(best, [](unsigned x, unsigned y) { return x > y ? x : y; });
-                    e = 0xffff - int(best & 0xffffu);
-                } else {
-                    // a lane's experts ascend with s: the first of equals is the lowest
-#pragma unroll
-                    for (int s = 0; s < PER; ++s)
-                        if (key[s] > best) {
-                            best = key[s];
-                            e = R::expert(lane, s);
-                        }
-                    const unsigned own = best;
-                    best = across<G>(best, [](unsigned x, unsigned y) { return x > y ? x : y; });
-                    e = int(across<G>(own == best ? unsigned(e) : 0xffffu,
-                                      [](unsigned x, unsigned y) { return x < y ? x : y; }));
-                }
-#pragma unroll
-                for (int s = 0; s < PER; ++s)
-                    key[s] = e == R::expert(lane, s) ? 0 : key[s];
-#pragma unroll
-                for (int i = 0; i < R::kKeep; ++i)
-                    if (k == i * G + lane) {
-                        mine[i] = e;
-                        w[i] = key_value<BF16>(best);
-                    }
-            }
-            float chosen = 0.0f;
-#pragma unroll
-            for (int i = 0; i < R::kKeep; ++i) {
+            for (int i = 0; i < kKeep; ++i) {
                 w[i] = i * G + lane < a.topk ? exp_from(w[i], base) : 0.0f;
                 chosen += w[i];
             }
             float by = inv;
             if (a.renormalize) {
                 chosen = row_sum<G>(chosen);
-                by = chosen == 0.0f ? 0.0f : 1.0f / chosen;
+                by = chosen == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(chosen);
             }
 #pragma unroll
-            for (int i = 0; i < R::kKeep; ++i) {
+            for (int i = 0; i < kKeep; ++i) {
                 w[i] *= by;
-                if (mine[i] >= 0)
+                if (i * G + lane < a.topk)
                     atomicAdd(&count[mine[i]], 1);
             }
-            lse = top + logf(total);
+            lse = __builtin_fmaf(__builtin_amdgcn_logf(total), kLn2, K::value(top_key));
             ++kept;
         }
 #pragma unroll
-        for (int i = 0; i < R::kKeep; ++i)
+        for (int i = 0; i < kKeep; ++i)
             if (i * G + lane < a.topk) {
                 a.choice[r * a.topk + i * G + lane] = mine[i];
                 a.weight[r * a.topk + i * G + lane] = w[i];
@@ -275,10 +453,10 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a)
             sums[threadIdx.x / 64][R::expert(lane, s)] = sum[s];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i <= a.experts; i += kThreads) {
+    for (int i = threadIdx.x; i <= a.experts; i += kRouteThreads) {
         if (i < a.experts) {
             float t = 0.0f;
-            for (int w = 0; w < kWaves; ++w)
+            for (int w = 0; w < kRouteWaves; ++w)
                 t += sums[w][i];
             a.prob_sum[int64_t(blockIdx.x) * a.experts + i] = t;
         }
@@ -294,16 +472,14 @@ __global__ __launch_bounds__(kSumThreads) void route_sum_kernel(RouteSumArgs a)
     __shared__ int ns[kSumThreads];
     __shared__ float ss[kSumThreads];
     const int i = blockIdx.x * kSumWide + threadIdx.x % kSumWide, first = threadIdx.x / kSumWide;
+    const int in = i < a.experts ? i : a.experts, is = i < a.experts ? i : 0;
     constexpr int kStep = kSumThreads / kSumWide;
     int n = 0;
     float s = 0.0f;
-    if (i <= a.experts) {
 #pragma unroll 8
-        for (int b = first; b < a.blocks; b += kStep) {
-            n += a.part_counts[int64_t(b) * (a.experts + 1) + i];
-            if (i < a.experts)
-                s += a.part_sum[int64_t(b) * a.experts + i];
-        }
+    for (int b = first; b < a.blocks; b += kStep) {
+        n += a.part_counts[int64_t(b) * (a.experts + 1) + in];
+        s += a.part_sum[int64_t(b) * a.experts + is];
     }
     ns[threadIdx.x] = n;
     ss[threadIdx.x] = s;
@@ -352,52 +528,86 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a)
     }
 }
 
+// What one row's gradient needs beside its logits, of the choices that a lane
+// holds.
+template <int KEEP>
+struct Chosen {
+    int c[KEEP];
+    float w[KEEP], g[KEEP], lse;
+    int keep;
+
+    template <int G>
+    __device__ void load(const RouteGradArgs &a, int64_t r, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) {
+            const int64_t n = r * a.topk + (i * G + lane < a.topk ? i * G + lane : 0);
+            c[i] = a.choice[n];
+            w[i] = a.weight[n];
+            g[i] = a.grad_weight[n];
+        }
+        lse = a.lse[r];
+        keep = a.keep ? a.keep[r] : 1;
+    }
+};
+
 // The chosen experts' own terms lie in LDS, zero at every other expert, and
 // are zeroed again once read.
-template <bool BF16, typename R>
+template <bool BF16, typename R, int L, bool RENORM>
 __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a)
 {
-    constexpr int G = R::G, PER = R::PER, V = R::V;
-    __shared__ __attribute__((aligned(16))) float chosen_terms[R::kGroups][G * PER];
+    constexpr int G = R::G, PER = R::PER, V = R::V, kGroups = kThreads / G;
+    constexpr int kKeep = ((L ? L : RR_MAX_ROUTE_TOPK) + G - 1) / G;
+    __shared__ __attribute__((aligned(16))) float chosen_terms[kGroups][G * PER];
     const int lane = threadIdx.x % G, group = threadIdx.x / G;
     float *own = chosen_terms[group];
-    const int64_t es = BF16 ? 2 : 4, step = int64_t(gridDim.x) * R::kGroups;
+    const int64_t step = int64_t(gridDim.x) * kGroups;
+    int64_t r = int64_t(blockIdx.x) * kGroups + group;
+    if (r >= a.rows)
+        return;
+    R row;
+    Chosen<kKeep> of;
+    row.load(static_cast<const char *>(a.logits) + r * a.experts * R::kEs, lane, a.experts);
+    of.template load<G>(a, r, lane);
     const float gl = a.grad_loss[0];
     float slope[PER];
 #pragma unroll
-    for (int s = 0; s < PER; ++s) {
+    for (int s = 0; s < PER; s += V) {
         const int e = R::expert(lane, s);
-        slope[s] = e < a.experts ? gl * a.slope[e] : 0.0f;
-        own[e] = 0.0f;
+        __builtin_memcpy(&slope[s], a.slope + (e < a.experts ? e : 0), 4 * V);
+        for (int n = 0; n < V; ++n)
+            own[e + n] = 0.0f;
     }
-    for (int64_t r = int64_t(blockIdx.x) * R::kGroups + group; r < a.rows; r += step) {
-        const int64_t at = r * a.experts * es;
-        R row;
-        row.load(static_cast<const char *>(a.logits) + at, lane, a.experts, R::kNothing);
-        const float base = finite_base(a.lse[r]);
-        float w[R::kKeep], g[R::kKeep], mean = 0.0f;
-        int c[R::kKeep];
 #pragma unroll
-        for (int i = 0; i < R::kKeep; ++i) {
-            const int64_t n = r * a.topk + i * G + lane;
-            const bool in = i * G + lane < a.topk;
-            c[i] = in ? a.choice[n] : -1;
-            w[i] = in && a.renormalize ? a.weight[n] : 0.0f;
-            g[i] = in ? a.grad_weight[n] : 0.0f;
-            if (c[i] >= a.experts)
-                c[i] = -1;
-            mean += w[i] * g[i];
+    for (int s = 0; s < PER; ++s)
+        slope[s] *= gl;
+    for (; r < a.rows; r += step) {
+        R next = row;
+        Chosen<kKeep> next_of = of;
+        if (r + step < a.rows) {
+            next.load(static_cast<const char *>(a.logits) + (r + step) * a.experts * R::kEs, lane, a.experts);
+            next_of.template load<G>(a, r + step, lane);
         }
-        if (!a.keep || a.keep[r]) {
-            if (a.renormalize)
+        float d[PER];
+        if (of.keep) {
+            row.pad(lane, a.experts);
+            float mean = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) {
+                if (i * G + lane >= a.topk || unsigned(of.c[i]) >= unsigned(a.experts))
+                    of.c[i] = -1;
+                mean += i * G + lane < a.topk ? of.w[i] * of.g[i] : 0.0f;
+            }
+            if constexpr (RENORM)
                 mean = row_sum<G>(mean);
 #pragma unroll
-            for (int i = 0; i < R::kKeep; ++i)
-                if (c[i] >= 0)
-                    own[c[i]] = a.renormalize ? w[i] * (g[i] - mean) : g[i];
+            for (int i = 0; i < kKeep; ++i)
+                if (of.c[i] >= 0)
+                    own[of.c[i]] = RENORM ? of.w[i] * (of.g[i] - mean) : of.g[i];
             // one wave's LDS operations keep their order; so has the compiler to
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
+            const float base = finite_base(of.lse);
             float p[PER], term[PER], dot = 0.0f;
 #pragma unroll
             for (int s = 0; s < PER; s += V)
@@ -405,81 +615,121 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a)
 #pragma unroll
             for (int s = 0; s < PER; ++s) {
                 p[s] = exp_from(row.get(s), base);
-                dot = __builtin_fmaf(p[s], a.renormalize ? slope[s] : slope[s] + term[s], dot);
+                d[s] = RENORM ? slope[s] : slope[s] + term[s];
+                dot = __builtin_fmaf(p[s], d[s], dot);
             }
             dot = row_sum<G>(dot);
 #pragma unroll
             for (int s = 0; s < PER; ++s)
-                row.set(s, a.renormalize ? __builtin_fmaf(p[s], slope[s] - dot, term[s])
-                                         : p[s] * (slope[s] + term[s] - dot));
+                d[s] = RENORM ? __builtin_fmaf(p[s], d[s] - dot, term[s]) : p[s] * (d[s] - dot);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int i = 0; i < R::kKeep; ++i)
-                if (c[i] >= 0)
-                    own[c[i]] = 0.0f;
+            for (int i = 0; i < kKeep; ++i)
+                if (of.c[i] >= 0)
+                    own[of.c[i]] = 0.0f;
         } else {
 #pragma unroll
             for (int s = 0; s < PER; ++s)
-                row.set(s, 0.0f);
+                d[s] = 0.0f;
         }
-        row.store(static_cast<char *>(a.dlogits) + at, lane, a.experts);
+        row.set(d);
+        row.store(static_cast<char *>(a.dlogits) + r * a.experts * R::kEs, lane, a.experts);
+        row = next;
+        of = next_of;
     }
 }
 
-// Lanes of a row.
-int lanes_of(int experts) { return experts <= 256 ? 16 : 64; }
+// Lanes of a row, and f(Row type) for a number of experts.
+int lanes_of(int experts) { return experts <= 32 ? 4 : experts <= 64 ? 8 : experts <= 256 ? 16 : 64; }
 
-// f(Row type) for a number of experts: the next power of two per lane, in
-// chunks of up to 16 bytes where those divide a row.
 template <bool BF16, int G, int PER, typename F>
 hipError_t with_chunk(int experts, F f)
 {
-    constexpr int kMost = BF16 ? 8 : 4, V = PER < kMost ? PER : kMost;
-    if (experts % V == 0)
-        return f(Row<BF16, G, PER, V>{});
+    if constexpr (BF16 && PER >= 8)
+        if (experts % 8 == 0)
+            return f(Row<BF16, G, PER, 8>{});
+    if (experts % 4 == 0)
+        return f(Row<BF16, G, PER, 4>{});
     return f(Row<BF16, G, PER, 1>{});
 }
 
 template <bool BF16, typename F>
 hipError_t with_row(int experts, F f)
 {
-    if (lanes_of(experts) == 64)
-        return experts <= 512 ? with_chunk<BF16, 64, 8>(experts, f) : with_chunk<BF16, 64, 16>(experts, f);
     if (experts <= 16)
-        return with_chunk<BF16, 16, 1>(experts, f);
+        return with_chunk<BF16, 4, 4>(experts, f);
     if (experts <= 32)
-        return with_chunk<BF16, 16, 2>(experts, f);
+        return with_chunk<BF16, 4, 8>(experts, f);
     if (experts <= 64)
-        return with_chunk<BF16, 16, 4>(experts, f);
+        return with_chunk<BF16, 8, 8>(experts, f);
     if (experts <= 128)
         return with_chunk<BF16, 16, 8>(experts, f);
-    return with_chunk<BF16, 16, 16>(experts, f);
+    if (experts <= 256)
+        return with_chunk<BF16, 16, 16>(experts, f);
+    if (experts <= 512)
+        return with_chunk<BF16, 64, 8>(experts, f);
+    return with_chunk<BF16, 64, 16>(experts, f);
+}
+
+template <int N> using Int = std::integral_constant<int, N>;
+
+// f(list length) for a number of choices.
+template <typename F>
+hipError_t with_list(int topk, F f)
+{
+    return topk <= 2 ? f(Int<2>{}) : topk <= 4 ? f(Int<4>{}) : topk <= 8 ? f(Int<8>{}) : f(Int<0>{});
 }
 
 }  // namespace
 
 int32_t route_blocks(int64_t rows, int32_t experts)
 {
-    const int64_t groups = kThreads / lanes_of(experts), n = (rows + groups - 1) / groups;
+    const int64_t groups = kRouteThreads / lanes_of(experts), n = (rows + groups - 1) / groups;
     // up to four rows per group a second launch costs more than it saves
-    return n <= 4 ? 1 : int32_t(n < 1024 ? n : 1024);
+    return n <= 4 ? 1 : int32_t(n < 512 ? n : 512);
 }
+
+namespace {
+
+template <bool BF16>
+hipError_t route(const RouteArgs &a, hipStream_t stream)
+{
+    return with_row<BF16>(a.experts, [&](auto row) {
+        return with_list(a.topk, [&](auto list) {
+            route_kernel<BF16, decltype(row), decltype(list)::value>
+                <<<dim3(unsigned(a.blocks)), dim3(kRouteThreads), 0, stream>>>(a);
+            return hipGetLastError();
+        });
+    });
+}
+
+template <bool BF16>
+hipError_t route_grad(const RouteGradArgs &a, hipStream_t stream)
+{
+    const int64_t groups = kThreads / lanes_of(a.experts), n = (a.rows + groups - 1) / groups;
+    const dim3 grid(unsigned(n < 2048 ? n : 2048)), threads(kThreads);
+    return with_row<BF16>(a.experts, [&](auto row) {
+        using R = decltype(row);
+        if (a.topk <= 8 && a.renormalize)
+            route_grad_kernel<BF16, R, 8, true><<<grid, threads, 0, stream>>>(a);
+        else if (a.topk <= 8)
+            route_grad_kernel<BF16, R, 8, false><<<grid, threads, 0, stream>>>(a);
+        else if (a.renormalize)
+            route_grad_kernel<BF16, R, 0, true><<<grid, threads, 0, stream>>>(a);
+        else
+            route_grad_kernel<BF16, R, 0, false><<<grid, threads, 0, stream>>>(a);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace
 
 hipError_t launch_route(const Op &op, hipStream_t stream)
 {
     const RouteArgs a = op.get<RouteArgs>();
     (void)hipGetLastError();
-    const dim3 grid(unsigned(a.blocks)), threads(kThreads);
-    if (a.bf16)
-        return with_row<true>(a.experts, [&](auto r) {
-            route_kernel<true, decltype(r)><<<grid, threads, 0, stream>>>(a);
-            return hipGetLastError();
-        });
-    return with_row<false>(a.experts, [&](auto r) {
-        route_kernel<false, decltype(r)><<<grid, threads, 0, stream>>>(a);
-        return hipGetLastError();
-    });
+    return a.bf16 ? route<true>(a, stream) : route<false>(a, stream);
 }
 
 hipError_t launch_route_sum(const Op &op, hipStream_t stream)
@@ -501,18 +751,8 @@ hipError_t launch_balance(const Op &op, hipStream_t stream)
 hipError_t launch_route_grad(const Op &op, hipStream_t stream)
 {
     const RouteGradArgs a = op.get<RouteGradArgs>();
-    const int64_t groups = kThreads / lanes_of(a.experts), n = (a.rows + groups - 1) / groups;
-    const dim3 grid(unsigned(n < 2048 ? n : 2048)), threads(kThreads);
     (void)hipGetLastError();
-    if (a.bf16)
-        return with_row<true>(a.experts, [&](auto r) {
-            route_grad_kernel<true, decltype(r)><<<grid, threads, 0, stream>>>(a);
-            return hipGetLastError();
-        });
-    return with_row<false>(a.experts, [&](auto r) {
-        route_grad_kernel<false, decltype(r)><<<grid, threads, 0, stream>>>(a);
-        return hipGetLastError();
-    });
+    return a.bf16 ? route_grad<true>(a, stream) : route_grad<false>(a, stream);
 }
 
 }  // namespace rr
