@@ -135,38 +135,38 @@ private:
 };
 
 // The workspace of rr_vocab_grad.  dz is held for one piece of the vocabulary
-// at a time, in both layouts.
+// at a time.
 struct GradSpace {
-    int64_t piece, ldr, ldv, lda;
-    int32_t splits;
+    int64_t piece, ldd, ldv, lda;
+    int32_t pieces, splits;
     float2 *row;
-    char *xt, *wt, *dz, *dzt;
+    char *x, *w, *dz;    // x, w: copies in 16-byte chunks, of operands that are not
     float *acc;
     int64_t bytes;
 };
 
-// Bytes of one piece of dz in one layout.
+// Bytes of one piece of dz.
 constexpr int64_t kPieceBytes = int64_t(1) << 28;
 
 GradSpace grad_space(const rr_vocab *v, int dtype, int64_t rows, void *base)
 {
     const int64_t es = elem_size(dtype);
     GradSpace s{};
-    s.ldr = round_up(std::max<int64_t>(rows, 1), 64);
-    const int64_t most = std::max<int64_t>(kPieceBytes / (s.ldr * es) / 256 * 256, 256);
+    const int64_t most = std::max<int64_t>(kPieceBytes / (std::max<int64_t>(rows, 1) * es) / 256 * 256, 256);
     const int64_t pieces = (v->vocab + most - 1) / most;
     s.piece = pieces ? std::min(round_up((v->vocab + pieces - 1) / pieces, 256), v->vocab) : 0;
+    s.ldd = round_up(v->dim, 16 / es);
     s.ldv = round_up(s.piece, 64);
     s.lda = round_up(v->dim, 4);
+    s.pieces = s.piece ? int32_t((v->vocab + s.piece - 1) / s.piece) : 0;
     // one number of parts for every piece, as the sums go on from piece to piece
-    s.splits = product_splits(Product{nullptr, nullptr, s.ldv, s.ldv, v->dim, int32_t(rows), int32_t(s.piece),
+    s.splits = product_splits(Product{nullptr, nullptr, s.ldd, s.ldv, v->dim, int32_t(rows), int32_t(s.piece),
                                       dtype == RR_BF16});
     Carver c(base);
     s.row = static_cast<float2 *>(c.take(rows * 8));
-    s.xt = static_cast<char *>(c.take(v->dim * s.ldr * es));
-    s.wt = static_cast<char *>(c.take(v->dim * s.ldv * es));
+    s.x = static_cast<char *>(c.take(rows * s.ldd * es));
+    s.w = static_cast<char *>(c.take(s.piece * s.ldd * es));
     s.dz = static_cast<char *>(c.take(rows * s.ldv * es));
-    s.dzt = static_cast<char *>(c.take(s.piece * s.ldr * es));
     s.acc = static_cast<float *>(c.take(s.splits * rows * s.lda * 4));
     s.bytes = c.used();
     return s;
@@ -366,23 +366,30 @@ rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *
             l.add(launch_gather, GatherArgs{nullptr, dw, v->vocab, 0, dim, 0, bf16});
         return l.finish();
     }
-    if (v->vocab > 0) {
+    if (v->vocab > 0)
         l.add(launch_rows, RowsArgs{index, lse, prob, grad, n, v->topk, v->total, v->scale, s.row});
-        l.add(launch_transpose, TransposeArgs{x, s.xt, dim, s.ldr, n, dim, bf16});
-    }
+    const bool copy_x = !in_chunks(x, dim, es), copy_w = !in_chunks(w, dim, es);
+    const bool whole = s.pieces == 1 && s.splits == 1;  // dx is one product
+    const void *xc = copy_x ? s.x : x;
+    const int64_t ldx = copy_x ? s.ldd : dim, ldw = copy_w ? s.ldd : dim;
+    if (copy_x && v->vocab > 0)
+        l.add(launch_align, AlignArgs{x, s.x, rows, s.ldd, dim, bf16});
     for (int64_t v0 = 0; v0 < v->vocab; v0 += s.piece) {
         const int32_t c = int32_t(std::min(s.piece, v->vocab - v0));
-        const char *wp = static_cast<const char *>(w) + v0 * dim * es;
+        const void *wc = static_cast<const char *>(w) + v0 * dim * es;
         char *dwp = static_cast<char *>(dw) + v0 * dim * es;
-        l.add(launch_dz, DzArgs{Product{wp, x, dim, dim, c, n, dim, bf16}, v->scale, s.row, s.dz, s.dzt, s.ldv, s.ldr});
-        l.add(launch_targets, TargetArgs{index, logit, prob, s.row, n, v->topk, c, bf16, v->first + v0,
-                                         s.dz, s.dzt, s.ldv, s.ldr});
-        l.add(launch_transpose, TransposeArgs{wp, s.wt, dim, s.ldv, c, dim, bf16});
-        l.add(launch_store, StoreArgs{Product{s.xt, s.dzt, s.ldr, s.ldr, dim, c, n, bf16}, dwp, dim, nullptr, 0, 1, 0});
-        l.add(launch_store, StoreArgs{Product{s.wt, s.dz, s.ldv, s.ldv, dim, n, c, bf16}, nullptr, 0, s.acc,
-                                      s.lda, s.splits, v0 > 0});
+        if (copy_w) {
+            l.add(launch_align, AlignArgs{wc, s.w, c, s.ldd, dim, bf16});
+            wc = s.w;
+        }
+        l.add(launch_dz, DzArgs{Product{wc, xc, ldw, ldx, c, n, dim, bf16}, v->scale, s.row, s.dz, s.ldv});
+        l.add(launch_targets, TargetArgs{index, logit, prob, s.row, n, v->topk, c, bf16, v->first + v0, s.dz, s.ldv});
+        l.add(launch_store, StoreArgs{Product{xc, s.dz, ldx, s.ldv, dim, c, n, bf16}, dwp, dim, nullptr, 0, 1, 0, 1});
+        l.add(launch_store, StoreArgs{Product{wc, s.dz, ldw, s.ldv, dim, n, c, bf16}, whole ? dx : nullptr, dim,
+                                      whole ? nullptr : s.acc, s.lda, s.splits, v0 > 0, 0});
     }
-    l.add(launch_gather, GatherArgs{s.acc, dx, rows, s.lda, dim, v->vocab > 0 ? s.splits : 0, bf16});
+    if (!whole)
+        l.add(launch_gather, GatherArgs{s.acc, dx, rows, s.lda, dim, v->vocab > 0 ? s.splits : 0, bf16});
     return l.finish();
 }
 

@@ -46,17 +46,23 @@ rr_status set_error(rr_status st, const char *fmt, ...) __attribute__((format(pr
 rr_status set_ok();
 
 // ---------------------------------------------------------------------------
-// Vocabulary head.  Every product is C[j][i] = sum_k A[i][k] * B[j][k], both
-// operands with contiguous k: "i" (the fast axis of C) runs over the
-// vocabulary for the logits and over dim for dw and dx.
+// Vocabulary head.  Every product is C[j][i] = sum_k A[i][k] * B[j][k], an
+// operand lying as [i or j][k], or tall as [k][i or j]: "i" (the fast axis of
+// C) runs over the vocabulary for the logits and over dim for dw and dx.
 // ---------------------------------------------------------------------------
 
 struct Product {
-    const void *a, *b;   // [ni][lda], [nj][ldb]
+    const void *a, *b;   // [ni][lda], [nj][ldb]; tall [nk][lda], [nk][ldb]
     int64_t lda, ldb;    // elements
     int32_t ni, nj, nk;
     int32_t bf16;        // element type of a and b
 };
+
+// Rows that start at, and are a multiple of, 16 bytes.
+inline bool in_chunks(const void *p, int64_t ld, int64_t es)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0;
+}
 
 // The logits' softmax statistics per part of the vocabulary.
 struct StatsArgs {
@@ -105,13 +111,14 @@ struct RowsArgs {
 };
 hipError_t launch_rows(const Op &, hipStream_t);
 
-// dz of one piece of the vocabulary without its targets, in both layouts.
+// dz of one piece of the vocabulary without its targets.  Operands in 16-byte
+// chunks.
 struct DzArgs {
     Product p;           // a = the piece of w, b = x
     float scale;
     const float2 *row;
-    void *dz, *dzt;      // [nj][ldz], [ni][ldt]
-    int64_t ldz, ldt;
+    void *dz;            // [nj][ldz]
+    int64_t ldz;
 };
 hipError_t launch_dz(const Op &, hipStream_t);
 
@@ -122,23 +129,22 @@ struct TargetArgs {
     const float2 *row;
     int32_t rows, topk, count, bf16;  // entries [first, first + count) of the vocabulary
     int64_t first;
-    void *dz, *dzt;
-    int64_t ldz, ldt;
+    void *dz;
+    int64_t ldz;
 };
 hipError_t launch_targets(const Op &, hipStream_t);
 
-// out[c][r] = in[r][c] for r < rows, c < cols; out rows end in zeros up to
-// the next multiple of 64 of rows.
-struct TransposeArgs {
-    const void *in;
-    void *out;
-    int64_t ldi, ldo;
-    int32_t rows, cols, bf16;
+// A matrix copied to rows that start at multiples of 16 bytes and end in zeros.
+struct AlignArgs {
+    const void *in;      // [rows][cols]
+    void *out;           // [rows][ldo]
+    int64_t rows, ldo;
+    int32_t cols, bf16;
 };
-hipError_t launch_transpose(const Op &, hipStream_t);
+hipError_t launch_align(const Op &, hipStream_t);
 
-// A product stored as the element type, or in fp32 as one sum for each of the
-// `splits` parts of k.
+// A product, A tall, stored as the element type, or in fp32 as one sum for each
+// of the `splits` parts of k.  Operands in 16-byte chunks.
 struct StoreArgs {
     Product p;
     void *out;           // [nj][ldo]
@@ -146,6 +152,7 @@ struct StoreArgs {
     float *acc;          // not null: [splits][nj][lda] instead of out
     int64_t lda;         // a multiple of 4
     int32_t splits, add; // add: to what acc holds
+    int32_t tall_b;
 };
 int32_t product_splits(const Product &p);
 hipError_t launch_store(const Op &, hipStream_t);

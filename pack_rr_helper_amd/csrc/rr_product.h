@@ -1,13 +1,23 @@
 // rr_product.h -- one output tile of C[j][i] = sum_k A[i][k] B[j][k] on the
-// gfx950 matrix cores, both operands with contiguous k.
+// gfx950 matrix cores.  Either operand lies with contiguous k, or "tall", with
+// contiguous i or j.
 //
 // A workgroup of WI x WJ waves computes TI x TJ results in registers.  k goes
-// by in steps of 128 bytes per row (64 bf16, 32 fp32).  STAGES steps of both
-// operands are held in LDS; the loads of step t + STAGES - 1 are issued before
-// step t is computed, and write LDS directly (buffer_load ... lds) without
-// passing through registers.  A row's eight 16-byte chunks lie in LDS at chunk
-// c ^ ((row >> 1) & 7): sixteen consecutive rows of one logical chunk then
-// cover all 64 banks, which is what one fragment read touches.
+// by in steps of 64 bf16 or 32 fp32.  STAGES steps of both operands are held in
+// LDS; loads write LDS directly (buffer_load ... lds) without passing through
+// registers.  A step is computed in two halves.  While the first runs, the
+// second's fragments are read; a quarter into the second, one barrier says that
+// this step has been read by all and that the next one has arrived, the loads
+// of step s + STAGES go out and the next first half's fragments are read, so
+// that the matrix instructions find theirs in registers.
+//
+// LDS layout of a step with contiguous k: 128 bytes per row, the eight 16-byte
+// chunks at chunk c ^ ((row >> 1) & 7); sixteen consecutive rows of one logical
+// chunk then cover all 64 banks, which is what one fragment read touches.
+// Tall: one row per k as wide as the tile, chunk c at c ^ f(k).  bf16 fragments
+// are read transposed (ds_read_b64_tr_b16: sixteen lanes read four rows of 32
+// bytes, each lane gets a column), f(k) = 2 (k % 4 + 4 (k / 8 % 2)) sets eight
+// such rows side by side; fp32 ones by the element, f(k) = 4 (k / 4 % 4).
 //
 // fp32 elements go through the fp32 matrix instructions.  A lane's 16-byte
 // fragment holds four consecutive k there, used by four instructions in turn;
@@ -28,17 +38,29 @@ constexpr int kRowBytes = 128;
 constexpr int kBufferFormat = 0x00020000;  // raw buffer: 32-bit data format, no swizzle
 constexpr int kNowhere = 0x7fff0000;       // a byte offset past the end of every buffer
 
-// At most n vector memory operations outstanding.
+// At most N vector memory operations outstanding, and no LDS operation.
 template <int N>
 __device__ __forceinline__ void wait_loads()
 {
-    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4 | 15 << 8);
+    static_assert(N < 64, "");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4 | 0 << 8);
 }
 
 // The LDS address of a generic pointer into LDS (its low half).
 __device__ __forceinline__ __attribute__((address_space(3))) void *lds_pointer(char *p)
 {
     return reinterpret_cast<__attribute__((address_space(3))) void *>(uint32_t(reinterpret_cast<uintptr_t>(p)));
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 *LdsTile;
+
+// Sixteen lanes read four rows of 32 bytes, 8 bytes each; a lane gets its column
+// of the four.  The restricted pointer tells the compiler that loads into LDS
+// under way do not concern this read, for which it would wait otherwise.
+__device__ __forceinline__ s16x4 read_transposed(LdsTile __restrict p)
+{
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
 }
 
 // Sixteen bytes at any element alignment, zeros from byte `left` on.
@@ -94,17 +116,21 @@ __device__ __forceinline__ void tile_at(int b, int n, int tiles_i, int tiles_j, 
     j = group * kGroup + in % wide;
 }
 
-template <bool BF16, int TI_, int TJ_, int WI, int WJ, int STAGES, bool DIRECT>
+template <bool BF16, int TI_, int TJ_, int WI, int WJ, int STAGES, bool DIRECT, bool TALL_A = false, bool TALL_B = false>
 struct Tile {
     static constexpr int TI = TI_, TJ = TJ_, kWaves = WI * WJ, kThreads = kWaves * 64;
     static constexpr int FI = TI / WI / 16, FJ = TJ / WJ / 16;  // 16 x 16 results per wave
     static constexpr int kEs = BF16 ? 2 : 4, kStep = kRowBytes / kEs;
     static constexpr int kRows = 8 * kWaves;                    // rows of one load of the workgroup
+    static constexpr int kLoadBytes = kRows * kRowBytes;
     static constexpr int kLoadsA = TI / kRows, kLoadsB = (TJ + kRows - 1) / kRows;
     static constexpr int kLoads = kLoadsA + kLoadsB;
-    static constexpr int kStageBytes = kLoads * kRows * kRowBytes;
+    static constexpr int kStageBytes = kLoads * kLoadBytes;
     static constexpr int kLdsBytes = STAGES * kStageBytes;
     static_assert(TI % kRows == 0 && FI * WI * 16 == TI && FJ * WJ * 16 == TJ, "");
+    static_assert(DIRECT || !(TALL_A || TALL_B), "");
+    static_assert(!TALL_A || TI >= 128, "a tall row has to hold the swizzle");
+    static_assert(!TALL_B || (TJ >= 128 && TJ % kRows == 0), "");
 
     struct Acc {
         f32x4 c[FI][FJ];
@@ -116,6 +142,119 @@ struct Tile {
     __device__ static int lane_i(int f) { return wave_i() + f * 16 + threadIdx.x % 64 / 16 * 4; }
     __device__ static int lane_j(int f) { return wave_j() + f * 16 + threadIdx.x % 16; }
 
+    // One operand: W rows of the tile, n in all from row r0 on.
+    template <bool TALL, int W, int LOADS>
+    struct Side {
+        const char *base;
+        int64_t ld;       // bytes
+        int off[LOADS];   // this lane's byte offsets within a step
+        int chunk;        // of k, TALL: unused
+        int left;         // bytes of base: of all steps, TALL: of the row
+        int nk;
+        __amdgpu_buffer_rsrc_t whole;
+
+        __device__ void init(const void *p, int64_t stride, int n, int64_t r0, int k)
+        {
+            const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+            ld = stride * kEs;
+            nk = k;
+            const int rows = int(n - r0 < W ? n - r0 : W);
+            if constexpr (TALL) {
+                constexpr int kWide = W * kEs;
+                base = static_cast<const char *>(p) + r0 * kEs;
+                left = (rows * kEs + 15) / 16 * 16;
+#pragma unroll
+                for (int l = 0; l < LOADS; ++l) {
+                    const int at = l * kLoadBytes + wave * 1024 + lane * 16, row = at / kWide;
+                    const int f = BF16 ? 2 * (row % 4 + 4 * (row / 8 % 2)) : 4 * (row / 4 % 4);
+                    const int c = ((at % kWide / 16) ^ f) * 16;
+                    off[l] = c < left && row * ld < kNowhere - kRowBytes * W ? int(row * ld) + c : kNowhere;
+                }
+                chunk = 0;
+            } else {
+                base = static_cast<const char *>(p) + r0 * ld;
+                const int row0 = wave * 8 + lane / 8;
+                chunk = ((lane % 8) ^ ((row0 >> 1) & 7)) * 16;   // kRows is a multiple of 16
+#pragma unroll
+                for (int l = 0; l < LOADS; ++l) {
+                    const int row = l * kRows + row0;
+                    off[l] = row < rows ? int(row * ld) + chunk : kNowhere;
+                }
+                left = int(rows * ld);
+                whole = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), (short)0, left, kBufferFormat);
+            }
+        }
+        // Step s to LDS; what lies past k, past the operand, or in a step that
+        // is not wanted becomes zeros.
+        __device__ void fetch(int s, bool wanted, char *to) const
+        {
+            if constexpr (TALL) {
+                const int64_t k0 = int64_t(s) * kStep;
+                const int rows = nk - k0 < kStep ? int(nk - k0) : kStep;
+                // bytes from this step's first to the operand's last
+                const int have = wanted && rows > 0 ? int((rows - 1) * ld) + left : 0;
+                const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                    const_cast<char *>(base + (wanted ? k0 * ld : 0)), (short)0, have, kBufferFormat);
+#pragma unroll
+                for (int l = 0; l < LOADS; ++l)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_pointer(to + l * kLoadBytes), 16, off[l], 0, 0, 0);
+            } else {
+                const int k = s * kRowBytes;
+                const bool in = k + chunk < nk * kEs && wanted;
+#pragma unroll
+                for (int l = 0; l < LOADS; ++l)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(whole, lds_pointer(to + l * kLoadBytes), 16,
+                                                             in ? off[l] : kNowhere, k, 0, 0);
+            }
+        }
+        // The same through registers, for operands at any element alignment.
+        __device__ void hold(int s, bool wanted, u32x4 *held) const
+        {
+            const int k = s * kRowBytes, end = nk * kEs;
+#pragma unroll
+            for (int l = 0; l < LOADS; ++l) {
+                held[l] = u32x4{0, 0, 0, 0};
+                if (k + chunk < end && wanted && off[l] != kNowhere)
+                    held[l] = load_chunk<kEs>(base + off[l] + k, end - k - chunk);
+            }
+        }
+        // This lane's part of 16 rows from row f on, of half h.
+        __device__ static u32x4 fragment(const char *stage, int f, int h)
+        {
+            const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
+            if constexpr (!TALL) {
+                return *reinterpret_cast<const u32x4 *>(stage + (f + r) * kRowBytes + ((4 * h + g) ^ (r >> 1)) * 16);
+            } else if constexpr (BF16) {
+                const char *at = stage + (32 * h + 8 * g + r / 4) * (W * 2) +
+                                 ((f / 8) ^ (2 * (r / 4 + 4 * (g % 2)))) * 16 + r % 4 * 8;
+                struct {
+                    s16x4 lo, hi;
+                } v;
+                v.lo = read_transposed((LdsTile)lds_pointer(const_cast<char *>(at)));
+                v.hi = read_transposed((LdsTile)lds_pointer(const_cast<char *>(at + 4 * W * 2)));
+                return __builtin_bit_cast(u32x4, v);
+            } else {
+                const char *at = stage + (16 * h + 4 * g) * (W * 4) + ((f / 4) ^ (4 * g)) * 16 + r * 4;
+                u32x4 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = *reinterpret_cast<const unsigned *>(at + e * W * 4);
+                return v;
+            }
+        }
+    };
+
+    __device__ static void multiply(const u32x4 &a, const u32x4 &b, f32x4 &c)
+    {
+        if constexpr (BF16) {
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c, 0, 0, 0);
+        }
+    }
+
     // Steps [s0, s1) of k of the tile at (i0, j0).
     __device__ static void run(const Product &p, int64_t i0, int64_t j0, int s0, int s1, char *lds, Acc &acc)
     {
@@ -125,101 +264,103 @@ struct Tile {
 #pragma unroll
             for (int j = 0; j < FJ; ++j)
                 acc.c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-        const int64_t lda = p.lda * kEs, ldb = p.ldb * kEs;
-        const int rows_a = int(p.ni - i0 < TI ? p.ni - i0 : TI), rows_b = int(p.nj - j0 < TJ ? p.nj - j0 : TJ);
-        const char *base_a = static_cast<const char *>(p.a) + i0 * lda, *base_b = static_cast<const char *>(p.b) + j0 * ldb;
-        const int end = p.nk * kEs;
-        // this lane's rows and chunks of each load
-        int off[kLoads], chunk[kLoads];
-#pragma unroll
-        for (int n = 0; n < kLoads; ++n) {
-            const bool is_a = n < kLoadsA;
-            const int row = (is_a ? n : n - kLoadsA) * kRows + wave * 8 + lane / 8;
-            chunk[n] = ((lane % 8) ^ ((row >> 1) & 7)) * 16;
-            off[n] = row < (is_a ? rows_a : rows_b) ? int(row * (is_a ? lda : ldb)) + chunk[n] : kNowhere;
-        }
-        const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char *>(base_a), (short)0, int(rows_a * lda), kBufferFormat);
-        const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char *>(base_b), (short)0, int(rows_b * ldb), kBufferFormat);
-
-        u32x4 held[DIRECT ? 1 : kLoads];
-        // Step s into its LDS buffer (DIRECT) or into registers; chunks past
-        // the end of k and rows past the end of an operand become zeros.
-        auto fetch = [&](int s) {
-            const int k = s * kRowBytes;
-            char *to = lds + s % STAGES * kStageBytes + wave * 1024;
-#pragma unroll
-            for (int n = 0; n < kLoads; ++n) {
-                const bool in = k + chunk[n] < end && s < s1;
-                if constexpr (DIRECT) {
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(n < kLoadsA ? ra : rb, lds_pointer(to + n * kRows * kRowBytes),
-                                                             16, in ? off[n] : kNowhere, k, 0, 0);
-                } else {
-                    held[n] = u32x4{0, 0, 0, 0};
-                    if (in && off[n] != kNowhere)
-                        held[n] = load_chunk<kEs>((n < kLoadsA ? base_a : base_b) + off[n] + k, end - k - chunk[n]);
-                }
-            }
-        };
-        auto commit = [&](int s) {
-            char *to = lds + s % STAGES * kStageBytes + wave * 1024 + lane * 16;
-#pragma unroll
-            for (int n = 0; n < kLoads; ++n)
-                *reinterpret_cast<u32x4 *>(to + n * kRows * kRowBytes) = held[DIRECT ? 0 : n];
-        };
-        // fragment reads: this lane's row and chunk in each half of a step
-        const int frow = lane % 16;
-        const int swz = (frow >> 1) & 7;
-        const int at0 = frow * kRowBytes + ((lane / 16) ^ swz) * 16, at1 = frow * kRowBytes + ((4 + lane / 16) ^ swz) * 16;
+        using A = Side<TALL_A, TI, kLoadsA>;
+        using B = Side<TALL_B, TJ, kLoadsB>;
+        A a;
+        B b;
+        a.init(p.a, p.lda, p.ni, i0, p.nk);
+        b.init(p.b, p.ldb, p.nj, j0, p.nk);
+        const int wi = wave_i(), wj = wave_j();
 
         if constexpr (DIRECT) {
+            auto fetch = [&](int s) {
+                char *to = lds + s % STAGES * kStageBytes + wave * 1024;
+                a.fetch(s, s < s1, to);
+                b.fetch(s, s < s1, to + kLoadsA * kLoadBytes);
+            };
+            u32x4 a0[FI], b0[FJ], a1[FI], b1[FJ];
+            auto read = [&](int s, int h, u32x4 *fa, u32x4 *fb, int n) {
+                const char *stage = lds + s % STAGES * kStageBytes;
+                if (n < FJ)
+                    fb[n] = B::fragment(stage + kLoadsA * kLoadBytes, wj + n * 16, h);
+                else if (n < FJ + FI)
+                    fa[n - FJ] = A::fragment(stage, wi + (n - FJ) * 16, h);
+            };
+            constexpr int kReads = FI + FJ, kAt = (FI + 3) / 4 - 1;  // the barrier: after this row of the second half
+            constexpr int kPer = (kReads + FI - 1) / FI, kPerNext = (kReads + FI - 2 - kAt) / (FI - 1 - kAt);
 #pragma unroll
-            for (int s = 0; s < STAGES - 1; ++s)
+            for (int s = 0; s < STAGES; ++s)
                 fetch(s0 + s);
-        } else {
-            fetch(s0);
-            commit(s0);
-        }
-        for (int s = s0; s < s1; ++s) {
-            if constexpr (DIRECT) {
-                wait_loads<(STAGES - 2) * kLoads>();
-                __builtin_amdgcn_s_barrier();
-                fetch(s + STAGES - 1);
-            } else {
-                __syncthreads();
-                fetch(s + 1);
-            }
-            const char *stage = lds + s % STAGES * kStageBytes;
-            const char *sa = stage + wave_i() * kRowBytes, *sb = stage + (kLoadsA * kRows + wave_j()) * kRowBytes;
+            wait_loads<(STAGES - 1) * kLoads>();
+            __builtin_amdgcn_s_barrier();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int at = h ? at1 : at0;
-                u32x4 a[FI], b[FJ];
+            for (int n = 0; n < kReads; ++n)
+                read(s0, 0, a0, b0, n);
+            for (int s = s0; s < s1; ++s) {
 #pragma unroll
-                for (int i = 0; i < FI; ++i)
-                    a[i] = *reinterpret_cast<const u32x4 *>(sa + at + i * 16 * kRowBytes);
+                for (int i = 0; i < FI; ++i) {
 #pragma unroll
-                for (int j = 0; j < FJ; ++j)
-                    b[j] = *reinterpret_cast<const u32x4 *>(sb + at + j * 16 * kRowBytes);
+                    for (int j = 0; j < FJ; ++j)
+                        multiply(a0[i], b0[j], acc.c[i][j]);
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < FI; ++i)
+                    for (int n = 0; n < kPer; ++n)
+                        read(s, 1, a1, b1, i * kPer + n);
+                }
 #pragma unroll
-                    for (int j = 0; j < FJ; ++j) {
-                        if constexpr (BF16) {
-                            acc.c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                __builtin_bit_cast(bf16x8, a[i]), __builtin_bit_cast(bf16x8, b[j]), acc.c[i][j], 0, 0, 0);
-                        } else {
+                for (int i = 0; i < FI; ++i) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc.c[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                                    __uint_as_float(a[i][e]), __uint_as_float(b[j][e]), acc.c[i][j], 0, 0, 0);
-                        }
+                    for (int j = 0; j < FJ; ++j)
+                        multiply(a1[i], b1[j], acc.c[i][j]);
+                    if (i == kAt) {
+                        wait_loads<(STAGES - 2) * kLoads>();
+                        __builtin_amdgcn_s_barrier();
+                        fetch(s + STAGES);
                     }
+                    if (i >= kAt) {
+#pragma unroll
+                        for (int n = 0; n < kPerNext; ++n)
+                            read(s + 1, 0, a0, b0, (i - kAt) * kPerNext + n);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
-            if constexpr (!DIRECT)
+        } else {
+            u32x4 ha[kLoadsA], hb[kLoadsB];
+            auto commit = [&](int s) {
+                char *to = lds + s % STAGES * kStageBytes + wave * 1024 + lane * 16;
+#pragma unroll
+                for (int l = 0; l < kLoadsA; ++l)
+                    *reinterpret_cast<u32x4 *>(to + l * kLoadBytes) = ha[l];
+#pragma unroll
+                for (int l = 0; l < kLoadsB; ++l)
+                    *reinterpret_cast<u32x4 *>(to + (kLoadsA + l) * kLoadBytes) = hb[l];
+            };
+            a.hold(s0, s0 < s1, ha);
+            b.hold(s0, s0 < s1, hb);
+            commit(s0);
+            for (int s = s0; s < s1; ++s) {
+                __syncthreads();
+                a.hold(s + 1, s + 1 < s1, ha);
+                b.hold(s + 1, s + 1 < s1, hb);
+                const char *stage = lds + s % STAGES * kStageBytes;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    u32x4 fa[FI], fb[FJ];
+#pragma unroll
+                    for (int i = 0; i < FI; ++i)
+                        fa[i] = A::fragment(stage, wi + i * 16, h);
+#pragma unroll
+                    for (int j = 0; j < FJ; ++j)
+                        fb[j] = B::fragment(stage + kLoadsA * kLoadBytes, wj + j * 16, h);
+#pragma unroll
+                    for (int i = 0; i < FI; ++i)
+#pragma unroll
+                        for (int j = 0; j < FJ; ++j)
+                            multiply(fa[i], fb[j], acc.c[i][j]);
+                }
                 commit(s + 1);
+            }
         }
         // the loads past s1 have written zeros: LDS is free after this
         wait_loads<0>();

@@ -253,8 +253,8 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a)
     a.row[j] = used ? float2{a.lse[j] * kLog2e, a.grad[j] * a.scale} : float2{0.0f, 0.0f};
 }
 
-// A tile in the element type, [TJ][TI] with 4 bytes after each row: column
-// reads of eight rows at a time then fall on different banks.
+// A tile in the element type, [TJ][TI] with 4 bytes after each row: sixteen
+// rows that are written at once then start on different banks.
 template <typename T>
 struct Staged {
     static constexpr int kStride = T::TI * T::kEs + 4;
@@ -286,29 +286,6 @@ struct Staged {
             store_chunk<T::kEs>(out + j * stride + c * 16, u32x4{from[0], from[1], from[2], from[3]}, left);
         }
     }
-
-    // Transposed: results i < ni, rows j < nj (a multiple of 16 bytes) to out[i][j].
-    __device__ static void store_columns(const char *lds, char *out, int64_t stride, int nj, int ni)
-    {
-        constexpr int kPer = 16 / T::kEs, kChunks = T::TJ / kPer, kWide = kChunks < 8 ? kChunks : 8;
-        // eight chunks of j by eight i at a time: whole 128-byte lines, all banks
-        for (int t = threadIdx.x; t < T::TI * kChunks; t += T::kThreads) {
-            const int i = t / kWide % T::TI, c = t % kWide + t / (kWide * T::TI) * kWide;
-            if (i >= ni || c * kPer >= nj)
-                continue;
-            u32x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const char *from = lds + c * kPer * kStride + i * T::kEs;
-                if constexpr (T::kEs == 2)
-                    v[e] = *reinterpret_cast<const unsigned short *>(from + 2 * e * kStride) |
-                           unsigned(*reinterpret_cast<const unsigned short *>(from + (2 * e + 1) * kStride)) << 16;
-                else
-                    v[e] = *reinterpret_cast<const unsigned *>(from + e * kStride);
-            }
-            *reinterpret_cast<u32x4 *>(out + i * stride + c * 16) = v;
-        }
-    }
 };
 
 template <typename T>
@@ -316,9 +293,9 @@ constexpr int staged_lds = T::kLdsBytes > Staged<T>::kBytes ? T::kLdsBytes : Sta
 
 __device__ __forceinline__ int round64(int n) { return (n + 63) / 64 * 64; }
 
-// dz = coefficient * exp(z - lse), zero past the piece and past the rows up to
-// the next multiple of 64.  bf16 keeps dz at 8 bits for the products: each
-// gradient sums many of these roundings, which leaves it within its own.
+// dz = coefficient * exp(z - lse), zero past the piece up to the next multiple
+// of 64.  bf16 keeps dz at 8 bits for the products: each gradient sums many of
+// these roundings, which leaves it within its own.
 template <typename T>
 __global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, int tiles_j)
 {
@@ -347,11 +324,9 @@ __global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, 
         }
     }
     __syncthreads();
-    const int left_i = round64(a.p.ni) - i0, left_j = round64(a.p.nj) - j0;
+    const int left_i = round64(a.p.ni) - i0;
     Staged<T>::store_rows(lds, static_cast<char *>(a.dz) + (j0 * a.ldz + i0) * T::kEs, a.ldz * T::kEs,
                           a.p.nj - j0 < T::TJ ? a.p.nj - j0 : T::TJ, left_i < T::TI ? left_i : T::TI);
-    Staged<T>::store_columns(lds, static_cast<char *>(a.dzt) + (i0 * a.ldt + j0) * T::kEs, a.ldt * T::kEs,
-                             left_j < T::TJ ? left_j : T::TJ, a.p.ni - i0 < T::TI ? a.p.ni - i0 : T::TI);
 }
 
 // One thread per entry.  Equal entries of a row write the same value.
@@ -374,27 +349,19 @@ __global__ __launch_bounds__(kThreads) void targets_kernel(TargetArgs a)
     }
     const float d = row.y == 0.0f ? 0.0f : row.y * (__builtin_amdgcn_exp2f(__builtin_fmaf(a.logit[n], kLog2e, -row.x)) - p);
     store<BF16>(a.dz, j * a.ldz + i, d);
-    store<BF16>(a.dzt, i * a.ldt + j, d);
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void transpose_kernel(TransposeArgs a)
+// One wave per row at a time.
+template <int ES>
+__global__ __launch_bounds__(kThreads) void align_kernel(AlignArgs a)
 {
-    __shared__ T tile[64][65];
-    const int64_t tall = (a.rows + 63) / 64, all = tall * ((a.cols + 63) / 64);
-    for (int64_t b = blockIdx.x; b < all; b += gridDim.x) {
-    const int64_t r0 = b % tall * 64, c0 = b / tall * 64;
-    for (int t = threadIdx.x; t < 64 * 64; t += kThreads) {
-        const int r = t / 64, c = t % 64;
-        tile[r][c] = r0 + r < a.rows && c0 + c < a.cols ? static_cast<const T *>(a.in)[(r0 + r) * a.ldi + c0 + c] : T(0);
-    }
-    __syncthreads();
-    for (int t = threadIdx.x; t < 64 * 64; t += kThreads) {
-        const int c = t / 64, r = t % 64;
-        if (c0 + c < a.cols)
-            static_cast<T *>(a.out)[(c0 + c) * a.ldo + r0 + r] = tile[r][c];
-    }
-    __syncthreads();
+    const int lane = threadIdx.x % 64, bytes = a.cols * ES;
+    const int64_t waves = int64_t(gridDim.x) * (kThreads / 64);
+    for (int64_t r = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64; r < a.rows; r += waves) {
+        const char *from = static_cast<const char *>(a.in) + r * bytes;
+        char *to = static_cast<char *>(a.out) + r * a.ldo * ES;
+        for (int c = lane * 16; c < bytes; c += 64 * 16)
+            *reinterpret_cast<u32x4 *>(to + c) = load_chunk<ES>(from + c, bytes - c);
     }
 }
 
@@ -481,42 +448,43 @@ Shape shape_of(const Product &p)
 // Both operands in 16-byte chunks.
 bool direct(const Product &p)
 {
-    const int64_t es = p.bf16 ? 2 : 4;
-    return (reinterpret_cast<uintptr_t>(p.a) | reinterpret_cast<uintptr_t>(p.b) | uintptr_t(p.lda * es) |
-            uintptr_t(p.ldb * es) | uintptr_t(p.nk * es)) % 16 == 0;
+    const int es = p.bf16 ? 2 : 4;
+    return in_chunks(p.a, p.lda, es) && in_chunks(p.b, p.ldb, es) && p.nk * int64_t(es) % 16 == 0;
 }
 
-template <bool BF16, bool DIRECT> using Rows16 = Tile<BF16, 128, 16, 4, 1, DIRECT ? 4 : 2, DIRECT>;
-template <bool BF16, bool DIRECT> using Rows32 = Tile<BF16, 128, 32, 4, 1, DIRECT ? 4 : 2, DIRECT>;
-template <bool BF16, bool DIRECT> using Rows64 = Tile<BF16, 128, 64, 4, 1, DIRECT ? 3 : 2, DIRECT>;
-template <bool BF16, bool DIRECT> using Mid = Tile<BF16, 128, 128, 2, 2, 2, DIRECT>;
-template <bool BF16, bool DIRECT> using Big = Tile<BF16, 256, 256, 2, 4, 2, DIRECT>;
+template <bool BF16, int TJ, int STAGES, bool DIRECT, bool TALL> using Rows = Tile<BF16, 128, TJ, 4, 1, DIRECT ? STAGES : 2, DIRECT, TALL, false>;
+template <bool BF16, bool DIRECT, bool TA, bool TB> using Mid = Tile<BF16, 128, 128, 2, 2, 2, DIRECT, TA, TB>;
+template <bool BF16, bool DIRECT, bool TA, bool TB> using Big = Tile<BF16, 256, 256, 2, 4, 2, DIRECT, TA, TB>;
 
 int tiles(int n, int per) { return n / per + (n % per != 0); }
 
-// f(tile type) for the product's tile.
-template <bool BF16, bool DIRECT, typename F>
+// f(tile type) for the product's tile.  A tall B keeps to the wide ones.
+template <bool BF16, bool DIRECT, bool TA, bool TB, typename F>
 hipError_t with_shape(Shape s, F f)
 {
-    switch (s) {
-    case kRows16: return f(Rows16<BF16, DIRECT>{});
-    case kRows32: return f(Rows32<BF16, DIRECT>{});
-    case kRows64: return f(Rows64<BF16, DIRECT>{});
-    case kBig:
-        if constexpr (BF16)
-            return f(Big<BF16, DIRECT>{});
-    default: return f(Mid<BF16, DIRECT>{});
+    if constexpr (!TB) {
+        switch (s) {
+        case kRows16: return f(Rows<BF16, 16, 4, DIRECT, TA>{});
+        case kRows32: return f(Rows<BF16, 32, 4, DIRECT, TA>{});
+        case kRows64: return f(Rows<BF16, 64, 3, DIRECT, TA>{});
+        default: break;
+        }
     }
+    if constexpr (BF16)
+        if (s == kBig)
+            return f(Big<BF16, DIRECT, TA, TB>{});
+    return f(Mid<BF16, DIRECT, TA, TB>{});
 }
 
-template <bool ALWAYS_DIRECT, typename F>
-hipError_t with_tile(const Product &p, F f)
+// The logits' tile; operands at any element alignment, or (ALIGNED) in 16-byte chunks.
+template <bool ALIGNED, typename F>
+hipError_t with_logits_tile(const Product &p, F f)
 {
     const Shape s = shape_of(p);
-    if (ALWAYS_DIRECT || direct(p))
-        return p.bf16 ? with_shape<true, true>(s, f) : with_shape<false, true>(s, f);
-    if constexpr (!ALWAYS_DIRECT)
-        return p.bf16 ? with_shape<true, false>(s, f) : with_shape<false, false>(s, f);
+    if (ALIGNED || direct(p))
+        return p.bf16 ? with_shape<true, true, false, false>(s, f) : with_shape<false, true, false, false>(s, f);
+    if constexpr (!ALIGNED)
+        return p.bf16 ? with_shape<true, false, false, false>(s, f) : with_shape<false, false, false, false>(s, f);
     return hipErrorInvalidValue;
 }
 
@@ -535,7 +503,7 @@ hipError_t launch_stats(const Op &op, hipStream_t stream)
 {
     const StatsArgs a = op.get<StatsArgs>();
     (void)hipGetLastError();
-    return with_tile<false>(a.p, [&](auto t) {
+    return with_logits_tile<false>(a.p, [&](auto t) {
         using T = decltype(t);
         const int ti = tiles(a.p.ni, T::TI), tj = tiles(a.p.nj, T::TJ);
         stats_kernel<T><<<dim3(unsigned(ti) * unsigned(tj)), dim3(T::kThreads), 0, stream>>>(a, ti, tj);
@@ -585,7 +553,7 @@ hipError_t launch_dz(const Op &op, hipStream_t stream)
 {
     const DzArgs a = op.get<DzArgs>();
     (void)hipGetLastError();
-    return with_tile<false>(a.p, [&](auto t) {
+    return with_logits_tile<true>(a.p, [&](auto t) {
         using T = decltype(t);
         const int ti = tiles(a.p.ni, T::TI), tj = tiles(a.p.nj, T::TJ);
         dz_kernel<T><<<dim3(unsigned(ti) * unsigned(tj)), dim3(T::kThreads), 0, stream>>>(a, ti, tj);
@@ -602,14 +570,14 @@ hipError_t launch_targets(const Op &op, hipStream_t stream)
     RR_LAUNCH(targets_kernel<false>, grid, a);
 }
 
-hipError_t launch_transpose(const Op &op, hipStream_t stream)
+hipError_t launch_align(const Op &op, hipStream_t stream)
 {
-    const TransposeArgs a = op.get<TransposeArgs>();
-    const int64_t all = ((a.rows + 63) / 64) * int64_t((a.cols + 63) / 64);
-    const dim3 grid(unsigned(all < 65536 ? all : 65536));
+    const AlignArgs a = op.get<AlignArgs>();
+    const unsigned all = blocks(a.rows, kThreads / 64);
+    const dim3 grid(all < 8192u ? all : 8192u);
     if (a.bf16)
-        RR_LAUNCH(transpose_kernel<unsigned short>, grid, a);
-    RR_LAUNCH(transpose_kernel<unsigned>, grid, a);
+        RR_LAUNCH(align_kernel<2>, grid, a);
+    RR_LAUNCH(align_kernel<4>, grid, a);
 }
 
 // Parts of k, so that a product of few tiles still fills the compute units.
@@ -626,12 +594,16 @@ hipError_t launch_store(const Op &op, hipStream_t stream)
 {
     const StoreArgs a = op.get<StoreArgs>();
     (void)hipGetLastError();
-    return with_tile<true>(a.p, [&](auto t) {
+    const auto go = [&](auto t) {
         using T = decltype(t);
         const int ti = tiles(a.p.ni, T::TI), tj = tiles(a.p.nj, T::TJ);
         store_kernel<T><<<dim3(unsigned(ti) * unsigned(tj) * unsigned(a.splits)), dim3(T::kThreads), 0, stream>>>(a, ti, tj);
         return hipGetLastError();
-    });
+    };
+    const Shape s = shape_of(a.p);
+    if (a.tall_b)
+        return a.p.bf16 ? with_shape<true, true, true, true>(s, go) : with_shape<false, true, true, true>(s, go);
+    return a.p.bf16 ? with_shape<true, true, true, false>(s, go) : with_shape<false, true, true, false>(s, go);
 }
 
 hipError_t launch_gather(const Op &op, hipStream_t stream)
