@@ -129,8 +129,8 @@ struct Tile {
     static constexpr int kLdsBytes = STAGES * kStageBytes;
     static_assert(TI % kRows == 0 && FI * WI * 16 == TI && FJ * WJ * 16 == TJ, "");
     static_assert(DIRECT || !(TALL_A || TALL_B), "");
-    static_assert(!TALL_A || TI >= 128, "a tall row has to hold the swizzle");
-    static_assert(!TALL_B || (TJ >= 128 && TJ % kRows == 0), "");
+    static_assert(!TALL_A || TI * kEs >= 256, "a tall row has to hold the swizzle");
+    static_assert(!TALL_B || (TJ * kEs >= 256 && TJ % kRows == 0), "");
 
     struct Acc {
         f32x4 c[FI][FJ];

@@ -8,6 +8,8 @@
 // and over the four lane groups of a wave.
 #include "rr_product.h"
 
+#include <math.h>
+
 namespace rr {
 namespace {
 
@@ -427,22 +429,56 @@ unsigned blocks(int64_t n, int64_t per) { return unsigned((n + per - 1) / per); 
 
 namespace {
 
-// Tiles of a product, by its rows j (the rows of x, mostly).  Up to 64 rows
-// the vocabulary streams past them and a narrow tile wastes least; 256 x 256
-// tiles reuse an operand most, but need enough of them for the 256 compute
-// units; fp32 tiles of that size would not fit LDS when staged.
 enum Shape { kRows16, kRows32, kRows64, kMid, kBig };
 
-Shape shape_of(const Product &p)
+int tiles(int n, int per) { return n / per + (n % per != 0); }
+
+struct Form {
+    Shape shape;
+    int32_t splits;  // parts of k
+};
+
+// Tiles and parts of a product by the time that they would take: the busiest of
+// 256 compute units has so many tiles, at the rate that a tile's shape reached
+// against the largest (4096 x 2048 x 32768 in bf16: 1010 TFLOP/s, 0.75 and 0.64
+// of it at 128 x 128 and 128 x 64; 2048 x 1024 x 16384 in fp32: 116 TFLOP/s at
+// 128 x 128, 0.93 and 0.83 of it at 128 x 64 and 128 x 32).  A workgroup of the
+// smaller ones alone on its unit does not fill it.  In units of a
+// multiplication of a compute unit at that rate; a part of k costs the writing
+// and reading of its sums, about 5 (bf16) or 0.5 (fp32) for each.  Up to 64
+// rows the narrowest tile that holds them streams the vocabulary past them.
+Form form_of(const Product &p, bool may_split, bool tall_b)
 {
-    if (p.nj <= 16)
-        return kRows16;
-    if (p.nj <= 32)
-        return kRows32;
-    if (p.nj <= 64)
-        return kRows64;
-    const int64_t big = ((p.ni + 255) / 256) * int64_t((p.nj + 255) / 256);
-    return p.bf16 && big >= 192 ? kBig : kMid;
+    static const struct {
+        Shape shape;
+        int ti, tj;
+        double bf16, fp32;
+    } all[] = {{kRows16, 128, 16, 0.3, 0.6}, {kRows32, 128, 32, 0.46, 0.83}, {kRows64, 128, 64, 0.64, 0.93},
+               {kMid, 128, 128, 0.75, 1.0}, {kBig, 256, 256, 1.0, 0.0}};
+    Form best{kMid, 1};
+    double least = INFINITY;
+    const int steps = tiles(p.nk, p.bf16 ? 64 : 32), most = may_split ? (steps / 4 < 64 ? steps / 4 : 64) : 1;
+    for (const auto &f : all) {
+        const double rate = p.bf16 ? f.bf16 : f.fp32;
+        if (rate == 0.0 || (tall_b && f.tj < (p.bf16 ? 128 : 64)))
+            continue;
+        // rows that fit a narrow tile
+        if (!tall_b && p.nj <= 64 && (f.tj < p.nj || f.tj > 64 || f.tj >= 2 * p.nj + 16))
+            continue;
+        if (!tall_b && p.nj > 64 && f.tj < (p.bf16 ? 64 : 32))
+            continue;
+        const double n = double(tiles(p.ni, f.ti)) * tiles(p.nj, f.tj);
+        for (int s = 1; s <= (most < 1 ? 1 : most); ++s) {
+            const double busy = ceil(n * s / 256);
+            const double time = (busy == 1 && f.shape != kBig ? 1.6 : busy) * f.ti * f.tj / rate * (double(p.nk) / s + 256) +
+                                (may_split ? (p.bf16 ? 5.0 : 0.5) * s * p.ni * p.nj : 0.0);
+            if (time < least) {
+                least = time;
+                best = Form{f.shape, s};
+            }
+        }
+    }
+    return best;
 }
 
 // Both operands in 16-byte chunks.
@@ -452,24 +488,24 @@ bool direct(const Product &p)
     return in_chunks(p.a, p.lda, es) && in_chunks(p.b, p.ldb, es) && p.nk * int64_t(es) % 16 == 0;
 }
 
-template <bool BF16, int TJ, int STAGES, bool DIRECT, bool TALL> using Rows = Tile<BF16, 128, TJ, 4, 1, DIRECT ? STAGES : 2, DIRECT, TALL, false>;
+template <bool BF16, int TJ, int STAGES, bool DIRECT, bool TA, bool TB>
+using Rows = Tile<BF16, 128, TJ, 4, 1, DIRECT ? STAGES : 2, DIRECT, TA, TB>;
 template <bool BF16, bool DIRECT, bool TA, bool TB> using Mid = Tile<BF16, 128, 128, 2, 2, 2, DIRECT, TA, TB>;
 template <bool BF16, bool DIRECT, bool TA, bool TB> using Big = Tile<BF16, 256, 256, 2, 4, 2, DIRECT, TA, TB>;
 
-int tiles(int n, int per) { return n / per + (n % per != 0); }
-
-// f(tile type) for the product's tile.  A tall B keeps to the wide ones.
+// f(tile type).
 template <bool BF16, bool DIRECT, bool TA, bool TB, typename F>
 hipError_t with_shape(Shape s, F f)
 {
     if constexpr (!TB) {
-        switch (s) {
-        case kRows16: return f(Rows<BF16, 16, 4, DIRECT, TA>{});
-        case kRows32: return f(Rows<BF16, 32, 4, DIRECT, TA>{});
-        case kRows64: return f(Rows<BF16, 64, 3, DIRECT, TA>{});
-        default: break;
-        }
+        if (s == kRows16)
+            return f(Rows<BF16, 16, 4, DIRECT, TA, TB>{});
+        if (s == kRows32)
+            return f(Rows<BF16, 32, 4, DIRECT, TA, TB>{});
     }
+    if constexpr (!(TB && BF16))
+        if (s == kRows64)
+            return f(Rows<BF16, 64, 3, DIRECT, TA, TB>{});
     if constexpr (BF16)
         if (s == kBig)
             return f(Big<BF16, DIRECT, TA, TB>{});
@@ -480,7 +516,7 @@ hipError_t with_shape(Shape s, F f)
 template <bool ALIGNED, typename F>
 hipError_t with_logits_tile(const Product &p, F f)
 {
-    const Shape s = shape_of(p);
+    const Shape s = form_of(p, false, false).shape;
     if (ALIGNED || direct(p))
         return p.bf16 ? with_shape<true, true, false, false>(s, f) : with_shape<false, true, false, false>(s, f);
     if constexpr (!ALIGNED)
@@ -492,7 +528,7 @@ hipError_t with_logits_tile(const Product &p, F f)
 
 int64_t stats_parts(const Product &p)
 {
-    switch (shape_of(p)) {
+    switch (form_of(p, false, false).shape) {
     case kRows16: case kRows32: case kRows64: return int64_t(tiles(p.ni, 128)) * 4;
     case kMid: return int64_t(tiles(p.ni, 128)) * 2;
     default: return int64_t(tiles(p.ni, 256)) * 2;
@@ -580,15 +616,7 @@ hipError_t launch_align(const Op &op, hipStream_t stream)
     RR_LAUNCH(align_kernel<4>, grid, a);
 }
 
-// Parts of k, so that a product of few tiles still fills the compute units.
-int32_t product_splits(const Product &p)
-{
-    const Shape s = shape_of(p);
-    const int64_t all = s == kBig ? int64_t(tiles(p.ni, 256)) * tiles(p.nj, 256)
-                                  : int64_t(tiles(p.ni, 128)) * tiles(p.nj, s == kMid ? 128 : 64);
-    const int64_t steps = tiles(p.nk, p.bf16 ? 64 : 32), fill = (s == kBig ? 256 : 512) / (all ? all : 1);
-    return int32_t(fill < 1 ? 1 : fill > steps / 4 ? (steps / 4 ? steps / 4 : 1) : fill);
-}
+int32_t product_splits(const Product &p) { return form_of(p, true, false).splits; }
 
 hipError_t launch_store(const Op &op, hipStream_t stream)
 {
@@ -600,7 +628,7 @@ hipError_t launch_store(const Op &op, hipStream_t stream)
         store_kernel<T><<<dim3(unsigned(ti) * unsigned(tj) * unsigned(a.splits)), dim3(T::kThreads), 0, stream>>>(a, ti, tj);
         return hipGetLastError();
     };
-    const Shape s = shape_of(a.p);
+    const Shape s = form_of(a.p, !a.tall_b, a.tall_b).shape;
     if (a.tall_b)
         return a.p.bf16 ? with_shape<true, true, true, true>(s, go) : with_shape<false, true, true, true>(s, go);
     return a.p.bf16 ? with_shape<true, true, true, false>(s, go) : with_shape<false, true, true, false>(s, go);
