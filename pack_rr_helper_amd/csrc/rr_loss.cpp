@@ -363,11 +363,12 @@ rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *
     if (rows == 0) {
         // no row contributes: dw is zero
         if (v->vocab > 0)
-            l.add(launch_gather, GatherArgs{nullptr, dw, v->vocab, 0, dim, 0, bf16});
+            l.add(launch_gather, GatherArgs{nullptr, dw, v->vocab, s.lda, dim, 0, bf16});
         return l.finish();
     }
-    if (v->vocab > 0)
-        l.add(launch_rows, RowsArgs{index, lse, prob, grad, n, v->topk, v->total, v->scale, s.row});
+    const RowsArgs of_rows{index, lse, prob, grad, n, v->topk, v->total, v->scale, s.row};
+    if (v->vocab > 0 && prob)
+        l.add(launch_rows, of_rows);
     const bool copy_x = !in_chunks(x, dim, es), copy_w = !in_chunks(w, dim, es);
     const bool whole = s.pieces == 1 && s.splits == 1;  // dx is one product
     const void *xc = copy_x ? s.x : x;
@@ -382,8 +383,9 @@ rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *
             l.add(launch_align, AlignArgs{wc, s.w, c, s.ldd, dim, bf16});
             wc = s.w;
         }
-        l.add(launch_dz, DzArgs{Product{wc, xc, ldw, ldx, c, n, dim, bf16}, v->scale, s.row, s.dz, s.ldv});
-        l.add(launch_targets, TargetArgs{index, logit, prob, s.row, n, v->topk, c, bf16, v->first + v0, s.dz, s.ldv});
+        l.add(launch_dz, DzArgs{Product{wc, xc, ldw, ldx, c, n, dim, bf16}, of_rows, logit, v->first + v0, s.dz, s.ldv});
+        if (prob)
+            l.add(launch_targets, TargetArgs{index, logit, prob, s.row, n, v->topk, c, bf16, v->first + v0, s.dz, s.ldv});
         l.add(launch_store, StoreArgs{Product{xc, s.dz, ldx, s.ldv, dim, c, n, bf16}, dwp, dim, nullptr, 0, 1, 0, 1});
         l.add(launch_store, StoreArgs{Product{wc, s.dz, ldw, s.ldv, dim, n, c, bf16}, whole ? dx : nullptr, dim,
                                       whole ? nullptr : s.acc, s.lda, s.splits, v0 > 0, 0});

@@ -100,29 +100,31 @@ struct CombineArgs {
 hipError_t launch_cross_entropy(const Op &, hipStream_t);
 hipError_t launch_distill(const Op &, hipStream_t);
 
-// Per row: lse in units of ln 2 and grad * scale, or zeros for a row without a target.
+// What makes a row's (lse in units of ln 2, grad * scale), zeros for a row
+// without a target; of distillation, row is filled with them first.
 struct RowsArgs {
     const int64_t *index;
-    const float *lse, *prob, *grad;
+    const float *lse, *prob, *grad;  // prob: null for cross entropy
     int32_t rows, topk;
     int64_t total;
     float scale;
-    float2 *row;         // (lse, coefficient)
+    float2 *row;
 };
 hipError_t launch_rows(const Op &, hipStream_t);
 
-// dz of one piece of the vocabulary without its targets.  Operands in 16-byte
-// chunks.
+// dz of one piece of the vocabulary; of distillation without its targets.
+// Operands in 16-byte chunks.
 struct DzArgs {
     Product p;           // a = the piece of w, b = x
-    float scale;
-    const float2 *row;
+    RowsArgs rows;
+    const float *logit;
+    int64_t first;       // the piece's first entry of the vocabulary
     void *dz;            // [nj][ldz]
     int64_t ldz;
 };
 hipError_t launch_dz(const Op &, hipStream_t);
 
-// dz at the targets of one piece.
+// dz at the targets of one piece, for distillation.
 struct TargetArgs {
     const int64_t *index;
     const float *logit, *prob;

@@ -57,35 +57,49 @@ __global__ __launch_bounds__(T::kThreads) void stats_kernel(StatsArgs a, int til
     const int i0 = ti * T::TI, j0 = tj * T::TJ;
     typename T::Acc acc;
     T::run(a.p, i0, j0, 0, (a.p.nk + T::kStep - 1) / T::kStep, lds, acc);
-    const bool full = i0 + T::TI <= a.p.ni;
     const int part = ti * (T::TI / (T::FI * 16)) + T::wave_i() / (T::FI * 16);
+    // z = scale * acc; the largest is at the largest of acc once scale is positive
+    const float scale = fabsf(a.scale), c = scale * kLog2e;
+    if (a.scale < 0.0f) {
+#pragma unroll
+        for (int i = 0; i < T::FI; ++i)
+#pragma unroll
+            for (int j = 0; j < T::FJ; ++j)
+                acc.c[i][j] = -acc.c[i][j];
+    }
+    if (i0 + T::TI > a.p.ni) {
+#pragma unroll
+        for (int i = 0; i < T::FI; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i0 + T::lane_i(i) + e >= a.p.ni) {
+#pragma unroll
+                    for (int j = 0; j < T::FJ; ++j)
+                        acc.c[i][j][e] = -INFINITY;
+                }
+    }
 #pragma unroll
     for (int j = 0; j < T::FJ; ++j) {
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < T::FI; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float z = acc.c[i][j][e] * a.scale;
-                if (!full && i0 + T::lane_i(i) + e >= a.p.ni)
-                    z = -INFINITY;
-                acc.c[i][j][e] = z;
-                top = fmaxf(top, z);
-            }
+            for (int e = 0; e < 4; ++e)
+                top = fmaxf(top, acc.c[i][j][e]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float base = top == -INFINITY ? 0.0f : top * -kLog2e;
+        const float base = top == -INFINITY ? 0.0f : -(top * c);
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < T::FI; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc.c[i][j][e], kLog2e, base));
+                sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc.c[i][j][e], c, base));
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
         const int row = j0 + T::lane_j(j);
         if (threadIdx.x % 64 < 16 && row < a.p.nj)
-            a.part[int64_t(part) * a.p.nj + row] = float2{top, sum};
+            a.part[int64_t(part) * a.p.nj + row] = float2{top == -INFINITY ? top : top * scale, sum};
     }
 }
 
@@ -112,8 +126,8 @@ __device__ __forceinline__ float wave_sum(float v)
 }
 
 // The first `joins` workgroups join the parts of `wide` rows each (a power of
-// two up to 64), the others compute the logits of one entry per wave.
-template <bool BF16>
+// two up to 64), the others compute the logits of kPicks entries per wave.
+template <bool BF16, int kPicks>
 __global__ __launch_bounds__(kThreads) void stats_done_kernel(StatsDoneArgs a, int joins, int wide)
 {
     __shared__ float2 sums[kThreads];
@@ -143,31 +157,52 @@ __global__ __launch_bounds__(kThreads) void stats_done_kernel(StatsDoneArgs a, i
             a.stats[row] = sums[threadIdx.x];
         return;
     }
+    constexpr int kEs = BF16 ? 2 : 4, kPer = 16 / kEs;
     const int lane = threadIdx.x % 64;
     const int64_t entries = int64_t(a.rows) * a.topk, waves = int64_t(gridDim.x - joins) * (kThreads / 64);
-    for (int64_t n = (int64_t(blockIdx.x) - joins) * (kThreads / 64) + threadIdx.x / 64; n < entries; n += waves) {
-        const int64_t i = a.index[n] - a.first;
-        float z = 0.0f;
-        if (i >= 0 && i < a.vocab) {
-            constexpr int kEs = BF16 ? 2 : 4, kPer = 16 / kEs;
-            const char *x = static_cast<const char *>(a.x) + n / a.topk * a.dim * kEs;
-            const char *w = static_cast<const char *>(a.w) + i * a.dim * kEs;
-            for (int k = lane * kPer; k < a.dim; k += 64 * kPer) {
-                const u32x4 u = load_chunk<kEs>(x + k * kEs, (a.dim - k) * kEs), v = load_chunk<kEs>(w + k * kEs, (a.dim - k) * kEs);
+    for (int64_t n0 = ((int64_t(blockIdx.x) - joins) * (kThreads / 64) + threadIdx.x / 64) * kPicks; n0 < entries; n0 += waves * kPicks) {
+        // loads of all of them under way together; one that is not held here reads row 0
+        const char *x[kPicks], *w[kPicks];
+        bool held[kPicks];
+        float z[kPicks];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (BF16) {
-                        z = __builtin_fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), z);
-                        z = __builtin_fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(v[e] & 0xffff0000u), z);
-                    } else {
-                        z = __builtin_fmaf(__uint_as_float(u[e]), __uint_as_float(v[e]), z);
-                    }
-                }
-            }
-            z = wave_sum(z) * a.scale;
+        for (int m = 0; m < kPicks; ++m) {
+            const int64_t n = n0 + m < entries ? n0 + m : entries - 1, i = a.index[n] - a.first;
+            held[m] = i >= 0 && i < a.vocab;
+            x[m] = static_cast<const char *>(a.x) + n / a.topk * a.dim * kEs;
+            w[m] = static_cast<const char *>(a.w) + (held[m] ? i : 0) * a.dim * kEs;
+            z[m] = 0.0f;
         }
-        if (lane == 0)
-            a.picked[n] = z;
+        bool any = false;
+#pragma unroll
+        for (int m = 0; m < kPicks; ++m)
+            any |= held[m];
+        if (any)
+            for (int k = lane * kPer; k < a.dim; k += 64 * kPer) {
+                u32x4 u[kPicks], v[kPicks];
+#pragma unroll
+                for (int m = 0; m < kPicks; ++m) {
+                    u[m] = load_chunk<kEs>(x[m] + k * kEs, (a.dim - k) * kEs);
+                    v[m] = load_chunk<kEs>(w[m] + k * kEs, (a.dim - k) * kEs);
+                }
+#pragma unroll
+                for (int m = 0; m < kPicks; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (BF16) {
+                            z[m] = __builtin_fmaf(__uint_as_float(u[m][e] << 16), __uint_as_float(v[m][e] << 16), z[m]);
+                            z[m] = __builtin_fmaf(__uint_as_float(u[m][e] & 0xffff0000u), __uint_as_float(v[m][e] & 0xffff0000u), z[m]);
+                        } else {
+                            z[m] = __builtin_fmaf(__uint_as_float(u[m][e]), __uint_as_float(v[m][e]), z[m]);
+                        }
+                    }
+            }
+#pragma unroll
+        for (int m = 0; m < kPicks; ++m) {
+            const float sum = wave_sum(z[m]) * a.scale;
+            if (lane == 0 && n0 + m < entries)
+                a.picked[n0 + m] = held[m] ? sum : 0.0f;
+        }
     }
 }
 
@@ -244,15 +279,24 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(CombineArgs a)
     }
 }
 
+// A row's lse in units of ln 2 and its coefficient of dz; zeros without a target.
+__device__ __forceinline__ float2 row_factors(const RowsArgs &a, int64_t j, bool used)
+{
+    return used ? float2{a.lse[j] * kLog2e, a.grad[j] * a.scale} : float2{0.0f, 0.0f};
+}
+
+// One wave per row.
 __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a)
 {
-    const int64_t j = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t j = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
     if (j >= a.rows)
         return;
     bool used = false;
-    for (int e = 0; e < a.topk; ++e)
-        used |= a.prob ? a.prob[j * a.topk + e] != 0.0f : counts(a.index[j * a.topk + e], a.total);
-    a.row[j] = used ? float2{a.lse[j] * kLog2e, a.grad[j] * a.scale} : float2{0.0f, 0.0f};
+    for (int e = threadIdx.x % 64; e < a.topk; e += 64)
+        used |= a.prob[j * a.topk + e] != 0.0f;
+    used = __ballot(used) != 0;
+    if (threadIdx.x % 64 == 0)
+        a.row[j] = row_factors(a, j, used);
 }
 
 // A tile in the element type, [TJ][TI] with 4 bytes after each row: sixteen
@@ -274,6 +318,11 @@ struct Staged {
             for (int e = 0; e < 4; ++e)
                 to[e] = __float_as_uint(v[e]);
         }
+    }
+
+    __device__ static void put_one(char *lds, int j, int i, float v)
+    {
+        store<T::kEs == 2>(lds + j * kStride, i, v);
     }
 
     // Rows j < nj, results i < ni to out[j][i].
@@ -308,22 +357,43 @@ __global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, 
     typename T::Acc acc;
     T::run(a.p, i0, j0, 0, (a.p.nk + T::kStep - 1) / T::kStep, lds, acc);
     const bool full = i0 + T::TI <= a.p.ni;
-    const float c = a.scale * kLog2e;
+    const float c = a.rows.scale * kLog2e;
 #pragma unroll
     for (int j = 0; j < T::FJ; ++j) {
         const int row = j0 + T::lane_j(j);
-        const float2 r = row < a.p.nj ? a.row[row] : float2{0.0f, 0.0f};
+        float2 r{0.0f, 0.0f};
+        int target = -1;   // cross entropy: within the wave's results
+        if (row < a.p.nj) {
+            if (a.rows.prob) {
+                r = a.rows.row[row];
+            } else {
+                const int64_t at = a.rows.index[row];
+                r = row_factors(a.rows, row, counts(at, a.rows.total));
+                if (at >= a.first + i0 && at < a.first + a.p.ni && at - a.first - i0 < T::TI)
+                    target = int(at - a.first) - i0 - T::wave_i();
+            }
+        }
+        // no dz in a row without a target, whatever its logits
+        if (r.y == 0.0f) {
+#pragma unroll
+            for (int i = 0; i < T::FI; ++i)
+                acc.c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
 #pragma unroll
         for (int i = 0; i < T::FI; ++i) {
             f32x4 d;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 d[e] = r.y * __builtin_amdgcn_exp2f(__builtin_fmaf(acc.c[i][j][e], c, -r.x));
-                if (r.y == 0.0f || (!full && i0 + T::lane_i(i) + e >= a.p.ni))
+                if (!full && i0 + T::lane_i(i) + e >= a.p.ni)
                     d[e] = 0.0f;
             }
             Staged<T>::put(lds, T::lane_j(j), T::lane_i(i), d);
         }
+        // the lane that holds the target has just written it
+        if (target >= 0 && target < T::FI * 16 && target % 16 / 4 == threadIdx.x % 64 / 16)
+            Staged<T>::put_one(lds, T::lane_j(j), T::wave_i() + target, r.y == 0.0f ? 0.0f :
+                r.y * (__builtin_amdgcn_exp2f(__builtin_fmaf(a.logit[row], kLog2e, -r.x)) - 1.0f));
     }
     __syncthreads();
     const int left_i = round64(a.p.ni) - i0;
@@ -331,26 +401,45 @@ __global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, 
                           a.p.nj - j0 < T::TJ ? a.p.nj - j0 : T::TJ, left_i < T::TI ? left_i : T::TI);
 }
 
-// One thread per entry.  Equal entries of a row write the same value.
+// One wave per row.  Equal entries of a row write the same value.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void targets_kernel(TargetArgs a)
 {
-    const int64_t n = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-    if (n >= int64_t(a.rows) * a.topk)
+    struct Entry {
+        int i;      // within the piece, or -1
+        float p;
+    };
+    __shared__ Entry of_row[kThreads / 64][RR_MAX_TOPK];
+    const int64_t j = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
+    const int lane = threadIdx.x % 64;
+    Entry *entry = of_row[threadIdx.x / 64];
+    if (j >= a.rows)
         return;
-    const int64_t at = a.index[n], i = at - a.first, j = n / a.topk;
-    if (i < 0 || i >= a.count)
-        return;
-    const float2 row = a.row[j];
-    float p = 1.0f;
-    if (a.prob) {
-        p = 0.0f;
-        for (int e = 0; e < a.topk; ++e)
-            if (a.index[j * a.topk + e] == at)
-                p += a.prob[j * a.topk + e];
+    bool any = false;
+    for (int e = lane; e < a.topk; e += 64) {
+        const int64_t i = a.index[j * a.topk + e] - a.first;
+        const bool in = i >= 0 && i < a.count;
+        entry[e] = Entry{in ? int(i) : -1, a.prob[j * a.topk + e]};
+        any |= in;
     }
-    const float d = row.y == 0.0f ? 0.0f : row.y * (__builtin_amdgcn_exp2f(__builtin_fmaf(a.logit[n], kLog2e, -row.x)) - p);
-    store<BF16>(a.dz, j * a.ldz + i, d);
+    if (!__ballot(any))
+        return;
+    // one wave's LDS operations keep their order; so has the compiler to
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const float2 row = a.row[j];
+    for (int e = lane; e < a.topk; e += 64) {
+        const int i = entry[e].i;
+        float p = 0.0f;
+#pragma unroll 8
+        for (int o = 0; o < a.topk; ++o)
+            p += entry[o].i == i ? entry[o].p : 0.0f;
+        if (i >= 0) {
+            const float z = a.logit[j * a.topk + e];
+            store<BF16>(a.dz, j * a.ldz + i,
+                        row.y == 0.0f ? 0.0f : row.y * (__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -row.x)) - p));
+        }
+    }
 }
 
 // One wave per row at a time.
@@ -403,16 +492,38 @@ __global__ __launch_bounds__(T::kThreads) void store_kernel(StoreArgs a, int til
                           a.p.nj - j0 < T::TJ ? a.p.nj - j0 : T::TJ, a.p.ni - i0 < T::TI ? a.p.ni - i0 : T::TI);
 }
 
-template <bool BF16>
+// Four columns of a row per PARTS threads, each of which takes its share of the
+// sums.
+template <bool BF16, int PARTS>
 __global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a)
 {
-    const int64_t n = a.rows * a.dim;
-    for (int64_t t = int64_t(blockIdx.x) * kThreads + threadIdx.x; t < n; t += int64_t(gridDim.x) * kThreads) {
-        const int64_t row = t / a.dim, at = row * a.lda + (t - row * a.dim);
-        float s = 0.0f;
-        for (int i = 0; i < a.splits; ++i)
-            s += a.acc[i * a.rows * a.lda + at];
-        store<BF16>(a.out, t, s);
+    constexpr int kWide = kThreads / PARTS;
+    __shared__ f32x4 sums[kThreads];
+    const int part = threadIdx.x / kWide;
+    const int64_t wide = a.lda / 4, n = a.rows * wide, stride = a.rows * a.lda;
+    for (int64_t t0 = int64_t(blockIdx.x) * kWide; t0 < n; t0 += int64_t(gridDim.x) * kWide) {
+        const int64_t t = t0 + threadIdx.x % kWide, row = t / wide;
+        const int col = int(t - row * wide) * 4;
+        f32x4 s{0.0f, 0.0f, 0.0f, 0.0f};
+        if (t < n) {
+#pragma unroll 8
+            for (int i = part; i < a.splits; i += PARTS)
+                s += *reinterpret_cast<const f32x4 *>(a.acc + i * stride + row * a.lda + col);
+        }
+        if constexpr (PARTS > 1) {
+            sums[threadIdx.x] = s;
+            __syncthreads();
+            if (part == 0)
+#pragma unroll
+                for (int o = 1; o < PARTS; ++o)
+                    s += sums[o * kWide + threadIdx.x];
+            __syncthreads();
+        }
+        if (part == 0 && t < n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < a.dim)
+                    store<BF16>(a.out, row * a.dim + col + e, s[e]);
     }
 }
 
@@ -457,7 +568,7 @@ Form form_of(const Product &p, bool may_split, bool tall_b)
                {kMid, 128, 128, 0.75, 1.0}, {kBig, 256, 256, 1.0, 0.0}};
     Form best{kMid, 1};
     double least = INFINITY;
-    const int steps = tiles(p.nk, p.bf16 ? 64 : 32), most = may_split ? (steps / 4 < 64 ? steps / 4 : 64) : 1;
+    const int steps = tiles(p.nk, p.bf16 ? 64 : 32), most = may_split ? (steps / 4 < 256 ? steps / 4 : 256) : 1;
     for (const auto &f : all) {
         const double rate = p.bf16 ? f.bf16 : f.fp32;
         if (rate == 0.0 || (tall_b && f.tj < (p.bf16 ? 128 : 64)))
@@ -554,14 +665,20 @@ hipError_t launch_stats_done(const Op &op, hipStream_t stream)
     int wide = 1;
     while (wide < 64 && a.rows / wide > 512)
         wide *= 2;
-    const unsigned joins = blocks(a.rows, wide), entries = blocks(int64_t(a.rows) * a.topk, kThreads / 64),
+    // several entries per wave once there are waves for every compute unit without
+    const int64_t all = int64_t(a.rows) * a.topk;
+    const int picks = all < 32768 ? 1 : 4;
+    const unsigned joins = blocks(a.rows, wide), entries = blocks(all, picks * kThreads / 64),
                    grid = joins + (entries < 65536u ? entries : 65536u);
     (void)hipGetLastError();
-    if (a.bf16)
-        stats_done_kernel<true><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
-    else
-        stats_done_kernel<false><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
-    return hipGetLastError();
+    const auto go = [&](auto bf16) {
+        if (picks == 1)
+            stats_done_kernel<decltype(bf16)::value, 1><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
+        else
+            stats_done_kernel<decltype(bf16)::value, 4><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
+        return hipGetLastError();
+    };
+    return a.bf16 ? go(std::true_type{}) : go(std::false_type{});
 }
 
 hipError_t launch_cross_entropy(const Op &op, hipStream_t stream)
@@ -582,7 +699,7 @@ hipError_t launch_distill(const Op &op, hipStream_t stream)
 hipError_t launch_rows(const Op &op, hipStream_t stream)
 {
     const RowsArgs a = op.get<RowsArgs>();
-    RR_LAUNCH(rows_kernel, dim3(blocks(a.rows, kThreads)), a);
+    RR_LAUNCH(rows_kernel, dim3(blocks(a.rows, kThreads / 64)), a);
 }
 
 hipError_t launch_dz(const Op &op, hipStream_t stream)
@@ -600,7 +717,7 @@ hipError_t launch_dz(const Op &op, hipStream_t stream)
 hipError_t launch_targets(const Op &op, hipStream_t stream)
 {
     const TargetArgs a = op.get<TargetArgs>();
-    const dim3 grid(blocks(int64_t(a.rows) * a.topk, kThreads));
+    const dim3 grid(blocks(a.rows, kThreads / 64));
     if (a.bf16)
         RR_LAUNCH(targets_kernel<true>, grid, a);
     RR_LAUNCH(targets_kernel<false>, grid, a);
@@ -637,11 +754,16 @@ hipError_t launch_store(const Op &op, hipStream_t stream)
 hipError_t launch_gather(const Op &op, hipStream_t stream)
 {
     const GatherArgs a = op.get<GatherArgs>();
-    const unsigned all = blocks(a.rows * a.dim, kThreads);
+    const bool many = a.splits >= 16;
+    const unsigned all = blocks(a.rows * (a.lda / 4), many ? kThreads / 8 : kThreads);
     const dim3 grid(all < 4096u ? all : 4096u);
+    if (a.bf16 && many)
+        RR_LAUNCH((gather_kernel<true, 8>), grid, a);
     if (a.bf16)
-        RR_LAUNCH(gather_kernel<true>, grid, a);
-    RR_LAUNCH(gather_kernel<false>, grid, a);
+        RR_LAUNCH((gather_kernel<true, 1>), grid, a);
+    if (many)
+        RR_LAUNCH((gather_kernel<false, 8>), grid, a);
+    RR_LAUNCH((gather_kernel<false, 1>), grid, a);
 }
 
 }  // namespace rr
