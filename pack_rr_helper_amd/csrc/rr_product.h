@@ -101,6 +101,13 @@ __device__ __forceinline__ void store_chunk(char *p, u32x4 v, int left)
     }
 }
 
+__device__ __forceinline__ unsigned pack_bf16(float lo, float hi)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 // Which tile a workgroup computes.  Consecutive workgroups go to the eight
 // dies in turn; each die gets a contiguous range of an order that walks i for
 // kGroup rows of tiles at a time, so that the tiles a die runs at once share
@@ -134,6 +141,15 @@ struct Tile {
 
     struct Acc {
         f32x4 c[FI][FJ];
+
+        __device__ void clear()
+        {
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int j = 0; j < FJ; ++j)
+                    c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
     };
 
     // First row of the wave's results, and of the lane's.
@@ -255,116 +271,166 @@ struct Tile {
         }
     }
 
-    // Steps [s0, s1) of k of the tile at (i0, j0).
-    __device__ static void run(const Product &p, int64_t i0, int64_t j0, int s0, int s1, char *lds, Acc &acc)
-    {
-        const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-#pragma unroll
-        for (int i = 0; i < FI; ++i)
-#pragma unroll
-            for (int j = 0; j < FJ; ++j)
-                acc.c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        using A = Side<TALL_A, TI, kLoadsA>;
-        using B = Side<TALL_B, TJ, kLoadsB>;
-        A a;
-        B b;
-        a.init(p.a, p.lda, p.ni, i0, p.nk);
-        b.init(p.b, p.ldb, p.nj, j0, p.nk);
-        const int wi = wave_i(), wj = wave_j();
+    // Steps [s0, s1) of k of the tile at (i0, j0): start() sends its first loads,
+    // finish() computes it.  What needs none of the tile's LDS can stand between.
+    struct Pipe {
+        Side<TALL_A, TI, kLoadsA> a;
+        Side<TALL_B, TJ, kLoadsB> b;
+        char *lds;
+        int s0, s1;
 
-        if constexpr (DIRECT) {
-            auto fetch = [&](int s) {
-                char *to = lds + s % STAGES * kStageBytes + wave * 1024;
-                a.fetch(s, s < s1, to);
-                b.fetch(s, s < s1, to + kLoadsA * kLoadBytes);
-            };
-            u32x4 a0[FI], b0[FJ], a1[FI], b1[FJ];
-            auto read = [&](int s, int h, u32x4 *fa, u32x4 *fb, int n) {
-                const char *stage = lds + s % STAGES * kStageBytes;
-                if (n < FJ)
-                    fb[n] = B::fragment(stage + kLoadsA * kLoadBytes, wj + n * 16, h);
-                else if (n < FJ + FI)
-                    fa[n - FJ] = A::fragment(stage, wi + (n - FJ) * 16, h);
-            };
-            constexpr int kReads = FI + FJ, kAt = (FI + 3) / 4 - 1;  // the barrier: after this row of the second half
-            constexpr int kPer = (kReads + FI - 1) / FI, kPerNext = (kReads + FI - 2 - kAt) / (FI - 1 - kAt);
+        __device__ void fetch(int s) const
+        {
+            char *to = lds + s % STAGES * kStageBytes + threadIdx.x / 64 * 1024;
+            a.fetch(s, s < s1, to);
+            b.fetch(s, s < s1, to + kLoadsA * kLoadBytes);
+        }
+        __device__ void hold(int s, u32x4 *ha, u32x4 *hb) const
+        {
+            a.hold(s, s < s1, ha);
+            b.hold(s, s < s1, hb);
+        }
+        __device__ void commit(int s, const u32x4 *ha, const u32x4 *hb) const
+        {
+            char *to = lds + s % STAGES * kStageBytes + threadIdx.x * 16;
 #pragma unroll
-            for (int s = 0; s < STAGES; ++s)
-                fetch(s0 + s);
-            wait_loads<(STAGES - 1) * kLoads>();
-            __builtin_amdgcn_s_barrier();
+            for (int l = 0; l < kLoadsA; ++l)
+                *reinterpret_cast<u32x4 *>(to + l * kLoadBytes) = ha[l];
 #pragma unroll
-            for (int n = 0; n < kReads; ++n)
-                read(s0, 0, a0, b0, n);
-            for (int s = s0; s < s1; ++s) {
+            for (int l = 0; l < kLoadsB; ++l)
+                *reinterpret_cast<u32x4 *>(to + (kLoadsA + l) * kLoadBytes) = hb[l];
+        }
+        // Fragment n of a half: first B's, then A's.
+        __device__ void read(int s, int h, u32x4 *fa, u32x4 *fb, int n) const
+        {
+            const char *stage = lds + s % STAGES * kStageBytes;
+            if (n < FJ)
+                fb[n] = decltype(b)::fragment(stage + kLoadsA * kLoadBytes, wave_j() + n * 16, h);
+            else if (n < FJ + FI)
+                fa[n - FJ] = decltype(a)::fragment(stage, wave_i() + (n - FJ) * 16, h);
+        }
+
+        __device__ void start(const Product &p, int64_t i0, int64_t j0, int first, int last, char *buffer)
+        {
+            lds = buffer;
+            s0 = first;
+            s1 = last;
+            a.init(p.a, p.lda, p.ni, i0, p.nk);
+            b.init(p.b, p.ldb, p.nj, j0, p.nk);
+            if constexpr (DIRECT) {
 #pragma unroll
-                for (int i = 0; i < FI; ++i) {
-#pragma unroll
-                    for (int j = 0; j < FJ; ++j)
-                        multiply(a0[i], b0[j], acc.c[i][j]);
-                    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int n = 0; n < kPer; ++n)
-                        read(s, 1, a1, b1, i * kPer + n);
-                }
-#pragma unroll
-                for (int i = 0; i < FI; ++i) {
-#pragma unroll
-                    for (int j = 0; j < FJ; ++j)
-                        multiply(a1[i], b1[j], acc.c[i][j]);
-                    if (i == kAt) {
-                        wait_loads<(STAGES - 2) * kLoads>();
-                        __builtin_amdgcn_s_barrier();
-                        fetch(s + STAGES);
-                    }
-                    if (i >= kAt) {
-#pragma unroll
-                        for (int n = 0; n < kPerNext; ++n)
-                            read(s + 1, 0, a0, b0, (i - kAt) * kPerNext + n);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            }
-        } else {
-            u32x4 ha[kLoadsA], hb[kLoadsB];
-            auto commit = [&](int s) {
-                char *to = lds + s % STAGES * kStageBytes + wave * 1024 + lane * 16;
-#pragma unroll
-                for (int l = 0; l < kLoadsA; ++l)
-                    *reinterpret_cast<u32x4 *>(to + l * kLoadBytes) = ha[l];
-#pragma unroll
-                for (int l = 0; l < kLoadsB; ++l)
-                    *reinterpret_cast<u32x4 *>(to + (kLoadsA + l) * kLoadBytes) = hb[l];
-            };
-            a.hold(s0, s0 < s1, ha);
-            b.hold(s0, s0 < s1, hb);
-            commit(s0);
-            for (int s = s0; s < s1; ++s) {
-                __syncthreads();
-                a.hold(s + 1, s + 1 < s1, ha);
-                b.hold(s + 1, s + 1 < s1, hb);
-                const char *stage = lds + s % STAGES * kStageBytes;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    u32x4 fa[FI], fb[FJ];
-#pragma unroll
-                    for (int i = 0; i < FI; ++i)
-                        fa[i] = A::fragment(stage, wi + i * 16, h);
-#pragma unroll
-                    for (int j = 0; j < FJ; ++j)
-                        fb[j] = B::fragment(stage + kLoadsA * kLoadBytes, wj + j * 16, h);
-#pragma unroll
-                    for (int i = 0; i < FI; ++i)
-#pragma unroll
-                        for (int j = 0; j < FJ; ++j)
-                            multiply(fa[i], fb[j], acc.c[i][j]);
-                }
-                commit(s + 1);
+                for (int s = 0; s < STAGES; ++s)
+                    fetch(s0 + s);
+            } else {
+                u32x4 ha[kLoadsA], hb[kLoadsB];
+                hold(s0, ha, hb);
+                commit(s0, ha, hb);
             }
         }
-        // the loads past s1 have written zeros: LDS is free after this
-        wait_loads<0>();
-        __syncthreads();
+
+        // acc += the tile's products
+        __device__ void finish(Acc &acc) const
+        {
+            constexpr int kReads = FI + FJ;
+            if constexpr (DIRECT) {
+                constexpr int kAt = (FI + 3) / 4 - 1;  // the barrier: after this row of the second half
+                constexpr int kPer = (kReads + FI - 1) / FI, kPerNext = (kReads + FI - 2 - kAt) / (FI - 1 - kAt);
+                u32x4 a0[FI], b0[FJ], a1[FI], b1[FJ];
+                wait_loads<(STAGES - 1) * kLoads>();
+                __builtin_amdgcn_s_barrier();
+#pragma unroll
+                for (int n = 0; n < kReads; ++n)
+                    read(s0, 0, a0, b0, n);
+                for (int s = s0; s < s1; ++s) {
+#pragma unroll
+                    for (int i = 0; i < FI; ++i) {
+#pragma unroll
+                        for (int j = 0; j < FJ; ++j)
+                            multiply(a0[i], b0[j], acc.c[i][j]);
+                        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int n = 0; n < kPer; ++n)
+                            read(s, 1, a1, b1, i * kPer + n);
+                    }
+#pragma unroll
+                    for (int i = 0; i < FI; ++i) {
+#pragma unroll
+                        for (int j = 0; j < FJ; ++j)
+                            multiply(a1[i], b1[j], acc.c[i][j]);
+                        if (i == kAt) {
+                            wait_loads<(STAGES - 2) * kLoads>();
+                            __builtin_amdgcn_s_barrier();
+                            fetch(s + STAGES);
+                        }
+                        if (i >= kAt) {
+#pragma unroll
+                            for (int n = 0; n < kPerNext; ++n)
+                                read(s + 1, 0, a0, b0, (i - kAt) * kPerNext + n);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            } else {
+                for (int s = s0; s < s1; ++s) {
+                    u32x4 ha[kLoadsA], hb[kLoadsB];
+                    __syncthreads();
+                    hold(s + 1, ha, hb);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        u32x4 fa[FI], fb[FJ];
+#pragma unroll
+                        for (int n = 0; n < kReads; ++n)
+                            read(s, h, fa, fb, n);
+#pragma unroll
+                        for (int i = 0; i < FI; ++i)
+#pragma unroll
+                            for (int j = 0; j < FJ; ++j)
+                                multiply(fa[i], fb[j], acc.c[i][j]);
+                    }
+                    commit(s + 1, ha, hb);
+                }
+            }
+            // the loads past s1 have written zeros: LDS is free after this
+            wait_loads<0>();
+            __syncthreads();
+        }
+    };
+
+    // The lane's row j of the wave's results, v, to out (at the tile's first
+    // i), `left` of them from there on.  bf16 lanes 16 apart swap halves of two
+    // neighbouring fragments, which makes 16 bytes per lane and 64 per row.
+    __device__ static void store_row(char *out, const f32x4 *v, int left)
+    {
+        const int g = threadIdx.x % 64 / 16;
+        if constexpr (BF16) {
+#pragma unroll
+            for (int f = 0; f < FI; f += 2) {
+                u32x4 w;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const auto s = __builtin_amdgcn_permlane16_swap(pack_bf16(v[f][2 * n], v[f][2 * n + 1]),
+                                                                    pack_bf16(v[f + 1][2 * n], v[f + 1][2 * n + 1]), false, false);
+                    w[n] = s[0];
+                    w[2 + n] = s[1];
+                }
+                const int i = wave_i() + (f + g % 2) * 16 + g / 2 * 8;
+                if (i < left)
+                    store_chunk<2>(out + i * 2, w, (left - i) * 2);
+            }
+        } else {
+#pragma unroll
+            for (int f = 0; f < FI; ++f) {
+                const int i = wave_i() + f * 16 + g * 4;
+                if (i < left)
+                    store_chunk<4>(out + i * 4, __builtin_bit_cast(u32x4, v[f]), (left - i) * 4);
+            }
+        }
+    }
+    // Whether store_row has this lane write result i of the wave's.
+    __device__ static bool stores(int i)
+    {
+        const int g = threadIdx.x % 64 / 16;
+        return i >= 0 && i < FI * 16 && g == (BF16 ? i / 16 % 2 + i % 16 / 8 * 2 : i % 16 / 4);
     }
 };
 

@@ -40,13 +40,6 @@ __device__ __forceinline__ float exp_below(float x, float top)
     return x == -INFINITY ? 0.0f : expf(x - top);
 }
 
-__device__ __forceinline__ unsigned pack_bf16(float lo, float hi)
-{
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
-
 // One wave's rows of a tile: part = the logits' maximum and sum of exponentials.
 template <typename T>
 __global__ __launch_bounds__(T::kThreads) void stats_kernel(StatsArgs a, int tiles_i, int tiles_j)
@@ -54,10 +47,12 @@ __global__ __launch_bounds__(T::kThreads) void stats_kernel(StatsArgs a, int til
     __shared__ __attribute__((aligned(1024))) char lds[T::kLdsBytes];
     int ti, tj;
     tile_at(blockIdx.x, gridDim.x, tiles_i, tiles_j, ti, tj);
-    const int i0 = ti * T::TI, j0 = tj * T::TJ;
+    const int i0 = ti * T::TI, j0 = tj * T::TJ, part = ti * (T::TI / (T::FI * 16)) + T::wave_i() / (T::FI * 16);
+    typename T::Pipe pipe;
+    pipe.start(a.p, i0, j0, 0, (a.p.nk + T::kStep - 1) / T::kStep, lds);
     typename T::Acc acc;
-    T::run(a.p, i0, j0, 0, (a.p.nk + T::kStep - 1) / T::kStep, lds, acc);
-    const int part = ti * (T::TI / (T::FI * 16)) + T::wave_i() / (T::FI * 16);
+    acc.clear();
+    pipe.finish(acc);
     // z = scale * acc; the largest is at the largest of acc once scale is positive
     const float scale = fabsf(a.scale), c = scale * kLog2e;
     if (a.scale < 0.0f) {
@@ -279,12 +274,6 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(CombineArgs a)
     }
 }
 
-// A row's lse in units of ln 2 and its coefficient of dz; zeros without a target.
-__device__ __forceinline__ float2 row_factors(const RowsArgs &a, int64_t j, bool used)
-{
-    return used ? float2{a.lse[j] * kLog2e, a.grad[j] * a.scale} : float2{0.0f, 0.0f};
-}
-
 // One wave per row.
 __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a)
 {
@@ -296,51 +285,8 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a)
         used |= a.prob[j * a.topk + e] != 0.0f;
     used = __ballot(used) != 0;
     if (threadIdx.x % 64 == 0)
-        a.row[j] = row_factors(a, j, used);
+        a.row[j] = used ? float2{a.lse[j] * kLog2e, a.grad[j] * a.scale} : float2{0.0f, 0.0f};
 }
-
-// A tile in the element type, [TJ][TI] with 4 bytes after each row: sixteen
-// rows that are written at once then start on different banks.
-template <typename T>
-struct Staged {
-    static constexpr int kStride = T::TI * T::kEs + 4;
-    static constexpr int kBytes = T::TJ * kStride;
-
-    // Four results of one row of the tile.
-    __device__ static void put(char *lds, int j, int i, f32x4 v)
-    {
-        unsigned *to = reinterpret_cast<unsigned *>(lds + j * kStride + i * T::kEs);
-        if constexpr (T::kEs == 2) {
-            to[0] = pack_bf16(v[0], v[1]);
-            to[1] = pack_bf16(v[2], v[3]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                to[e] = __float_as_uint(v[e]);
-        }
-    }
-
-    __device__ static void put_one(char *lds, int j, int i, float v)
-    {
-        store<T::kEs == 2>(lds + j * kStride, i, v);
-    }
-
-    // Rows j < nj, results i < ni to out[j][i].
-    __device__ static void store_rows(const char *lds, char *out, int64_t stride, int nj, int ni)
-    {
-        constexpr int kChunks = T::TI * T::kEs / 16;
-        for (int t = threadIdx.x; t < T::TJ * kChunks; t += T::kThreads) {
-            const int j = t / kChunks, c = t % kChunks, left = ni * T::kEs - c * 16;
-            if (j >= nj || left <= 0)
-                continue;
-            const unsigned *from = reinterpret_cast<const unsigned *>(lds + j * kStride + c * 16);
-            store_chunk<T::kEs>(out + j * stride + c * 16, u32x4{from[0], from[1], from[2], from[3]}, left);
-        }
-    }
-};
-
-template <typename T>
-constexpr int staged_lds = T::kLdsBytes > Staged<T>::kBytes ? T::kLdsBytes : Staged<T>::kBytes;
 
 __device__ __forceinline__ int round64(int n) { return (n + 63) / 64 * 64; }
 
@@ -350,55 +296,73 @@ __device__ __forceinline__ int round64(int n) { return (n + 63) / 64 * 64; }
 template <typename T>
 __global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, int tiles_j)
 {
-    __shared__ __attribute__((aligned(1024))) char lds[staged_lds<T>];
+    // a row's factors, its target within the piece (-1: none) and dz there
+    struct Row {
+        float2 r;
+        int target;
+        float d;
+    };
+    __shared__ __attribute__((aligned(1024))) char lds[T::kLdsBytes];
+    __shared__ Row rows[T::TJ];
     int ti, tj;
     tile_at(blockIdx.x, gridDim.x, tiles_i, tiles_j, ti, tj);
     const int i0 = ti * T::TI, j0 = tj * T::TJ;
+    // this thread's row, at a clamped place; its loads fly together with the tile's first
+    const int mine = j0 + int(threadIdx.x), in = mine < a.p.nj ? mine : 0;
+    float lse = 0.0f, grad = 0.0f, logit = 0.0f;
+    int64_t at = -1;
+    Row row{float2{0.0f, 0.0f}, -1, 0.0f};
+    if (a.rows.prob) {
+        row.r = a.rows.row[in];
+    } else {
+        at = a.rows.index[in];
+        lse = a.rows.lse[in];
+        grad = a.rows.grad[in];
+        logit = a.logit[in];
+    }
+    typename T::Pipe pipe;
+    pipe.start(a.p, i0, j0, 0, (a.p.nk + T::kStep - 1) / T::kStep, lds);
+    if (counts(at, a.rows.total)) {
+        row.r = float2{lse * kLog2e, grad * a.rows.scale};
+        if (at >= a.first && at < a.first + a.p.ni && row.r.y != 0.0f) {
+            row.target = int(at - a.first);
+            row.d = row.r.y * (__builtin_amdgcn_exp2f(__builtin_fmaf(logit, kLog2e, -row.r.x)) - 1.0f);
+        }
+    }
+    if (mine >= a.p.nj)
+        row = Row{float2{0.0f, 0.0f}, -1, 0.0f};
+    if (int(threadIdx.x) < T::TJ)
+        rows[threadIdx.x] = row;
     typename T::Acc acc;
-    T::run(a.p, i0, j0, 0, (a.p.nk + T::kStep - 1) / T::kStep, lds, acc);
+    acc.clear();
+    pipe.finish(acc);
     const bool full = i0 + T::TI <= a.p.ni;
     const float c = a.rows.scale * kLog2e;
 #pragma unroll
     for (int j = 0; j < T::FJ; ++j) {
-        const int row = j0 + T::lane_j(j);
-        float2 r{0.0f, 0.0f};
-        int target = -1;   // cross entropy: within the wave's results
-        if (row < a.p.nj) {
-            if (a.rows.prob) {
-                r = a.rows.row[row];
-            } else {
-                const int64_t at = a.rows.index[row];
-                r = row_factors(a.rows, row, counts(at, a.rows.total));
-                if (at >= a.first + i0 && at < a.first + a.p.ni && at - a.first - i0 < T::TI)
-                    target = int(at - a.first) - i0 - T::wave_i();
-            }
-        }
+        const Row of = rows[T::lane_j(j)];
+        f32x4 d[T::FI];
         // no dz in a row without a target, whatever its logits
-        if (r.y == 0.0f) {
+        if (of.r.y == 0.0f) {
 #pragma unroll
             for (int i = 0; i < T::FI; ++i)
                 acc.c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
 #pragma unroll
-        for (int i = 0; i < T::FI; ++i) {
-            f32x4 d;
+        for (int i = 0; i < T::FI; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                d[e] = r.y * __builtin_amdgcn_exp2f(__builtin_fmaf(acc.c[i][j][e], c, -r.x));
+                d[i][e] = of.r.y * __builtin_amdgcn_exp2f(__builtin_fmaf(acc.c[i][j][e], c, -of.r.x));
                 if (!full && i0 + T::lane_i(i) + e >= a.p.ni)
-                    d[e] = 0.0f;
+                    d[i][e] = 0.0f;
             }
-            Staged<T>::put(lds, T::lane_j(j), T::lane_i(i), d);
-        }
-        // the lane that holds the target has just written it
-        if (target >= 0 && target < T::FI * 16 && target % 16 / 4 == threadIdx.x % 64 / 16)
-            Staged<T>::put_one(lds, T::lane_j(j), T::wave_i() + target, r.y == 0.0f ? 0.0f :
-                r.y * (__builtin_amdgcn_exp2f(__builtin_fmaf(a.logit[row], kLog2e, -r.x)) - 1.0f));
+        const int64_t to = j0 + T::lane_j(j);
+        char *out = static_cast<char *>(a.dz) + (to * a.ldz + i0) * T::kEs;
+        T::store_row(out, d, to < a.p.nj ? round64(a.p.ni) - i0 : 0);
+        // by the lane that has just written there
+        if (of.target >= 0 && T::stores(of.target - i0 - T::wave_i()))
+            store<T::kEs == 2>(out, of.target - i0, of.d);
     }
-    __syncthreads();
-    const int left_i = round64(a.p.ni) - i0;
-    Staged<T>::store_rows(lds, static_cast<char *>(a.dz) + (j0 * a.ldz + i0) * T::kEs, a.ldz * T::kEs,
-                          a.p.nj - j0 < T::TJ ? a.p.nj - j0 : T::TJ, left_i < T::TI ? left_i : T::TI);
 }
 
 // One wave per row.  Equal entries of a row write the same value.
@@ -459,37 +423,47 @@ __global__ __launch_bounds__(kThreads) void align_kernel(AlignArgs a)
 template <typename T>
 __global__ __launch_bounds__(T::kThreads) void store_kernel(StoreArgs a, int tiles_i, int tiles_j)
 {
-    __shared__ __attribute__((aligned(1024))) char lds[staged_lds<T>];
+    __shared__ __attribute__((aligned(1024))) char lds[T::kLdsBytes];
     const int tiles = tiles_i * tiles_j, split = blockIdx.x / tiles;
     int ti, tj;
     tile_at(blockIdx.x - split * tiles, tiles, tiles_i, tiles_j, ti, tj);
     const int i0 = ti * T::TI, j0 = tj * T::TJ;
     const int steps = (a.p.nk + T::kStep - 1) / T::kStep, per = (steps + a.splits - 1) / a.splits;
     const int s0 = split * per < steps ? split * per : steps, s1 = s0 + per < steps ? s0 + per : steps;
+    typename T::Pipe pipe;
+    pipe.start(a.p, i0, j0, s0, s1, lds);
     typename T::Acc acc;
-    T::run(a.p, i0, j0, s0, s1, lds, acc);
-    if (a.acc) {
-        float *out = a.acc + int64_t(split) * a.p.nj * a.lda;
+    acc.clear();
+    const auto part = [&](int j, int i) {
+        const int row = j0 + T::lane_j(j), col = i0 + T::lane_i(i);
+        float *to = a.acc + (int64_t(split) * a.p.nj + row) * a.lda + col;
+        return row < a.p.nj && col < a.lda ? reinterpret_cast<f32x4 *>(to) : nullptr;
+    };
+    if (a.add) {
 #pragma unroll
         for (int j = 0; j < T::FJ; ++j)
 #pragma unroll
-            for (int i = 0; i < T::FI; ++i) {
-                const int row = j0 + T::lane_j(j), col = i0 + T::lane_i(i);
-                if (row >= a.p.nj || col >= a.lda)
-                    continue;
-                f32x4 *to = reinterpret_cast<f32x4 *>(out + row * a.lda + col);
-                *to = a.add ? *to + acc.c[i][j] : acc.c[i][j];
-            }
-        return;
+            for (int i = 0; i < T::FI; ++i)
+                if (const f32x4 *from = part(j, i))
+                    acc.c[i][j] = *from;
     }
+    pipe.finish(acc);
 #pragma unroll
-    for (int j = 0; j < T::FJ; ++j)
+    for (int j = 0; j < T::FJ; ++j) {
+        if (a.acc) {
 #pragma unroll
-        for (int i = 0; i < T::FI; ++i)
-            Staged<T>::put(lds, T::lane_j(j), T::lane_i(i), acc.c[i][j]);
-    __syncthreads();
-    Staged<T>::store_rows(lds, static_cast<char *>(a.out) + (j0 * a.ldo + i0) * T::kEs, a.ldo * T::kEs,
-                          a.p.nj - j0 < T::TJ ? a.p.nj - j0 : T::TJ, a.p.ni - i0 < T::TI ? a.p.ni - i0 : T::TI);
+            for (int i = 0; i < T::FI; ++i)
+                if (f32x4 *to = part(j, i))
+                    *to = acc.c[i][j];
+        } else {
+            f32x4 v[T::FI];
+#pragma unroll
+            for (int i = 0; i < T::FI; ++i)
+                v[i] = acc.c[i][j];
+            const int64_t row = j0 + T::lane_j(j);
+            T::store_row(static_cast<char *>(a.out) + (row * a.ldo + i0) * T::kEs, v, row < a.p.nj ? a.p.ni - i0 : 0);
+        }
+    }
 }
 
 // Four columns of a row per PARTS threads, each of which takes its share of the
@@ -610,9 +584,9 @@ hipError_t with_shape(Shape s, F f)
 {
     if constexpr (!TB) {
         if (s == kRows16)
-            return f(Rows<BF16, 16, 4, DIRECT, TA, TB>{});
+            return f(Rows<BF16, 16, 3, DIRECT, TA, TB>{});
         if (s == kRows32)
-            return f(Rows<BF16, 32, 4, DIRECT, TA, TB>{});
+            return f(Rows<BF16, 32, 3, DIRECT, TA, TB>{});
     }
     if constexpr (!(TB && BF16))
         if (s == kRows64)
