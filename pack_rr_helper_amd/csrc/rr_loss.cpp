@@ -138,10 +138,10 @@ private:
 // at a time.
 struct GradSpace {
     int64_t piece, ldd, ldv, lda;
-    int32_t pieces, splits;
+    int32_t pieces, x_splits, w_splits;
     float2 *row;
     char *x, *w, *dz;    // x, w: copies in 16-byte chunks, of operands that are not
-    float *acc;
+    float *dx, *dw;      // parts of the gradients' sums
     int64_t bytes;
 };
 
@@ -159,16 +159,18 @@ GradSpace grad_space(const rr_vocab *v, int dtype, int64_t rows, void *base)
     s.ldv = round_up(s.piece, 64);
     s.lda = round_up(v->dim, 4);
     s.pieces = s.piece ? int32_t((v->vocab + s.piece - 1) / s.piece) : 0;
-    // one number of parts for every piece, as the sums go on from piece to piece
-    s.splits = product_splits(Product{nullptr, nullptr, s.ldd, s.ldv, v->dim, int32_t(rows), int32_t(s.piece),
-                                      dtype == RR_BF16});
-    Carver c(base);
-    s.row = static_cast<float2 *>(c.take(rows * 8));
-    s.x = static_cast<char *>(c.take(rows * s.ldd * es));
-    s.w = static_cast<char *>(c.take(s.piece * s.ldd * es));
-    s.dz = static_cast<char *>(c.take(rows * s.ldv * es));
-    s.acc = static_cast<float *>(c.take(s.splits * rows * s.lda * 4));
-    s.bytes = c.used();
+    // one number of parts for every piece, as dx's sums go on from piece to piece
+    const int32_t bf16 = dtype == RR_BF16, n = int32_t(rows), c = int32_t(s.piece);
+    s.x_splits = product_splits(Product{nullptr, nullptr, s.ldd, s.ldv, v->dim, n, c, bf16}, false);
+    s.w_splits = product_splits(Product{nullptr, nullptr, s.ldd, s.ldv, v->dim, c, n, bf16}, true);
+    Carver space(base);
+    s.row = static_cast<float2 *>(space.take(rows * 8));
+    s.x = static_cast<char *>(space.take(rows * s.ldd * es));
+    s.w = static_cast<char *>(space.take(s.piece * s.ldd * es));
+    s.dz = static_cast<char *>(space.take(rows * s.ldv * es));
+    s.dx = static_cast<float *>(space.take(s.x_splits * rows * s.lda * 4));
+    s.dw = static_cast<float *>(space.take(s.w_splits > 1 ? s.w_splits * s.piece * s.lda * 4 : 0));
+    s.bytes = space.used();
     return s;
 }
 
@@ -370,7 +372,7 @@ rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *
     if (v->vocab > 0 && prob)
         l.add(launch_rows, of_rows);
     const bool copy_x = !in_chunks(x, dim, es), copy_w = !in_chunks(w, dim, es);
-    const bool whole = s.pieces == 1 && s.splits == 1;  // dx is one product
+    const bool whole = s.pieces == 1 && s.x_splits == 1;  // dx is one product
     const void *xc = copy_x ? s.x : x;
     const int64_t ldx = copy_x ? s.ldd : dim, ldw = copy_w ? s.ldd : dim;
     if (copy_x && v->vocab > 0)
@@ -386,12 +388,16 @@ rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *
         l.add(launch_dz, DzArgs{Product{wc, xc, ldw, ldx, c, n, dim, bf16}, of_rows, logit, v->first + v0, s.dz, s.ldv});
         if (prob)
             l.add(launch_targets, TargetArgs{index, logit, prob, s.row, n, v->topk, c, bf16, v->first + v0, s.dz, s.ldv});
-        l.add(launch_store, StoreArgs{Product{xc, s.dz, ldx, s.ldv, dim, c, n, bf16}, dwp, dim, nullptr, 0, 1, 0, 1});
+        const bool parts = s.w_splits > 1;
+        l.add(launch_store, StoreArgs{Product{xc, s.dz, ldx, s.ldv, dim, c, n, bf16}, parts ? nullptr : dwp, dim,
+                                      parts ? s.dw : nullptr, s.lda, s.w_splits, 0, 1});
+        if (parts)
+            l.add(launch_gather, GatherArgs{s.dw, dwp, c, s.lda, dim, s.w_splits, bf16});
         l.add(launch_store, StoreArgs{Product{wc, s.dz, ldw, s.ldv, dim, n, c, bf16}, whole ? dx : nullptr, dim,
-                                      whole ? nullptr : s.acc, s.lda, s.splits, v0 > 0, 0});
+                                      whole ? nullptr : s.dx, s.lda, s.x_splits, v0 > 0, 0});
     }
     if (!whole)
-        l.add(launch_gather, GatherArgs{s.acc, dx, rows, s.lda, dim, v->vocab > 0 ? s.splits : 0, bf16});
+        l.add(launch_gather, GatherArgs{s.dx, dx, rows, s.lda, dim, v->vocab > 0 ? s.x_splits : 0, bf16});
     return l.finish();
 }
 

@@ -156,7 +156,7 @@ struct StoreArgs {
     int32_t splits, add; // add: to what acc holds
     int32_t tall_b;
 };
-int32_t product_splits(const Product &p);
+int32_t product_splits(const Product &p, bool tall_b);
 hipError_t launch_store(const Op &, hipStream_t);
 
 // out = the sum of the partial sums (none: zero).

@@ -8,6 +8,7 @@
 // time.  rr_route is bound by these vector instructions, rr_route_grad by its
 // bytes.  Loads are unconditional, at clamped places: a load under a condition
 // is waited for where the condition ends.
+#include "rr_lanes.h"
 #include "rr_loss.h"
 
 namespace rr {
@@ -16,66 +17,6 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kRouteThreads = 512, kRouteWaves = kRouteThreads / 64;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
-
-template <int CTRL>
-__device__ __forceinline__ unsigned dpp(unsigned v)
-{
-    return unsigned(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, false));
-}
-
-// The value of the lane that step STEP of an exchange over G lanes pairs this
-// one with: its neighbour, the other pair, the mirror lane of 8, of 16, and
-// the lanes 16 and 32 away.
-template <int STEP>
-__device__ __forceinline__ unsigned other(unsigned v)
-{
-    if constexpr (STEP == 0)
-        return dpp<0xb1>(v);
-    else if constexpr (STEP == 1)
-        return dpp<0x4e>(v);
-    else if constexpr (STEP == 2)
-        return dpp<0x141>(v);
-    else if constexpr (STEP == 3)
-        return dpp<0x140>(v);
-    else
-        return unsigned(__shfl_xor(int(v), 1 << STEP));
-}
-template <int STEP>
-__device__ __forceinline__ float other(float v)
-{
-    return __uint_as_float(other<STEP>(__float_as_uint(v)));
-}
-template <int STEP>
-__device__ __forceinline__ double other(double v)
-{
-    const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
-    return __builtin_bit_cast(double, (unsigned long long)other<STEP>(unsigned(u >> 32)) << 32 | other<STEP>(unsigned(u)));
-}
-
-// f over the G lanes of a row, the result in every lane.  f commutes, and both
-// sides of each exchange combine the same two values, so all lanes get the
-// same bits.
-template <int G, int STEP = 0, typename T, typename F>
-__device__ __forceinline__ T across(T v, F f)
-{
-    if constexpr (1 << STEP == G)
-        return v;
-    else
-        return across<G, STEP + 1>(f(v, other<STEP>(v)), f);
-}
-
-template <int G>
-__device__ __forceinline__ float row_sum(float v)
-{
-    return across<G>(v, [](float a, float b) { return a + b; });
-}
-
-__device__ __forceinline__ float wave_sum(float v)
-{
-    for (int d = 1; d < 64; d *= 2)
-        v += __shfl_xor(v, d);
-    return v;
-}
 
 // Unsigned keys above 0 in the order of the floats: a positive number's bits
 // above all others, a negative one's negated, which makes both zeros equal.
@@ -407,7 +348,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a)
                 z[s] = exp_from(row.get(s), base);
                 total += z[s];
             }
-            total = row_sum<G>(total);
+            total = lanes_sum<G>(total);
             float chosen = 0.0f;
             const float inv = total == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(total);
 #pragma unroll
@@ -420,7 +361,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a)
             }
             float by = inv;
             if (a.renormalize) {
-                chosen = row_sum<G>(chosen);
+                chosen = lanes_sum<G>(chosen);
                 by = chosen == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(chosen);
             }
 #pragma unroll
@@ -516,7 +457,7 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a)
         a.slope[i] = float(a.experts) * f * inv;
         s += f * (p * inv);
     }
-    s = wave_sum(s);
+    s = lanes_sum<64>(s);
     if (threadIdx.x % 64 == 0)
         sums[threadIdx.x / 64] = s;
     __syncthreads();
@@ -599,7 +540,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a)
                 mean += i * G + lane < a.topk ? of.w[i] * of.g[i] : 0.0f;
             }
             if constexpr (RENORM)
-                mean = row_sum<G>(mean);
+                mean = lanes_sum<G>(mean);
 #pragma unroll
             for (int i = 0; i < kKeep; ++i)
                 if (of.c[i] >= 0)
@@ -618,7 +559,7 @@ __global__ __launch_bounds__(kThreads) void route_grad_kernel(RouteGradArgs a)
                 d[s] = RENORM ? slope[s] : slope[s] + term[s];
                 dot = __builtin_fmaf(p[s], d[s], dot);
             }
-            dot = row_sum<G>(dot);
+            dot = lanes_sum<G>(dot);
 #pragma unroll
             for (int s = 0; s < PER; ++s)
                 d[s] = RENORM ? __builtin_fmaf(p[s], d[s] - dot, term[s]) : p[s] * (d[s] - dot);

@@ -6,6 +6,7 @@
 // (rr_product.h) with different ends.  The vocabulary runs along the registers
 // of a tile, so a row's maximum and sum over the tile are taken within a lane
 // and over the four lane groups of a wave.
+#include "rr_lanes.h"
 #include "rr_product.h"
 
 #include <math.h>
@@ -106,23 +107,9 @@ __device__ __forceinline__ float2 join(float2 a, float2 b)
     return float2{top, a.y * fa + b.y * fb};
 }
 
-__device__ __forceinline__ float wave_max(float v)
-{
-    for (int d = 1; d < 64; d *= 2)
-        v = fmaxf(v, __shfl_xor(v, d));
-    return v;
-}
-
-__device__ __forceinline__ float wave_sum(float v)
-{
-    for (int d = 1; d < 64; d *= 2)
-        v += __shfl_xor(v, d);
-    return v;
-}
-
 // The first `joins` workgroups join the parts of `wide` rows each (a power of
-// two up to 64), the others compute the logits of kPicks entries per wave.
-template <bool BF16, int kPicks>
+// two up to 64), the others compute the logits of one entry per G lanes.
+template <bool BF16, int G>
 __global__ __launch_bounds__(kThreads) void stats_done_kernel(StatsDoneArgs a, int joins, int wide)
 {
     __shared__ float2 sums[kThreads];
@@ -153,51 +140,31 @@ __global__ __launch_bounds__(kThreads) void stats_done_kernel(StatsDoneArgs a, i
         return;
     }
     constexpr int kEs = BF16 ? 2 : 4, kPer = 16 / kEs;
-    const int lane = threadIdx.x % 64;
-    const int64_t entries = int64_t(a.rows) * a.topk, waves = int64_t(gridDim.x - joins) * (kThreads / 64);
-    for (int64_t n0 = ((int64_t(blockIdx.x) - joins) * (kThreads / 64) + threadIdx.x / 64) * kPicks; n0 < entries; n0 += waves * kPicks) {
-        // loads of all of them under way together; one that is not held here reads row 0
-        const char *x[kPicks], *w[kPicks];
-        bool held[kPicks];
-        float z[kPicks];
+    const int lane = threadIdx.x % G;
+    const int64_t entries = int64_t(a.rows) * a.topk, step = int64_t(gridDim.x - joins) * (kThreads / G);
+    for (int64_t n = (int64_t(blockIdx.x) - joins) * (kThreads / G) + threadIdx.x / G; n < entries; n += step) {
+        const int64_t i = a.index[n] - a.first;
+        float z = 0.0f;
+        if (i >= 0 && i < a.vocab) {
+            const char *x = static_cast<const char *>(a.x) + n / a.topk * a.dim * kEs;
+            const char *w = static_cast<const char *>(a.w) + i * a.dim * kEs;
+#pragma unroll 4
+            for (int k = lane * kPer; k < a.dim; k += G * kPer) {
+                const u32x4 u = load_chunk<kEs>(x + k * kEs, (a.dim - k) * kEs), v = load_chunk<kEs>(w + k * kEs, (a.dim - k) * kEs);
 #pragma unroll
-        for (int m = 0; m < kPicks; ++m) {
-            const int64_t n = n0 + m < entries ? n0 + m : entries - 1, i = a.index[n] - a.first;
-            held[m] = i >= 0 && i < a.vocab;
-            x[m] = static_cast<const char *>(a.x) + n / a.topk * a.dim * kEs;
-            w[m] = static_cast<const char *>(a.w) + (held[m] ? i : 0) * a.dim * kEs;
-            z[m] = 0.0f;
-        }
-        bool any = false;
-#pragma unroll
-        for (int m = 0; m < kPicks; ++m)
-            any |= held[m];
-        if (any)
-            for (int k = lane * kPer; k < a.dim; k += 64 * kPer) {
-                u32x4 u[kPicks], v[kPicks];
-#pragma unroll
-                for (int m = 0; m < kPicks; ++m) {
-                    u[m] = load_chunk<kEs>(x[m] + k * kEs, (a.dim - k) * kEs);
-                    v[m] = load_chunk<kEs>(w[m] + k * kEs, (a.dim - k) * kEs);
-                }
-#pragma unroll
-                for (int m = 0; m < kPicks; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if constexpr (BF16) {
-                            z[m] = __builtin_fmaf(__uint_as_float(u[m][e] << 16), __uint_as_float(v[m][e] << 16), z[m]);
-                            z[m] = __builtin_fmaf(__uint_as_float(u[m][e] & 0xffff0000u), __uint_as_float(v[m][e] & 0xffff0000u), z[m]);
-                        } else {
-                            z[m] = __builtin_fmaf(__uint_as_float(u[m][e]), __uint_as_float(v[m][e]), z[m]);
-                        }
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (BF16) {
+                        z = __builtin_fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), z);
+                        z = __builtin_fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(v[e] & 0xffff0000u), z);
+                    } else {
+                        z = __builtin_fmaf(__uint_as_float(u[e]), __uint_as_float(v[e]), z);
                     }
+                }
             }
-#pragma unroll
-        for (int m = 0; m < kPicks; ++m) {
-            const float sum = wave_sum(z[m]) * a.scale;
-            if (lane == 0 && n0 + m < entries)
-                a.picked[n0 + m] = held[m] ? sum : 0.0f;
+            z = lanes_sum<G>(z) * a.scale;
         }
+        if (lane == 0)
+            a.picked[n] = z;
     }
 }
 
@@ -248,13 +215,13 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(CombineArgs a)
         if (counts(a.index[n], a.total))
             top = fmaxf(top, a.scale * load<BF16>(a.teacher, n));
     }
-    top = wave_max(top);
+    top = lanes_max<64>(top);
     for (int e = lane; e < a.topk; e += 64) {
         const int64_t n = j * a.topk + e;
         if (counts(a.index[n], a.total))
             sum += exp_below(a.scale * load<BF16>(a.teacher, n), top);
     }
-    sum = wave_sum(sum);
+    sum = lanes_sum<64>(sum);
     const float log_sum = logf(sum);
     float loss = 0.0f;
     for (int e = lane; e < a.topk; e += 64) {
@@ -267,7 +234,7 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(CombineArgs a)
         if (live && p != 0.0f)
             loss += p * ((t - top) - log_sum - z + lse);
     }
-    loss = wave_sum(loss);
+    loss = lanes_sum<64>(loss);
     if (lane == 0) {
         a.lse[j] = lse;
         a.loss[j] = loss;
@@ -530,8 +497,9 @@ struct Form {
 // 128 x 128, 0.93 and 0.83 of it at 128 x 64 and 128 x 32).  A workgroup of the
 // smaller ones alone on its unit does not fill it.  In units of a
 // multiplication of a compute unit at that rate; a part of k costs the writing
-// and reading of its sums, about 5 (bf16) or 0.5 (fp32) for each.  Up to 64
-// rows the narrowest tile that holds them streams the vocabulary past them.
+// and reading of its sums, about 5 (bf16) or 0.5 (fp32) for each, and their
+// joining a launch, 4 us.  Up to 64 rows the narrowest tile that holds them
+// streams the vocabulary past them.
 Form form_of(const Product &p, bool may_split, bool tall_b)
 {
     static const struct {
@@ -550,13 +518,11 @@ Form form_of(const Product &p, bool may_split, bool tall_b)
         // rows that fit a narrow tile
         if (!tall_b && p.nj <= 64 && (f.tj < p.nj || f.tj > 64 || f.tj >= 2 * p.nj + 16))
             continue;
-        if (!tall_b && p.nj > 64 && f.tj < (p.bf16 ? 64 : 32))
-            continue;
         const double n = double(tiles(p.ni, f.ti)) * tiles(p.nj, f.tj);
         for (int s = 1; s <= (most < 1 ? 1 : most); ++s) {
             const double busy = ceil(n * s / 256);
             const double time = (busy == 1 && f.shape != kBig ? 1.6 : busy) * f.ti * f.tj / rate * (double(p.nk) / s + 256) +
-                                (may_split ? (p.bf16 ? 5.0 : 0.5) * s * p.ni * p.nj : 0.0);
+                                (s > 1 ? (p.bf16 ? 5.0 : 0.5) * s * p.ni * p.nj + (p.bf16 ? 1e7 : 1e6) : 0.0);
             if (time < least) {
                 least = time;
                 best = Form{f.shape, s};
@@ -639,17 +605,17 @@ hipError_t launch_stats_done(const Op &op, hipStream_t stream)
     int wide = 1;
     while (wide < 64 && a.rows / wide > 512)
         wide *= 2;
-    // several entries per wave once there are waves for every compute unit without
+    // 16 lanes an entry once that fills the compute units
     const int64_t all = int64_t(a.rows) * a.topk;
-    const int picks = all < 32768 ? 1 : 4;
-    const unsigned joins = blocks(a.rows, wide), entries = blocks(all, picks * kThreads / 64),
+    const int lanes = all < 8192 ? 64 : 16;
+    const unsigned joins = blocks(a.rows, wide), entries = blocks(all, kThreads / lanes),
                    grid = joins + (entries < 65536u ? entries : 65536u);
     (void)hipGetLastError();
     const auto go = [&](auto bf16) {
-        if (picks == 1)
-            stats_done_kernel<decltype(bf16)::value, 1><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
+        if (lanes == 64)
+            stats_done_kernel<decltype(bf16)::value, 64><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
         else
-            stats_done_kernel<decltype(bf16)::value, 4><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
+            stats_done_kernel<decltype(bf16)::value, 16><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
         return hipGetLastError();
     };
     return a.bf16 ? go(std::true_type{}) : go(std::false_type{});
@@ -707,7 +673,7 @@ hipError_t launch_align(const Op &op, hipStream_t stream)
     RR_LAUNCH(align_kernel<4>, grid, a);
 }
 
-int32_t product_splits(const Product &p) { return form_of(p, true, false).splits; }
+int32_t product_splits(const Product &p, bool tall_b) { return form_of(p, true, tall_b).splits; }
 
 hipError_t launch_store(const Op &op, hipStream_t stream)
 {
@@ -719,7 +685,7 @@ hipError_t launch_store(const Op &op, hipStream_t stream)
         store_kernel<T><<<dim3(unsigned(ti) * unsigned(tj) * unsigned(a.splits)), dim3(T::kThreads), 0, stream>>>(a, ti, tj);
         return hipGetLastError();
     };
-    const Shape s = form_of(a.p, !a.tall_b, a.tall_b).shape;
+    const Shape s = form_of(a.p, true, a.tall_b).shape;
     if (a.tall_b)
         return a.p.bf16 ? with_shape<true, true, true, true>(s, go) : with_shape<false, true, true, true>(s, go);
     return a.p.bf16 ? with_shape<true, true, true, false>(s, go) : with_shape<false, true, true, false>(s, go);
