@@ -365,39 +365,38 @@ rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *
     if (rows == 0) {
         // no row contributes: dw is zero
         if (v->vocab > 0)
-            l.add(launch_gather, GatherArgs{nullptr, dw, v->vocab, s.lda, dim, 0, bf16});
+            l.add(launch_gather, GathersArgs{GatherArgs{}, GatherArgs{nullptr, dw, v->vocab, s.lda, dim, 0}, bf16});
         return l.finish();
     }
     const RowsArgs of_rows{index, lse, prob, grad, n, v->topk, v->total, v->scale, s.row};
-    if (v->vocab > 0 && prob)
-        l.add(launch_rows, of_rows);
     const bool copy_x = !in_chunks(x, dim, es), copy_w = !in_chunks(w, dim, es);
-    const bool whole = s.pieces == 1 && s.x_splits == 1;  // dx is one product
+    const bool whole = s.pieces == 1 && s.x_splits == 1, parts = s.w_splits > 1;  // of dx, of dw
     const void *xc = copy_x ? s.x : x;
     const int64_t ldx = copy_x ? s.ldd : dim, ldw = copy_w ? s.ldd : dim;
-    if (copy_x && v->vocab > 0)
-        l.add(launch_align, AlignArgs{x, s.x, rows, s.ldd, dim, bf16});
+    if (v->vocab == 0)
+        l.add(launch_gather, GathersArgs{GatherArgs{nullptr, dx, rows, s.lda, dim, 0}, GatherArgs{}, bf16});
     for (int64_t v0 = 0; v0 < v->vocab; v0 += s.piece) {
+        const bool first = v0 == 0, last = v0 + s.piece >= v->vocab;
         const int32_t c = int32_t(std::min(s.piece, v->vocab - v0));
-        const void *wc = static_cast<const char *>(w) + v0 * dim * es;
+        const void *wp = static_cast<const char *>(w) + v0 * dim * es, *wc = copy_w ? s.w : wp;
         char *dwp = static_cast<char *>(dw) + v0 * dim * es;
-        if (copy_w) {
-            l.add(launch_align, AlignArgs{wc, s.w, c, s.ldd, dim, bf16});
-            wc = s.w;
-        }
+        if (copy_w || (first && (copy_x || prob)))
+            l.add(launch_prepare, PrepareArgs{first && prob ? of_rows : RowsArgs{},
+                                              first && copy_x ? AlignArgs{x, s.x, rows, s.ldd, dim} : AlignArgs{},
+                                              copy_w ? AlignArgs{wp, s.w, c, s.ldd, dim} : AlignArgs{}, bf16});
         l.add(launch_dz, DzArgs{Product{wc, xc, ldw, ldx, c, n, dim, bf16}, of_rows, logit, v->first + v0, s.dz, s.ldv});
         if (prob)
             l.add(launch_targets, TargetArgs{index, logit, prob, s.row, n, v->topk, c, bf16, v->first + v0, s.dz, s.ldv});
-        const bool parts = s.w_splits > 1;
-        l.add(launch_store, StoreArgs{Product{xc, s.dz, ldx, s.ldv, dim, c, n, bf16}, parts ? nullptr : dwp, dim,
-                                      parts ? s.dw : nullptr, s.lda, s.w_splits, 0, 1});
-        if (parts)
-            l.add(launch_gather, GatherArgs{s.dw, dwp, c, s.lda, dim, s.w_splits, bf16});
-        l.add(launch_store, StoreArgs{Product{wc, s.dz, ldw, s.ldv, dim, n, c, bf16}, whole ? dx : nullptr, dim,
-                                      whole ? nullptr : s.dx, s.lda, s.x_splits, v0 > 0, 0});
+        l.add(launch_stores, StoresArgs{
+            StoreArgs{Product{wc, s.dz, ldw, s.ldv, dim, n, c, bf16}, whole ? dx : nullptr, dim, whole ? nullptr : s.dx,
+                      s.lda, s.x_splits, !first},
+            StoreArgs{Product{xc, s.dz, ldx, s.ldv, dim, c, n, bf16}, parts ? nullptr : dwp, dim,
+                      parts ? s.dw : nullptr, s.lda, s.w_splits, 0}});
+        if (parts || (last && !whole))
+            l.add(launch_gather, GathersArgs{
+                last && !whole ? GatherArgs{s.dx, dx, rows, s.lda, dim, s.x_splits} : GatherArgs{},
+                parts ? GatherArgs{s.dw, dwp, c, s.lda, dim, s.w_splits} : GatherArgs{}, bf16});
     }
-    if (!whole)
-        l.add(launch_gather, GatherArgs{s.dx, dx, rows, s.lda, dim, v->vocab > 0 ? s.x_splits : 0, bf16});
     return l.finish();
 }
 

@@ -110,8 +110,6 @@ struct RowsArgs {
     float scale;
     float2 *row;
 };
-hipError_t launch_rows(const Op &, hipStream_t);
-
 // dz of one piece of the vocabulary; of distillation without its targets.
 // Operands in 16-byte chunks.
 struct DzArgs {
@@ -141,9 +139,16 @@ struct AlignArgs {
     const void *in;      // [rows][cols]
     void *out;           // [rows][ldo]
     int64_t rows, ldo;
-    int32_t cols, bf16;
+    int32_t cols;
 };
-hipError_t launch_align(const Op &, hipStream_t);
+
+// rows.prob, x.in, w.in: null where there is nothing to do; not all of them are.
+struct PrepareArgs {
+    RowsArgs rows;
+    AlignArgs x, w;
+    int32_t bf16;
+};
+hipError_t launch_prepare(const Op &, hipStream_t);
 
 // A product, A tall, stored as the element type, or in fp32 as one sum for each
 // of the `splits` parts of k.  Operands in 16-byte chunks.
@@ -154,17 +159,25 @@ struct StoreArgs {
     float *acc;          // not null: [splits][nj][lda] instead of out
     int64_t lda;         // a multiple of 4
     int32_t splits, add; // add: to what acc holds
-    int32_t tall_b;
+};
+// dx = (w, dz), dw = (x, dz), the second with a tall B too.
+struct StoresArgs {
+    StoreArgs x, w;
 };
 int32_t product_splits(const Product &p, bool tall_b);
-hipError_t launch_store(const Op &, hipStream_t);
+hipError_t launch_stores(const Op &, hipStream_t);
 
 // out = the sum of the partial sums (none: zero).
 struct GatherArgs {
     const float *acc;    // [splits][rows][lda]
     void *out;           // [rows][dim]
     int64_t rows, lda;
-    int32_t dim, splits, bf16;
+    int32_t dim, splits;
+};
+// out: null where there is nothing to do, not for both.
+struct GathersArgs {
+    GatherArgs x, w;
+    int32_t bf16;
 };
 hipError_t launch_gather(const Op &, hipStream_t);
 

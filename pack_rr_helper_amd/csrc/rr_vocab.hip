@@ -246,20 +246,6 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(CombineArgs a)
     }
 }
 
-// One wave per row.
-__global__ __launch_bounds__(kThreads) void rows_kernel(RowsArgs a)
-{
-    const int64_t j = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
-    if (j >= a.rows)
-        return;
-    bool used = false;
-    for (int e = threadIdx.x % 64; e < a.topk; e += 64)
-        used |= a.prob[j * a.topk + e] != 0.0f;
-    used = __ballot(used) != 0;
-    if (threadIdx.x % 64 == 0)
-        a.row[j] = used ? float2{a.lse[j] * kLog2e, a.grad[j] * a.scale} : float2{0.0f, 0.0f};
-}
-
 __device__ __forceinline__ int round64(int n) { return (n + 63) / 64 * 64; }
 
 // dz = coefficient * exp(z - lse), zero past the piece up to the next multiple
@@ -379,13 +365,26 @@ __global__ __launch_bounds__(kThreads) void targets_kernel(TargetArgs a)
     }
 }
 
-// One wave per row at a time: 174 MB in 56 us, 6.2 TB/s both ways.
+// One wave per row.
+__device__ void fill_row(const RowsArgs &a, int64_t j)
+{
+    if (j >= a.rows)
+        return;
+    bool used = false;
+    for (int e = threadIdx.x % 64; e < a.topk; e += 64)
+        used |= a.prob[j * a.topk + e] != 0.0f;
+    used = __ballot(used) != 0;
+    if (threadIdx.x % 64 == 0)
+        a.row[j] = used ? float2{a.lse[j] * kLog2e, a.grad[j] * a.scale} : float2{0.0f, 0.0f};
+}
+
+// One wave per row at a time, from row `first` in steps of `waves`: 174 MB in
+// 56 us, 6.2 TB/s both ways.
 template <int ES>
-__global__ __launch_bounds__(kThreads) void align_kernel(AlignArgs a)
+__device__ void align_rows(const AlignArgs &a, int64_t first, int64_t waves)
 {
     const int lane = threadIdx.x % 64, bytes = a.cols * ES;
-    const int64_t waves = int64_t(gridDim.x) * (kThreads / 64);
-    for (int64_t r = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64; r < a.rows; r += waves) {
+    for (int64_t r = first; r < a.rows; r += waves) {
         const char *from = static_cast<const char *>(a.in) + r * bytes;
         char *to = static_cast<char *>(a.out) + r * a.ldo * ES;
         for (int c = lane * 16; c < bytes; c += 64 * 16)
@@ -393,14 +392,34 @@ __global__ __launch_bounds__(kThreads) void align_kernel(AlignArgs a)
     }
 }
 
-// dw and dx: 4096 x 2048 x 32000 in bf16 in 455-470 us each, 1.15 PFLOP/s.
-template <typename T>
-__global__ __launch_bounds__(T::kThreads) void store_kernel(StoreArgs a, int tiles_i, int tiles_j)
+// What a gradient needs first: the rows' factors, and copies of x and w in
+// 16-byte chunks, each by its own workgroups of one launch.
+template <int ES>
+__global__ __launch_bounds__(kThreads) void prepare_kernel(PrepareArgs a, int rows_blocks, int x_blocks)
 {
-    __shared__ __attribute__((aligned(1024))) char lds[T::kLdsBytes];
-    const int tiles = tiles_i * tiles_j, split = blockIdx.x / tiles;
+    constexpr int kWaves = kThreads / 64;
+    int b = blockIdx.x;
+    const int wave = threadIdx.x / 64;
+    if (b < rows_blocks) {
+        fill_row(a.rows, int64_t(b) * kWaves + wave);
+        return;
+    }
+    b -= rows_blocks;
+    if (b < x_blocks)
+        align_rows<ES>(a.x, int64_t(b) * kWaves + wave, int64_t(x_blocks) * kWaves);
+    else
+        align_rows<ES>(a.w, int64_t(b - x_blocks) * kWaves + wave,
+                       int64_t(int(gridDim.x) - rows_blocks - x_blocks) * kWaves);
+}
+
+// Tile `block` of dw or dx.
+template <typename T>
+__device__ __forceinline__ void store_tile(const StoreArgs &a, int block, char *lds)
+{
+    const int tiles_i = (a.p.ni - 1) / T::TI + 1, tiles_j = (a.p.nj - 1) / T::TJ + 1;
+    const int tiles = tiles_i * tiles_j, split = block / tiles;
     int ti, tj;
-    tile_at(blockIdx.x - split * tiles, tiles, tiles_i, tiles_j, ti, tj);
+    tile_at(block - split * tiles, tiles, tiles_i, tiles_j, ti, tj);
     const int i0 = ti * T::TI, j0 = tj * T::TJ;
     const int steps = (a.p.nk + T::kStep - 1) / T::kStep, per = (steps + a.splits - 1) / a.splits;
     const int s0 = split * per < steps ? split * per : steps, s1 = s0 + per < steps ? s0 + per : steps;
@@ -440,16 +459,36 @@ __global__ __launch_bounds__(T::kThreads) void store_kernel(StoreArgs a, int til
     }
 }
 
+// 4096 x 2048 x 32000 in bf16 in 455-470 us, 1.15 PFLOP/s.
+template <typename T>
+__global__ __launch_bounds__(T::kThreads) void store_kernel(StoreArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[T::kLdsBytes];
+    store_tile<T>(a, blockIdx.x, lds);
+}
+
+// dx and dw in one launch, where neither fills the compute units for long.
+template <typename TX, typename TW>
+__global__ __launch_bounds__(TX::kThreads) void stores_kernel(StoresArgs a, int x_blocks)
+{
+    static_assert(TX::kThreads == TW::kThreads, "");
+    __shared__ __attribute__((aligned(1024))) char lds[TX::kLdsBytes > TW::kLdsBytes ? TX::kLdsBytes : TW::kLdsBytes];
+    if (int(blockIdx.x) < x_blocks)
+        store_tile<TX>(a.x, blockIdx.x, lds);
+    else
+        store_tile<TW>(a.w, blockIdx.x - x_blocks, lds);
+}
+
 // Four columns of a row per PARTS threads, each of which takes its share of the
 // sums: with 256 parts of 35 x 192 in 14 us by one thread each, in 4 us by eight.
 template <bool BF16, int PARTS>
-__global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a)
+__device__ __forceinline__ void gather(const GatherArgs &a, int block, int blocks)
 {
     constexpr int kWide = kThreads / PARTS;
     __shared__ f32x4 sums[kThreads];
     const int part = threadIdx.x / kWide;
     const int64_t wide = a.lda / 4, n = a.rows * wide, stride = a.rows * a.lda;
-    for (int64_t t0 = int64_t(blockIdx.x) * kWide; t0 < n; t0 += int64_t(gridDim.x) * kWide) {
+    for (int64_t t0 = int64_t(block) * kWide; t0 < n; t0 += int64_t(blocks) * kWide) {
         const int64_t t = t0 + threadIdx.x % kWide, row = t / wide;
         const int col = int(t - row * wide) * 4;
         f32x4 s{0.0f, 0.0f, 0.0f, 0.0f};
@@ -473,6 +512,16 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(GatherArgs a)
                 if (col + e < a.dim)
                     store<BF16>(a.out, row * a.dim + col + e, s[e]);
     }
+}
+
+// The first x_blocks workgroups join dx, the others dw.
+template <bool BF16, int PARTS>
+__global__ __launch_bounds__(kThreads) void gather_kernel(GathersArgs a, int x_blocks)
+{
+    if (int(blockIdx.x) < x_blocks)
+        gather<BF16, PARTS>(a.x, blockIdx.x, x_blocks);
+    else
+        gather<BF16, PARTS>(a.w, blockIdx.x - x_blocks, gridDim.x - x_blocks);
 }
 
 unsigned blocks(int64_t n, int64_t per) { return unsigned((n + per - 1) / per); }
@@ -551,7 +600,10 @@ using Rows = Tile<BF16, 128, TJ, 4, 1, DIRECT ? STAGES : 2, DIRECT, TA, TB>;
 template <bool BF16, bool DIRECT, bool TA, bool TB> using Mid = Tile<BF16, 128, 128, 2, 2, 2, DIRECT, TA, TB>;
 template <bool BF16, bool DIRECT, bool TA, bool TB> using Big = Tile<BF16, 256, 256, 2, 4, 2, DIRECT, TA, TB>;
 
-// f(tile type).
+// f(tile type).  For few rows a third step in LDS covers the latency of the
+// streamed weights (20 x 4096 x 32000 in bf16: 47 us against 49 us); in fp32,
+// which the matrix units bound, a third workgroup on a compute unit is worth
+// more (777 x 1000 x 5004 training: 360 us against 390 us).
 template <bool BF16, bool DIRECT, bool TA, bool TB, typename F>
 hipError_t with_shape(Shape s, F f)
 {
@@ -559,11 +611,11 @@ hipError_t with_shape(Shape s, F f)
         if (s == kRows16)
             return f(Rows<BF16, 16, 3, DIRECT, TA, TB>{});
         if (s == kRows32)
-            return f(Rows<BF16, 32, 3, DIRECT, TA, TB>{});
+            return f(Rows<BF16, 32, BF16 ? 3 : 2, DIRECT, TA, TB>{});
     }
     if constexpr (!(TB && BF16))
         if (s == kRows64)
-            return f(Rows<BF16, 64, 3, DIRECT, TA, TB>{});
+            return f(Rows<BF16, 64, BF16 ? 3 : 2, DIRECT, TA, TB>{});
     if constexpr (BF16)
         if (s == kBig)
             return f(Big<BF16, DIRECT, TA, TB>{});
@@ -643,12 +695,6 @@ hipError_t launch_distill(const Op &op, hipStream_t stream)
     RR_LAUNCH(distill_kernel<false>, grid, a);
 }
 
-hipError_t launch_rows(const Op &op, hipStream_t stream)
-{
-    const RowsArgs a = op.get<RowsArgs>();
-    RR_LAUNCH(rows_kernel, dim3(blocks(a.rows, kThreads / 64)), a);
-}
-
 hipError_t launch_dz(const Op &op, hipStream_t stream)
 {
     const DzArgs a = op.get<DzArgs>();
@@ -670,47 +716,89 @@ hipError_t launch_targets(const Op &op, hipStream_t stream)
     RR_LAUNCH(targets_kernel<false>, grid, a);
 }
 
-hipError_t launch_align(const Op &op, hipStream_t stream)
+hipError_t launch_prepare(const Op &op, hipStream_t stream)
 {
-    const AlignArgs a = op.get<AlignArgs>();
-    const unsigned all = blocks(a.rows, kThreads / 64);
-    const dim3 grid(all < 8192u ? all : 8192u);
+    const PrepareArgs a = op.get<PrepareArgs>();
+    const auto some = [](const AlignArgs &m) {
+        const unsigned n = m.in ? blocks(m.rows, kThreads / 64) : 0;
+        return n < 8192u ? n : 8192u;
+    };
+    const unsigned r = a.rows.prob ? blocks(a.rows.rows, kThreads / 64) : 0, x = some(a.x), w = some(a.w);
+    (void)hipGetLastError();
     if (a.bf16)
-        RR_LAUNCH(align_kernel<2>, grid, a);
-    RR_LAUNCH(align_kernel<4>, grid, a);
+        prepare_kernel<2><<<dim3(r + x + w), dim3(kThreads), 0, stream>>>(a, r, x);
+    else
+        prepare_kernel<4><<<dim3(r + x + w), dim3(kThreads), 0, stream>>>(a, r, x);
+    return hipGetLastError();
 }
 
 int32_t product_splits(const Product &p, bool tall_b) { return form_of(p, true, tall_b).splits; }
 
-hipError_t launch_store(const Op &op, hipStream_t stream)
+namespace {
+
+template <typename T>
+unsigned store_blocks(const StoreArgs &a)
 {
-    const StoreArgs a = op.get<StoreArgs>();
+    return unsigned(tiles(a.p.ni, T::TI)) * unsigned(tiles(a.p.nj, T::TJ)) * unsigned(a.splits);
+}
+
+template <bool BF16>
+hipError_t stores(const StoresArgs &a, hipStream_t stream)
+{
+    const Shape sx = form_of(a.x.p, true, false).shape, sw = form_of(a.w.p, true, true).shape;
+    if (sx == kBig || sw == kBig) {
+        const auto go = [&](const StoreArgs &s) {
+            return [&s, stream](auto t) {
+                using T = decltype(t);
+                store_kernel<T><<<dim3(store_blocks<T>(s)), dim3(T::kThreads), 0, stream>>>(s);
+                return hipGetLastError();
+            };
+        };
+        const hipError_t e = with_shape<BF16, true, true, false>(sx, go(a.x));
+        return e == hipSuccess ? with_shape<BF16, true, true, true>(sw, go(a.w)) : e;
+    }
+    return with_shape<BF16, true, true, false>(sx, [&](auto tx) {
+        return with_shape<BF16, true, true, true>(sw, [&](auto tw) {
+            using TX = decltype(tx);
+            using TW = decltype(tw);
+            if constexpr (TX::kThreads == TW::kThreads && TX::kThreads == 256) {
+                const unsigned x = store_blocks<TX>(a.x);
+                stores_kernel<TX, TW><<<dim3(x + store_blocks<TW>(a.w)), dim3(TX::kThreads), 0, stream>>>(a, x);
+                return hipGetLastError();
+            } else {
+                return hipErrorInvalidValue;
+            }
+        });
+    });
+}
+
+}  // namespace
+
+hipError_t launch_stores(const Op &op, hipStream_t stream)
+{
+    const StoresArgs a = op.get<StoresArgs>();
     (void)hipGetLastError();
-    const auto go = [&](auto t) {
-        using T = decltype(t);
-        const int ti = tiles(a.p.ni, T::TI), tj = tiles(a.p.nj, T::TJ);
-        store_kernel<T><<<dim3(unsigned(ti) * unsigned(tj) * unsigned(a.splits)), dim3(T::kThreads), 0, stream>>>(a, ti, tj);
-        return hipGetLastError();
-    };
-    const Shape s = form_of(a.p, true, a.tall_b).shape;
-    if (a.tall_b)
-        return a.p.bf16 ? with_shape<true, true, true, true>(s, go) : with_shape<false, true, true, true>(s, go);
-    return a.p.bf16 ? with_shape<true, true, true, false>(s, go) : with_shape<false, true, true, false>(s, go);
+    return a.x.p.bf16 ? stores<true>(a, stream) : stores<false>(a, stream);
 }
 
 hipError_t launch_gather(const Op &op, hipStream_t stream)
 {
-    const GatherArgs a = op.get<GatherArgs>();
-    const bool many = a.splits >= 16;
-    const unsigned all = blocks(a.rows * (a.lda / 4), many ? kThreads / 8 : kThreads);
-    const dim3 grid(all < 4096u ? all : 4096u);
-    if (a.bf16 && many)
-        RR_LAUNCH((gather_kernel<true, 8>), grid, a);
-    if (a.bf16)
-        RR_LAUNCH((gather_kernel<true, 1>), grid, a);
-    if (many)
-        RR_LAUNCH((gather_kernel<false, 8>), grid, a);
-    RR_LAUNCH((gather_kernel<false, 1>), grid, a);
+    const GathersArgs a = op.get<GathersArgs>();
+    const bool many = a.x.splits >= 16 || a.w.splits >= 16;
+    const auto some = [&](const GatherArgs &g) {
+        const unsigned n = g.out ? blocks(g.rows * (g.lda / 4), many ? kThreads / 8 : kThreads) : 0;
+        return n < 4096u ? n : 4096u;
+    };
+    const unsigned x = some(a.x), w = some(a.w);
+    (void)hipGetLastError();
+    const auto go = [&](auto bf16) {
+        if (many)
+            gather_kernel<decltype(bf16)::value, 8><<<dim3(x + w), dim3(kThreads), 0, stream>>>(a, x);
+        else
+            gather_kernel<decltype(bf16)::value, 1><<<dim3(x + w), dim3(kThreads), 0, stream>>>(a, x);
+        return hipGetLastError();
+    };
+    return a.bf16 ? go(std::true_type{}) : go(std::false_type{});
 }
 
 }  // namespace rr
