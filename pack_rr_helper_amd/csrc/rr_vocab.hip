@@ -110,11 +110,48 @@ __device__ __forceinline__ float2 join(float2 a, float2 b)
     return float2{top, a.y * fa + b.y * fb};
 }
 
-// The first `joins` workgroups join the parts of `wide` rows each (a power of
-// two up to 64), the others compute the logits of one entry per G lanes.  Bound
-// by the entries' rows of w: 4096 x 64 of 4 KiB in 118-134 us, 8 TB/s from the
-// last level cache.
+// x . w over G lanes, x and w in the element type; the sum in every lane.
 template <bool BF16, int G>
+__device__ __forceinline__ float dot(const char *x, const char *w, int dim)
+{
+    constexpr int kEs = BF16 ? 2 : 4, kPer = 16 / kEs;
+    float z = 0.0f;
+#pragma unroll 4
+    for (int k = threadIdx.x % G * kPer; k < dim; k += G * kPer) {
+        const u32x4 u = load_chunk<kEs>(x + k * kEs, (dim - k) * kEs), v = load_chunk<kEs>(w + k * kEs, (dim - k) * kEs);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (BF16) {
+                z = __builtin_fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), z);
+                z = __builtin_fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(v[e] & 0xffff0000u), z);
+            } else {
+                z = __builtin_fmaf(__uint_as_float(u[e]), __uint_as_float(v[e]), z);
+            }
+        }
+    }
+    return lanes_sum<G>(z);
+}
+
+// picked[n] by G lanes, x being n's row.
+template <bool BF16, int G>
+__device__ __forceinline__ void pick(const StatsDoneArgs &a, int64_t n, const char *x)
+{
+    const int64_t i = a.index[n] - a.first;
+    float z = 0.0f;
+    if (i >= 0 && i < a.vocab)
+        z = dot<BF16, G>(x, static_cast<const char *>(a.w) + i * a.dim * (BF16 ? 2 : 4), a.dim) * a.scale;
+    if (threadIdx.x % G == 0)
+        a.picked[n] = z;
+}
+
+constexpr int kRowEntries = 64;  // of a row that one workgroup takes
+
+// The first `joins` workgroups join the parts of `wide` rows each (a power of
+// two up to 64), the others compute the logits of one entry per G lanes.  Of
+// many entries a row, a workgroup takes up to 64 and keeps the row's x in LDS
+// (SHARED), which leaves the first-level cache to w.  Bound by the entries' rows
+// of w: 4096 x 64 of 4 KiB in 118-134 us, 8 TB/s from the last level cache.
+template <bool BF16, int G, bool SHARED>
 __global__ __launch_bounds__(kThreads) void stats_done_kernel(StatsDoneArgs a, int joins, int wide)
 {
     __shared__ float2 sums[kThreads];
@@ -144,32 +181,27 @@ __global__ __launch_bounds__(kThreads) void stats_done_kernel(StatsDoneArgs a, i
             a.stats[row] = sums[threadIdx.x];
         return;
     }
-    constexpr int kEs = BF16 ? 2 : 4, kPer = 16 / kEs;
-    const int lane = threadIdx.x % G;
-    const int64_t entries = int64_t(a.rows) * a.topk, step = int64_t(gridDim.x - joins) * (kThreads / G);
-    for (int64_t n = (int64_t(blockIdx.x) - joins) * (kThreads / G) + threadIdx.x / G; n < entries; n += step) {
-        const int64_t i = a.index[n] - a.first;
-        float z = 0.0f;
-        if (i >= 0 && i < a.vocab) {
-            const char *x = static_cast<const char *>(a.x) + n / a.topk * a.dim * kEs;
-            const char *w = static_cast<const char *>(a.w) + i * a.dim * kEs;
-#pragma unroll 4
-            for (int k = lane * kPer; k < a.dim; k += G * kPer) {
-                const u32x4 u = load_chunk<kEs>(x + k * kEs, (a.dim - k) * kEs), v = load_chunk<kEs>(w + k * kEs, (a.dim - k) * kEs);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (BF16) {
-                        z = __builtin_fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), z);
-                        z = __builtin_fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(v[e] & 0xffff0000u), z);
-                    } else {
-                        z = __builtin_fmaf(__uint_as_float(u[e]), __uint_as_float(v[e]), z);
-                    }
-                }
-            }
-            z = lanes_sum<G>(z) * a.scale;
+    constexpr int kEs = BF16 ? 2 : 4, kGroups = kThreads / G;
+    const int64_t first = int64_t(blockIdx.x) - joins, step = int64_t(gridDim.x) - joins;
+    const int group = threadIdx.x / G;
+    const char *x = static_cast<const char *>(a.x);
+    if constexpr (SHARED) {
+        extern __shared__ __attribute__((aligned(16))) char row[];
+        const int per = (a.topk + kRowEntries - 1) / kRowEntries, bytes = a.dim * kEs;
+        for (int64_t b = first; b < int64_t(a.rows) * per; b += step) {
+            const int64_t r = b / per;
+            const int e0 = int(b - r * per) * kRowEntries, e1 = a.topk - e0 < kRowEntries ? a.topk : e0 + kRowEntries;
+            for (int c = threadIdx.x * 16; c < bytes; c += kThreads * 16)
+                *reinterpret_cast<u32x4 *>(row + c) = load_chunk<kEs>(x + r * bytes + c, bytes - c);
+            __syncthreads();
+            for (int e = e0 + group; e < e1; e += kGroups)
+                pick<BF16, G>(a, r * a.topk + e, row);
+            __syncthreads();
         }
-        if (lane == 0)
-            a.picked[n] = z;
+    } else {
+        const int64_t entries = int64_t(a.rows) * a.topk;
+        for (int64_t n = first * kGroups + group; n < entries; n += step * kGroups)
+            pick<BF16, G>(a, n, x + n / a.topk * a.dim * kEs);
     }
 }
 
@@ -664,17 +696,26 @@ hipError_t launch_stats_done(const Op &op, hipStream_t stream)
     int wide = 1;
     while (wide < 64 && a.rows / wide > 512)
         wide *= 2;
-    // 16 lanes an entry once that fills the compute units
-    const int64_t all = int64_t(a.rows) * a.topk;
+    // 16 lanes an entry once that fills the compute units; x shared where
+    // workgroups of a row fill them too and it is long (bf16 with its joins:
+    // 3596 x 2112 x 1292 with 64 entries 100 us against 115 us for scoring, but
+    // 310 x 3328 x 1228 with 100 entries 52 us against 41 us and 7722 x 128 x
+    // 4690 78 us against 75 us)
+    const int64_t all = int64_t(a.rows) * a.topk, bytes = int64_t(a.dim) * (a.bf16 ? 2 : 4);
+    const int64_t of_rows = int64_t(a.rows) * ((a.topk + kRowEntries - 1) / kRowEntries);
+    const bool shared = a.topk >= 8 && of_rows >= 2048 && bytes >= 1024 && bytes <= 32768;
     const int lanes = all < 8192 ? 64 : 16;
-    const unsigned joins = blocks(a.rows, wide), entries = blocks(all, kThreads / lanes),
+    const unsigned joins = blocks(a.rows, wide), entries = shared ? blocks(of_rows, 1) : blocks(all, kThreads / lanes),
                    grid = joins + (entries < 65536u ? entries : 65536u);
     (void)hipGetLastError();
     const auto go = [&](auto bf16) {
-        if (lanes == 64)
-            stats_done_kernel<decltype(bf16)::value, 64><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
+        if (shared)
+            stats_done_kernel<decltype(bf16)::value, 16, true>
+                <<<dim3(grid), dim3(kThreads), size_t(bytes + 15) / 16 * 16, stream>>>(a, joins, wide);
+        else if (lanes == 64)
+            stats_done_kernel<decltype(bf16)::value, 64, false><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
         else
-            stats_done_kernel<decltype(bf16)::value, 16><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
+            stats_done_kernel<decltype(bf16)::value, 16, false><<<dim3(grid), dim3(kThreads), 0, stream>>>(a, joins, wide);
         return hipGetLastError();
     };
     return a.bf16 ? go(std::true_type{}) : go(std::false_type{});

@@ -176,3 +176,9 @@ def test_sharded_step_gradients():
     for got, want in ((s.dlogits, logits.grad), (s.dhead, head.grad)):
         assert (got.double() - want).abs().max() <= 512 * ref.U * want.abs().max()
     assert rr.load() is not None
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("rows,dim,topk", [(2100, 520, 9), (1100, 601, 65)], ids=str)
+def test_distill_rows_shared_by_a_workgroup(dt, rows, dim, topk):
+    Head(dt, rows, dim, 400, sizes=[150, 250], topk=topk, scale=0.5, distill=True).run()
