@@ -140,7 +140,7 @@ struct GradSpace {
     int64_t piece, ldd, ldv, lda;
     int32_t pieces, x_splits, w_splits;
     float2 *row;
-    char *x, *w, *dz;    // x, w: copies in 16-byte chunks, of operands that are not
+    char *x, *w, *dz;    // x without the rows that have no target; a piece of w, if not in 16-byte chunks
     float *dx, *dw;      // parts of the gradients' sums
     int64_t bytes;
 };
@@ -371,6 +371,7 @@ rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *
     const RowsArgs of_rows{index, lse, prob, grad, n, v->topk, v->total, v->scale, s.row};
     const bool copy_x = !in_chunks(x, dim, es), copy_w = !in_chunks(w, dim, es);
     const bool whole = s.pieces == 1 && s.x_splits == 1, parts = s.w_splits > 1;  // of dx, of dw
+    const AlignArgs x_copy{x, s.x, rows, s.ldd, dim};
     const void *xc = copy_x ? s.x : x;
     const int64_t ldx = copy_x ? s.ldd : dim, ldw = copy_w ? s.ldd : dim;
     if (v->vocab == 0)
@@ -381,16 +382,17 @@ rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *
         const void *wp = static_cast<const char *>(w) + v0 * dim * es, *wc = copy_w ? s.w : wp;
         char *dwp = static_cast<char *>(dw) + v0 * dim * es;
         if (copy_w || (first && (copy_x || prob)))
-            l.add(launch_prepare, PrepareArgs{first && prob ? of_rows : RowsArgs{},
-                                              first && copy_x ? AlignArgs{x, s.x, rows, s.ldd, dim} : AlignArgs{},
-                                              copy_w ? AlignArgs{wp, s.w, c, s.ldd, dim} : AlignArgs{}, bf16});
-        l.add(launch_dz, DzArgs{Product{wc, xc, ldw, ldx, c, n, dim, bf16}, of_rows, logit, v->first + v0, s.dz, s.ldv});
+            l.add(launch_prepare, PrepareArgs{of_rows, first && copy_x ? x_copy : AlignArgs{},
+                                              copy_w ? AlignArgs{wp, s.w, c, s.ldd, dim} : AlignArgs{},
+                                              first && prob, bf16});
+        l.add(launch_dz, DzArgs{Product{wc, xc, ldw, ldx, c, n, dim, bf16}, of_rows, logit, v->first + v0, s.dz, s.ldv,
+                                first && !copy_x ? x_copy : AlignArgs{}});
         if (prob)
             l.add(launch_targets, TargetArgs{index, logit, prob, s.row, n, v->topk, c, bf16, v->first + v0, s.dz, s.ldv});
         l.add(launch_stores, StoresArgs{
             StoreArgs{Product{wc, s.dz, ldw, s.ldv, dim, n, c, bf16}, whole ? dx : nullptr, dim, whole ? nullptr : s.dx,
                       s.lda, s.x_splits, !first},
-            StoreArgs{Product{xc, s.dz, ldx, s.ldv, dim, c, n, bf16}, parts ? nullptr : dwp, dim,
+            StoreArgs{Product{s.x, s.dz, s.ldd, s.ldv, dim, c, n, bf16}, parts ? nullptr : dwp, dim,
                       parts ? s.dw : nullptr, s.lda, s.w_splits, 0}});
         if (parts || (last && !whole))
             l.add(launch_gather, GathersArgs{

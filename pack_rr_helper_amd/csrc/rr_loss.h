@@ -110,6 +110,14 @@ struct RowsArgs {
     float scale;
     float2 *row;
 };
+// A matrix copied to rows that start at multiples of 16 bytes and end in zeros.
+struct AlignArgs {
+    const void *in;      // [rows][cols]
+    void *out;           // [rows][ldo]
+    int64_t rows, ldo;
+    int32_t cols;
+};
+
 // dz of one piece of the vocabulary; of distillation without its targets.
 // Operands in 16-byte chunks.
 struct DzArgs {
@@ -119,6 +127,7 @@ struct DzArgs {
     int64_t first;       // the piece's first entry of the vocabulary
     void *dz;            // [nj][ldz]
     int64_t ldz;
+    AlignArgs x;         // in not null: x copied beside, rows without a target as zeros
 };
 hipError_t launch_dz(const Op &, hipStream_t);
 
@@ -134,19 +143,12 @@ struct TargetArgs {
 };
 hipError_t launch_targets(const Op &, hipStream_t);
 
-// A matrix copied to rows that start at multiples of 16 bytes and end in zeros.
-struct AlignArgs {
-    const void *in;      // [rows][cols]
-    void *out;           // [rows][ldo]
-    int64_t rows, ldo;
-    int32_t cols;
-};
-
-// rows.prob, x.in, w.in: null where there is nothing to do; not all of them are.
+// factors: fill rows.row; x.in, w.in: null where there is nothing to copy.  Rows
+// of x without a target become zeros.
 struct PrepareArgs {
     RowsArgs rows;
     AlignArgs x, w;
-    int32_t bf16;
+    int32_t factors, bf16;
 };
 hipError_t launch_prepare(const Op &, hipStream_t);
 

@@ -278,14 +278,44 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(CombineArgs a)
     }
 }
 
+// Whether row j has a target; by a whole wave.
+__device__ __forceinline__ bool has_target(const RowsArgs &a, int64_t j)
+{
+    bool used = false;
+    if (a.prob) {
+        for (int e = threadIdx.x % 64; e < a.topk; e += 64)
+            used |= a.prob[j * a.topk + e] != 0.0f;
+    } else {
+        used = counts(a.index[j], a.total);
+    }
+    return __ballot(used) != 0;
+}
+
+// One wave per row at a time, from row `first` in steps of `waves`: 174 MB in
+// 56 us, 6.2 TB/s both ways.  Where `of` is given, rows without a target become
+// zeros: dw is then free of whatever they hold.
+template <int ES>
+__device__ __forceinline__ void align_rows(const AlignArgs &a, const RowsArgs *of, int64_t first, int64_t waves)
+{
+    const int lane = threadIdx.x % 64, bytes = a.cols * ES;
+    for (int64_t r = first; r < a.rows; r += waves) {
+        const char *from = static_cast<const char *>(a.in) + r * bytes;
+        char *to = static_cast<char *>(a.out) + r * a.ldo * ES;
+        const int have = !of || has_target(*of, r) ? bytes : 0;
+        for (int c = lane * 16; c < bytes; c += 64 * 16)
+            *reinterpret_cast<u32x4 *>(to + c) = load_chunk<ES>(from + c, have - c);
+    }
+}
+
 __device__ __forceinline__ int round64(int n) { return (n + 63) / 64 * 64; }
 
 // dz = coefficient * exp(z - lse), zero past the piece up to the next multiple
-// of 64.  4096 x 2048 x 32000 in bf16: 464-480 us, 1.1 PFLOP/s, of which the
+// of 64; the first `copies` workgroups copy x for dw meanwhile.  4096 x 2048 x
+// 32000 in bf16: 464-480 us, 1.1 PFLOP/s, of which the
 // statistics' kernel takes 415 us.  bf16 keeps dz at 8 bits for the products: each gradient sums many of
 // these roundings, which leaves it within its own.
 template <typename T>
-__global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, int tiles_j)
+__global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, int tiles_j, int copies)
 {
     // a row's factors, its target within the piece (-1: none) and dz there
     struct Row {
@@ -295,8 +325,13 @@ __global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, 
     };
     __shared__ __attribute__((aligned(1024))) char lds[T::kLdsBytes];
     __shared__ Row rows[T::TJ];
+    constexpr int kWaves = T::kThreads / 64;
+    if (int(blockIdx.x) < copies) {
+        align_rows<T::kEs>(a.x, &a.rows, int64_t(blockIdx.x) * kWaves + threadIdx.x / 64, int64_t(copies) * kWaves);
+        return;
+    }
     int ti, tj;
-    tile_at(blockIdx.x, gridDim.x, tiles_i, tiles_j, ti, tj);
+    tile_at(blockIdx.x - copies, gridDim.x - copies, tiles_i, tiles_j, ti, tj);
     const int i0 = ti * T::TI, j0 = tj * T::TJ;
     // this thread's row, at a clamped place; its loads fly together with the tile's first
     const int mine = j0 + int(threadIdx.x), in = mine < a.p.nj ? mine : 0;
@@ -397,33 +432,6 @@ __global__ __launch_bounds__(kThreads) void targets_kernel(TargetArgs a)
     }
 }
 
-// One wave per row.
-__device__ void fill_row(const RowsArgs &a, int64_t j)
-{
-    if (j >= a.rows)
-        return;
-    bool used = false;
-    for (int e = threadIdx.x % 64; e < a.topk; e += 64)
-        used |= a.prob[j * a.topk + e] != 0.0f;
-    used = __ballot(used) != 0;
-    if (threadIdx.x % 64 == 0)
-        a.row[j] = used ? float2{a.lse[j] * kLog2e, a.grad[j] * a.scale} : float2{0.0f, 0.0f};
-}
-
-// One wave per row at a time, from row `first` in steps of `waves`: 174 MB in
-// 56 us, 6.2 TB/s both ways.
-template <int ES>
-__device__ void align_rows(const AlignArgs &a, int64_t first, int64_t waves)
-{
-    const int lane = threadIdx.x % 64, bytes = a.cols * ES;
-    for (int64_t r = first; r < a.rows; r += waves) {
-        const char *from = static_cast<const char *>(a.in) + r * bytes;
-        char *to = static_cast<char *>(a.out) + r * a.ldo * ES;
-        for (int c = lane * 16; c < bytes; c += 64 * 16)
-            *reinterpret_cast<u32x4 *>(to + c) = load_chunk<ES>(from + c, bytes - c);
-    }
-}
-
 // What a gradient needs first: the rows' factors, and copies of x and w in
 // 16-byte chunks, each by its own workgroups of one launch.
 template <int ES>
@@ -433,14 +441,19 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(PrepareArgs a, int ro
     int b = blockIdx.x;
     const int wave = threadIdx.x / 64;
     if (b < rows_blocks) {
-        fill_row(a.rows, int64_t(b) * kWaves + wave);
+        const int64_t j = int64_t(b) * kWaves + wave;
+        if (j >= a.rows.rows)
+            return;
+        const bool used = has_target(a.rows, j);
+        if (threadIdx.x % 64 == 0)
+            a.rows.row[j] = used ? float2{a.rows.lse[j] * kLog2e, a.rows.grad[j] * a.rows.scale} : float2{0.0f, 0.0f};
         return;
     }
     b -= rows_blocks;
     if (b < x_blocks)
-        align_rows<ES>(a.x, int64_t(b) * kWaves + wave, int64_t(x_blocks) * kWaves);
+        align_rows<ES>(a.x, &a.rows, int64_t(b) * kWaves + wave, int64_t(x_blocks) * kWaves);
     else
-        align_rows<ES>(a.w, int64_t(b - x_blocks) * kWaves + wave,
+        align_rows<ES>(a.w, nullptr, int64_t(b - x_blocks) * kWaves + wave,
                        int64_t(int(gridDim.x) - rows_blocks - x_blocks) * kWaves);
 }
 
@@ -743,7 +756,9 @@ hipError_t launch_dz(const Op &op, hipStream_t stream)
     return with_logits_tile<true>(a.p, [&](auto t) {
         using T = decltype(t);
         const int ti = tiles(a.p.ni, T::TI), tj = tiles(a.p.nj, T::TJ);
-        dz_kernel<T><<<dim3(unsigned(ti) * unsigned(tj)), dim3(T::kThreads), 0, stream>>>(a, ti, tj);
+        // x's copy by the first workgroups, a multiple of the eight dies
+        const unsigned waves = T::kThreads / 64, rows = a.x.in ? blocks(a.x.rows, 8 * waves) * 8 : 0, copies = rows < 256u ? rows : 256u;
+        dz_kernel<T><<<dim3(unsigned(ti) * unsigned(tj) + copies), dim3(T::kThreads), 0, stream>>>(a, ti, tj, int(copies));
         return hipGetLastError();
     });
 }
@@ -764,7 +779,7 @@ hipError_t launch_prepare(const Op &op, hipStream_t stream)
         const unsigned n = m.in ? blocks(m.rows, kThreads / 64) : 0;
         return n < 8192u ? n : 8192u;
     };
-    const unsigned r = a.rows.prob ? blocks(a.rows.rows, kThreads / 64) : 0, x = some(a.x), w = some(a.w);
+    const unsigned r = a.factors ? blocks(a.rows.rows, kThreads / 64) : 0, x = some(a.x), w = some(a.w);
     (void)hipGetLastError();
     if (a.bf16)
         prepare_kernel<2><<<dim3(r + x + w), dim3(kThreads), 0, stream>>>(a, r, x);

@@ -182,3 +182,25 @@ def test_sharded_step_gradients():
 @pytest.mark.parametrize("rows,dim,topk", [(2100, 520, 9), (1100, 601, 65)], ids=str)
 def test_distill_rows_shared_by_a_workgroup(dt, rows, dim, topk):
     Head(dt, rows, dim, 400, sizes=[150, 250], topk=topk, scale=0.5, distill=True).run()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("rows,dim,topk,lead", [(40, 64, 1, 0), (40, 64, 3, 0), (40, 65, 1, 0), (60, 72, 5, 1), (1100, 136, 1, 0)],
+                         ids=str)
+def test_rows_without_a_target_may_hold_anything(dt, bad, rows, dim, topk, lead):
+    """Their x takes no part in dw and gets no gradient, whatever it is."""
+    h = Head(dt, rows, dim, 13000 if rows > 1000 else 500, topk=topk, scale=0.5 if topk > 1 else 1.0, masked=0.3, lead=lead)
+    none = (h.index < 0).all(dim=1)
+    assert none.any() and not none.all()
+    h.x[none] = 0
+    h.make()
+    h.issue()
+    torch.cuda.synchronize()
+    clean = [h.dx[0].t.clone(), h.dw[0].t.clone(), h.loss.t.clone()]
+    h.x[none] = bad
+    h.make()
+    h.issue()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(clean, [h.dx[0].t, h.dw[0].t, h.loss.t]))
+    assert not h.dx[0].t[none].any()
