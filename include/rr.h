@@ -472,9 +472,10 @@ rr_status rr_vocab_distill(const rr_vocab *v, int dtype, int64_t rows, const int
  *   lse, logit: as written by the combining call; prob: its probabilities, or
  *     null for cross entropy (topk must be 1 then).
  *   dz[r][v] = grad[r] * scale * (exp(z - lse) - p), p the summed probability
- *     of the row's entries equal to v; a row with no target has dz = 0 whatever
- *     its logits and its x are, NaN included.  For bf16, dz is rounded to bf16
- *     before the two products.
+ *     of the row's entries equal to v; a row with no target, or whose grad *
+ *     scale is 0, has dz = 0 and no part in dw whatever its logits and its x
+ *     are, NaN included.  For bf16, dz is rounded to bf16 before the two
+ *     products.
  *   dx [rows][dim] = dz w, dw [vocab][dim] = dz^T x, rounded once.
  */
 rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *x, const void *w,

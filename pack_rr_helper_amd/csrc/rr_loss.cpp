@@ -140,7 +140,7 @@ struct GradSpace {
     int64_t piece, ldd, ldv, lda;
     int32_t pieces, x_splits, w_splits;
     float2 *row;
-    char *x, *w, *dz;    // x without the rows that have no target; a piece of w, if not in 16-byte chunks
+    char *x, *w, *dz;    // x without the rows that have no gradient; a piece of w, if not in 16-byte chunks
     float *dx, *dw;      // parts of the gradients' sums
     int64_t bytes;
 };

@@ -100,8 +100,9 @@ struct CombineArgs {
 hipError_t launch_cross_entropy(const Op &, hipStream_t);
 hipError_t launch_distill(const Op &, hipStream_t);
 
-// What makes a row's (lse in units of ln 2, grad * scale), zeros for a row
-// without a target; of distillation, row is filled with them first.
+// What makes a row's (lse in units of ln 2, grad * scale), both 0 for a row
+// without a gradient (no target, or grad * scale = 0); of distillation, row is
+// filled with them first.
 struct RowsArgs {
     const int64_t *index;
     const float *lse, *prob, *grad;  // prob: null for cross entropy
@@ -127,7 +128,7 @@ struct DzArgs {
     int64_t first;       // the piece's first entry of the vocabulary
     void *dz;            // [nj][ldz]
     int64_t ldz;
-    AlignArgs x;         // in not null: x copied beside, rows without a target as zeros
+    AlignArgs x;         // in not null: x copied beside, rows without a gradient as zeros
 };
 hipError_t launch_dz(const Op &, hipStream_t);
 
@@ -144,7 +145,7 @@ struct TargetArgs {
 hipError_t launch_targets(const Op &, hipStream_t);
 
 // factors: fill rows.row; x.in, w.in: null where there is nothing to copy.  Rows
-// of x without a target become zeros.
+// of x without a gradient become zeros.
 struct PrepareArgs {
     RowsArgs rows;
     AlignArgs x, w;

@@ -278,9 +278,12 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(CombineArgs a)
     }
 }
 
-// Whether row j has a target; by a whole wave.
-__device__ __forceinline__ bool has_target(const RowsArgs &a, int64_t j)
+// Whether row j has a gradient: a target, and a loss of some weight.  By a whole
+// wave.
+__device__ __forceinline__ bool has_gradient(const RowsArgs &a, int64_t j)
 {
+    if (a.grad[j] * a.scale == 0.0f)
+        return false;
     bool used = false;
     if (a.prob) {
         for (int e = threadIdx.x % 64; e < a.topk; e += 64)
@@ -292,7 +295,7 @@ __device__ __forceinline__ bool has_target(const RowsArgs &a, int64_t j)
 }
 
 // One wave per row at a time, from row `first` in steps of `waves`: 174 MB in
-// 56 us, 6.2 TB/s both ways.  Where `of` is given, rows without a target become
+// 56 us, 6.2 TB/s both ways.  Where `of` is given, rows without a gradient become
 // zeros: dw is then free of whatever they hold.
 template <int ES>
 __device__ __forceinline__ void align_rows(const AlignArgs &a, const RowsArgs *of, int64_t first, int64_t waves)
@@ -301,7 +304,7 @@ __device__ __forceinline__ void align_rows(const AlignArgs &a, const RowsArgs *o
     for (int64_t r = first; r < a.rows; r += waves) {
         const char *from = static_cast<const char *>(a.in) + r * bytes;
         char *to = static_cast<char *>(a.out) + r * a.ldo * ES;
-        const int have = !of || has_target(*of, r) ? bytes : 0;
+        const int have = !of || has_gradient(*of, r) ? bytes : 0;
         for (int c = lane * 16; c < bytes; c += 64 * 16)
             *reinterpret_cast<u32x4 *>(to + c) = load_chunk<ES>(from + c, have - c);
     }
@@ -348,9 +351,11 @@ __global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, 
     }
     typename T::Pipe pipe;
     pipe.start(a.p, i0, j0, 0, (a.p.nk + T::kStep - 1) / T::kStep, lds);
-    if (counts(at, a.rows.total)) {
+    // a row of no weight is left as one without a target: exp(z - lse) of the
+    // zeros that take the place of its logits may overflow
+    if (counts(at, a.rows.total) && grad * a.rows.scale != 0.0f) {
         row.r = float2{lse * kLog2e, grad * a.rows.scale};
-        if (at >= a.first && at < a.first + a.p.ni && row.r.y != 0.0f) {
+        if (at >= a.first && at < a.first + a.p.ni) {
             row.target = int(at - a.first);
             row.d = row.r.y * (__builtin_amdgcn_exp2f(__builtin_fmaf(logit, kLog2e, -row.r.x)) - 1.0f);
         }
@@ -368,7 +373,7 @@ __global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, 
     for (int j = 0; j < T::FJ; ++j) {
         const Row of = rows[T::lane_j(j)];
         f32x4 d[T::FI];
-        // no dz in a row without a target, whatever its logits
+        // no dz in a row without a gradient, whatever its logits
         if (of.r.y == 0.0f) {
 #pragma unroll
             for (int i = 0; i < T::FI; ++i)
@@ -444,7 +449,7 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(PrepareArgs a, int ro
         const int64_t j = int64_t(b) * kWaves + wave;
         if (j >= a.rows.rows)
             return;
-        const bool used = has_target(a.rows, j);
+        const bool used = has_gradient(a.rows, j);
         if (threadIdx.x % 64 == 0)
             a.rows.row[j] = used ? float2{a.rows.lse[j] * kLog2e, a.rows.grad[j] * a.rows.scale} : float2{0.0f, 0.0f};
         return;
