@@ -408,7 +408,8 @@ typedef struct {
                                      total >= 1; vocab * dim and rows * vocab <= RR_MAX_PLANE */
     int32_t dim;                  /* 1 .. RR_MAX_DIM */
     int32_t topk;                 /* 1 .. RR_MAX_TOPK */
-    float scale;                  /* finite; 1, or one over the temperature */
+    float scale;                  /* finite; 1, or one over the temperature; 0: every entry
+                                     equally likely */
     int32_t reserved;
 } rr_vocab;
 
@@ -457,7 +458,8 @@ rr_status rr_vocab_cross_entropy(const rr_vocab *v, int64_t rows, const int64_t 
  *     call's dtype; those of entries that do not count are not used.
  *   prob [rows][topk]: p = softmax of scale * teacher over the entries that
  *     count; 0 elsewhere, and in a row with no such entry (or whose teacher
- *     logits are all -inf).
+ *     logits are all -inf).  With scale = 0, entries at -inf have p = 0 as with
+ *     every positive scale.
  *   lse [rows], logit [rows][topk]: as above.
  *   loss [rows] = sum p (log p - logit + lse) over the entries with p > 0.
  */

@@ -57,14 +57,17 @@ __global__ __launch_bounds__(T::kThreads) void stats_kernel(StatsArgs a, int til
     typename T::Acc acc;
     acc.clear();
     pipe.finish(acc);
-    // z = scale * acc; the largest is at the largest of acc once scale is positive
-    const float scale = fabsf(a.scale), c = scale * kLog2e;
-    if (a.scale < 0.0f) {
+    // z = scale * acc; the largest is at the largest of acc once scale is
+    // positive.  A scale of 0 goes into acc: -inf past the vocabulary stays what
+    // it is.
+    const float scale = a.scale == 0.0f ? 1.0f : fabsf(a.scale), c = scale * kLog2e;
+    if (a.scale <= 0.0f) {
+        const float by = a.scale == 0.0f ? 0.0f : -1.0f;
 #pragma unroll
         for (int i = 0; i < T::FI; ++i)
 #pragma unroll
             for (int j = 0; j < T::FJ; ++j)
-                acc.c[i][j] = -acc.c[i][j];
+                acc.c[i][j] *= by;
     }
     if (i0 + T::TI > a.p.ni) {
 #pragma unroll
@@ -237,6 +240,15 @@ __global__ __launch_bounds__(kThreads) void cross_entropy_kernel(CombineArgs a)
     a.loss[j] = counts(a.index[j], a.total) ? lse - z : 0.0f;
 }
 
+// A teacher's logit at its scale; one of -inf leaves its entry out at a scale of 0
+// too.
+template <bool BF16>
+__device__ __forceinline__ float teacher_logit(const CombineArgs &a, int64_t n)
+{
+    const float t = load<BF16>(a.teacher, n);
+    return a.scale == 0.0f && t == -INFINITY ? t : a.scale * t;
+}
+
 // One wave per row.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void distill_kernel(CombineArgs a)
@@ -250,20 +262,20 @@ __global__ __launch_bounds__(kThreads) void distill_kernel(CombineArgs a)
     for (int e = lane; e < a.topk; e += 64) {
         const int64_t n = j * a.topk + e;
         if (counts(a.index[n], a.total))
-            top = fmaxf(top, a.scale * load<BF16>(a.teacher, n));
+            top = fmaxf(top, teacher_logit<BF16>(a, n));
     }
     top = lanes_max<64>(top);
     for (int e = lane; e < a.topk; e += 64) {
         const int64_t n = j * a.topk + e;
         if (counts(a.index[n], a.total))
-            sum += exp_below(a.scale * load<BF16>(a.teacher, n), top);
+            sum += exp_below(teacher_logit<BF16>(a, n), top);
     }
     sum = lanes_sum<64>(sum);
     const float log_sum = logf(sum);
     float loss = 0.0f;
     for (int e = lane; e < a.topk; e += 64) {
         const int64_t n = j * a.topk + e;
-        const float z = joined_logit(a, n), t = a.scale * load<BF16>(a.teacher, n);
+        const float z = joined_logit(a, n), t = teacher_logit<BF16>(a, n);
         const bool live = counts(a.index[n], a.total) && t != -INFINITY;
         const float p = live ? exp_below(t, top) / sum : 0.0f;
         a.logit[n] = z;

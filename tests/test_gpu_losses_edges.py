@@ -55,3 +55,47 @@ def test_rows_of_no_weight_may_hold_anything(dt, bad, rows, dim, topk, lead):
     torch.cuda.synchronize()
     assert torch.equal(clean[0], h.dx[0].t) and torch.equal(clean[1], h.dw[0].t)
     assert not h.dx[0].t[1::4].any() and not h.loss.t[1::4].isfinite().any()
+
+
+# --------------------------------------------------------------------------
+# scale = 0: every entry is equally likely
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("rows,dim,vocab", [(1, 64, 100), (40, 72, 500), (50, 65, 513), (300, 64, 256), (1100, 64, 13001)], ids=str)
+@pytest.mark.parametrize("topk", [1, 4])
+def test_scale_of_zero(dt, rows, dim, vocab, topk):
+    h = Head(dt, rows, dim, vocab, topk=topk, scale=0.0, distill=topk > 1, masked=0.3 if rows > 1 else 0.0)
+    h.index[0, 0] = vocab - 1
+    h.run()
+    # one part's sum and its joins: vocab equal terms, the log of their number
+    assert ((h.lse.t.double() - math.log(vocab)).abs() <= (vocab + 16) * ref.U).all()
+    assert not h.dx[0].t.any() and not h.dw[0].t.any()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_scale_of_zero_over_shards(dt):
+    h = Head(dt, 77, 96, 1000, sizes=[1, 0, 300, 699], scale=0.0).run()
+    assert [s.t[0].tolist() for s in h.stats] == [[0.0, 1.0], [-math.inf, 0.0], [0.0, 300.0], [0.0, 699.0]]
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 0.5])
+def test_teacher_entries_at_minus_infinity_are_left_out(dt, scale):
+    h = Head(dt, 50, 64, 500, topk=6, scale=scale, masked=0.1)
+    h.index[:2] = torch.arange(6, device="cuda") * 3
+    h.teacher[0, 1::2] = -math.inf
+    h.teacher[1] = -math.inf                            # nothing left
+    h.make()
+    h.issue()
+    gone = h.teacher == -math.inf
+    assert not h.prob.t[gone].any() and not h.loss.t[1].any() and not h.dx[0].t[1].any()
+    # the entries' logits are given all the same; the rest is as if they were not there
+    picked = h.logit.t[:2].clone()
+    z = scale * (h.x[:2].double() @ h.w[h.index[0]].double().t())
+    size = abs(scale) * (h.x[:2].double().abs() @ h.w[h.index[0]].double().abs().t())
+    assert ((picked.double() - z).abs() <= (64 + 6) * ref.U * size).all()
+    h.index[gone] = -1
+    h.teacher[gone] = 0
+    h.logit.t[gone] = 0
+    h.verify()
