@@ -477,7 +477,8 @@ rr_status rr_vocab_distill(const rr_vocab *v, int dtype, int64_t rows, const int
  *     of the row's entries equal to v; a row with no target, or whose grad *
  *     scale is 0, has dz = 0 and no part in dw whatever its logits and its x
  *     are, NaN included.  For bf16, dz is rounded to bf16 before the two
- *     products.
+ *     products.  exp(z - lse) is formed from lse as given, so that its relative
+ *     error is about |lse| 2^-24: logits past 2^24 have no meaningful gradient.
  *   dx [rows][dim] = dz w, dw [vocab][dim] = dz^T x, rounded once.
  */
 rr_status rr_vocab_grad(const rr_vocab *v, int dtype, int64_t rows, const void *x, const void *w,

@@ -99,6 +99,14 @@ __global__ __launch_bounds__(T::kThreads) void stats_kernel(StatsArgs a, int til
                 sum += __builtin_amdgcn_exp2f(__builtin_fmaf(acc.c[i][j][e], c, base));
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
+        // Every term has the rounding of base in its exponent, which the
+        // largest's own exponent shows; the largest counts 1.  At huge logits
+        // that rounding is past a float's range, and there only the largest counts.
+        const float off = __builtin_fmaf(top, c, base);
+        const bool far = !(fabsf(off) < 64.0f);
+        sum = far ? sum : sum * __builtin_amdgcn_exp2f(-off);
+        if (top != -INFINITY && (sum < 1.0f || (far && sum == sum)))
+            sum = 1.0f;
         const int row = j0 + T::lane_j(j);
         if (threadIdx.x % 64 < 16 && row < a.p.nj)
             a.part[int64_t(part) * a.p.nj + row] = float2{top == -INFINITY ? top : top * scale, sum};

@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import pack_rr_helper_amd as rr
 from tests import loss_ref as ref
 from tests.test_gpu_losses import BF16, DT, F32, Head, device, said  # noqa: F401
 
@@ -99,3 +100,26 @@ def test_teacher_entries_at_minus_infinity_are_left_out(dt, scale):
     h.teacher[gone] = 0
     h.logit.t[gone] = 0
     h.verify()
+
+
+# --------------------------------------------------------------------------
+# far logits
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("size", [2.0 ** 33, 2.0 ** 66])
+@pytest.mark.parametrize("rows,dim,vocab", [(3, 64, 500), (40, 65, 700), (300, 72, 513), (1100, 64, 13001)], ids=str)
+def test_statistics_of_huge_logits(dt, size, rows, dim, vocab):
+    """Finite logits have a finite log sum exp: the largest counts once."""
+    h = Head(dt, rows, dim, vocab)
+    h.x = h.x * size
+    h.make()
+    for v, w, s, p, (_, ws) in zip(h.v, h.vw, h.stats, h.picked, h.works):
+        rr.rr_vocab_stats(v, dt, h.vx, w, h.index, s.t, p.t, workspace=ws)
+    rr.rr_vocab_cross_entropy(h.v[0], h.index, [s.t for s in h.stats], [p.t for p in h.picked], h.lse.t, h.logit.t, h.loss.t)
+    torch.cuda.synchronize()
+    want, tol = ref.head(h.x, h.w, h.index)
+    for n in ("lse", "logit", "loss"):
+        ref.check(n, getattr(h, n).t, want[n], tol[n])
+    sums = h.stats[0].t[:, 1]
+    assert (sums >= 1).all() and (sums <= vocab).all()
