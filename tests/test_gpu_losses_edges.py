@@ -123,3 +123,15 @@ def test_statistics_of_huge_logits(dt, size, rows, dim, vocab):
         ref.check(n, getattr(h, n).t, want[n], tol[n])
     sums = h.stats[0].t[:, 1]
     assert (sums >= 1).all() and (sums <= vocab).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("topk", [1, 5])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_non_finite_grad_of_a_row_without_a_target(dt, topk, bad):
+    h = Head(dt, 40, 64, 500, topk=topk)
+    none = (h.index < 0).all(dim=1)
+    assert none.any() and not none.all()
+    h.grad[none] = bad
+    h.run()
+    assert not h.dx[0].t[none].any() and not h.loss.t[none].any()
