@@ -135,3 +135,49 @@ def test_non_finite_grad_of_a_row_without_a_target(dt, topk, bad):
     h.grad[none] = bad
     h.run()
     assert not h.dx[0].t[none].any() and not h.loss.t[none].any()
+
+
+# --------------------------------------------------------------------------
+# several pieces of the vocabulary (one holds 2^28 bytes of dz, 256 entries at least)
+# --------------------------------------------------------------------------
+
+def around_pieces(h):
+    """Targets of the first rows at both ends of the vocabulary and of every
+    possible piece."""
+    edges = torch.arange(0, h.vocab, 256, device="cuda")
+    at = torch.cat([edges, edges[1:] - 1, torch.tensor([h.vocab - 1], device="cuda")])[:h.rows]
+    h.index[:at.numel(), 0] = at
+
+
+@pytest.mark.parametrize("dt,vocab", [(F32, 17001), (BF16, 33001)])
+@pytest.mark.parametrize("dim", [40, 41])
+@pytest.mark.parametrize("topk", [1, 3])
+def test_wide_pieces(dt, vocab, dim, topk):
+    h = Head(dt, 4200, dim, vocab, topk=topk, scale=0.5 if topk > 1 else 1.0)
+    assert 4200 * vocab * (4 if dt == F32 else 2) > 1 << 28
+    around_pieces(h)
+    h.run()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("dim,lead", [(40, 0), (41, 0), (40, 1)])
+@pytest.mark.parametrize("topk", [1, 3])
+def test_narrow_pieces(dt, dim, lead, topk):
+    """Three pieces of 256, 256 and 188 entries for many rows, most of them
+    without a target: those add nothing to a sum, so that the bounds are of the
+    others alone."""
+    h = Head(dt, 300000, dim, 700, topk=topk, scale=0.5 if topk > 1 else 1.0, masked=0.999, lead=lead)
+    around_pieces(h)
+    h.make()
+    h.issue()
+    torch.cuda.synchronize()
+    used = (h.index >= 0).any(dim=1)
+    assert 100 < used.sum() < 1000
+    want, tol = ref.head(h.x[used], h.w, h.index[used], h.scale, h.teacher[used] if h.distill else None, h.grad[used])
+    for n in ("lse", "logit", "loss", "dx"):
+        t = (h.dx[0] if n == "dx" else getattr(h, n)).t
+        ref.check(n, t[used], want[n], tol[n])
+    ref.check("dw", h.dw[0].t, want["dw"], tol["dw"])
+    assert not h.dx[0].t[~used].any() and not h.loss.t[~used].any()
+    assert all(o.untouched() for o in h.outs())
+    assert all(bool((big[ws.numel():] == 0xFF).all()) for big, ws in h.works)
