@@ -10,7 +10,8 @@ the weight updates::
     y       = x * (1 + sum_k weight_k * scale[choice_k])      the experts
     loss    = sum over targets of cross entropy(y, head) / n + balance * balance loss
 
-With a teacher's top logits the head's loss is the distillation instead.
+With a teacher's top logits the head's loss is the distillation instead, times
+the square of the temperature as usual.
 
     python -m pack_rr_helper_amd.sharded_step --steps 20
 """
@@ -31,7 +32,7 @@ class ShardedStep:
                  dtype=BF16, device="cuda", seed=0):
         gen = torch.Generator(device=device).manual_seed(seed)
         t, k = TORCH[dtype], max(teacher_topk, 1)
-        self.rows, self.balance, self.distills = rows, balance, teacher_topk > 0
+        self.rows, self.entries, self.balance, self.distills = rows, vocab, balance, teacher_topk > 0
         self.temperature = temperature if self.distills else 1.0
 
         def normal(*shape):
@@ -86,13 +87,15 @@ class ShardedStep:
                 rr_vocab_grad(v, dtype, self.y, w, self.index, lse, logit, prob, self.grad, dx, dw, workspace=work)
 
     def step(self, x, index, teacher=None, rate=0.0):
-        """One step on x [rows, dim]; index [rows, k] holds the targets (below 0:
-        none), teacher [rows, k] the teacher's logits for them.  Returns the mean
-        loss of the rows that have a target, and the balance loss."""
+        """One step on x [rows, dim]; index [rows, k] holds the targets (below 0,
+        or not below the vocabulary's size: none), teacher [rows, k] the teacher's
+        logits for them.  Returns the mean cross entropy or divergence of the rows
+        that have a target, without the temperature's square and the balance, and
+        the balance loss."""
         self.index.copy_(index)
         if self.distills:
             self.teacher.copy_(teacher)
-        torch.any(self.index >= 0, dim=1, out=self.keep)
+        torch.any((self.index >= 0) & (self.index < self.entries), dim=1, out=self.keep)
         n = self.keep.sum().clamp_min(1)
         self.grad.copy_(self.temperature ** 2 / n)
         x = x.float()

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import pack_rr_helper_amd as rr
+from pack_rr_helper_amd.sharded_step import ShardedStep
 from tests import loss_ref as ref
 from tests.test_gpu_losses import BF16, DT, F32, Head, device, said  # noqa: F401
 
@@ -181,3 +182,47 @@ def test_narrow_pieces(dt, dim, lead, topk):
     assert not h.dx[0].t[~used].any() and not h.loss.t[~used].any()
     assert all(o.untouched() for o in h.outs())
     assert all(bool((big[ws.numel():] == 0xFF).all()) for big, ws in h.works)
+
+
+# --------------------------------------------------------------------------
+# the step that runs the calls together
+# --------------------------------------------------------------------------
+
+def test_step_ignores_targets_outside_the_vocabulary():
+    """They are no targets: not in the mean, and not routed."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(60, 24, generator=gen, device="cuda")
+    index = torch.randint(0, 90, (60, 1), generator=gen, device="cuda")
+    index[::3] = -1
+    sides = []
+    for none in (-1, 90, 1 << 40):
+        s = ShardedStep(60, 24, 90, shards=2, experts=5, topk=2, dtype=F32)
+        loss, balance = s.step(x, torch.where(index < 0, none, index))
+        assert torch.equal(s.keep, index[:, 0] >= 0)
+        sides.append([loss, balance, s.dhead, s.dlogits, *s.dx])
+    assert all(torch.equal(a, b) for side in sides[1:] for a, b in zip(sides[0], side))
+
+
+def test_step_distills_gradients():
+    """Against autograd in 64 bits: temperature^2 times the distillation, in fp32."""
+    rows, dim, vocab, experts, k, t = 40, 24, 90, 5, 4, 2.0
+    s = ShardedStep(rows, dim, vocab, shards=2, experts=experts, topk=2, teacher_topk=k, temperature=t, balance=0.0, dtype=F32)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(rows, dim, generator=gen, device="cuda")
+    index = torch.stack([torch.randperm(vocab, generator=gen, device="cuda")[:k] for _ in range(rows)])
+    index[::6] = -1
+    teacher = 2 * torch.randn(rows, k, generator=gen, device="cuda")
+    loss, _ = s.step(x, index, teacher)
+    keep = (index >= 0).all(dim=1)
+    head, logits = s.head.double().requires_grad_(), s.logits.double().requires_grad_()
+    weight, choice = torch.softmax(logits, dim=1).topk(2, dim=1)
+    weight = weight / weight.sum(dim=1, keepdim=True) * keep[:, None]
+    y = x.double() * (1 + (weight[:, :, None] * s.scale.double()[choice]).sum(dim=1))
+    p = torch.log_softmax(teacher.double() / t, dim=1)
+    q = torch.log_softmax(y @ head.t() / t, dim=1).gather(1, index.clamp_min(0))
+    mean = (p.exp() * (p - q)).sum(dim=1)[keep].mean()
+    (t * t * mean).backward()
+    assert loss.item() == pytest.approx(mean.item(), rel=512 * ref.U)
+    # a few hundred fp32 roundings along the way
+    for got, want in ((s.dlogits, logits.grad), (s.dhead, head.grad)):
+        assert (got.double() - want).abs().max() <= 512 * ref.U * want.abs().max()
