@@ -334,9 +334,11 @@ __device__ __forceinline__ int round64(int n) { return (n + 63) / 64 * 64; }
 
 // dz = coefficient * exp(z - lse), zero past the piece up to the next multiple
 // of 64; the first `copies` workgroups copy x for dw meanwhile.  4096 x 2048 x
-// 32000 in bf16: 464-480 us, 1.1 PFLOP/s, of which the
-// statistics' kernel takes 415 us.  bf16 keeps dz at 8 bits for the products: each gradient sums many of
-// these roundings, which leaves it within its own.
+// 32000 in bf16: 464-480 us, 1.1 PFLOP/s, of which the statistics' kernel takes
+// 415 us.  bf16 keeps dz at 8 bits for the products, whose operand it is on the
+// matrix units.  These roundings average out where a gradient sums many of
+// them; where it sums few they add to its own (1023 x 1024 x 32000: 0.0019 off
+// in all, 0.0017 with dz in fp32; 64 entries a row: 0.0024).
 template <typename T>
 __global__ __launch_bounds__(T::kThreads) void dz_kernel(DzArgs a, int tiles_i, int tiles_j, int copies)
 {
