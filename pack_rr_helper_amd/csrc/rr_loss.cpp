@@ -7,19 +7,11 @@
 
 #include <algorithm>
 
+#include "rr_call.h"
+
 namespace {
 
 using namespace rr;
-
-int64_t elem_size(int dtype) { return dtype == RR_F32 ? 4 : 2; }
-int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-
-rr_status check_dtype(int dtype)
-{
-    if (dtype != RR_F32 && dtype != RR_BF16)
-        return set_error(RR_EINVAL, "unknown dtype %d", dtype);
-    return RR_OK;
-}
 
 rr_status check_tokens(int64_t rows)
 {
@@ -53,86 +45,10 @@ rr_status check_vocab(const rr_vocab *v, int64_t rows)
     return RR_OK;
 }
 
-// The buffers of one call: each checked for null and alignment, the written
-// ones against every other.
-class Buffers {
-public:
-    Buffers &in(const void *p, int64_t bytes, int64_t align, const char *what) { return add(p, bytes, align, what, false); }
-    Buffers &out(const void *p, int64_t bytes, int64_t align, const char *what) { return add(p, bytes, align, what, true); }
-
-    rr_status check()
-    {
-        if (st_ != RR_OK)
-            return st_;
-        for (int i = 0; i < n_; ++i)
-            for (int j = 0; j < i; ++j)
-                if ((b_[i].written || b_[j].written) && b_[i].lo < b_[j].hi && b_[j].lo < b_[i].hi)
-                    return set_error(RR_EALIAS, "%s overlaps %s", b_[i].what, b_[j].what);
-        return RR_OK;
-    }
-
-private:
-    struct Buf {
-        uintptr_t lo, hi;
-        const char *what;
-        bool written;
-    };
-    Buffers &add(const void *p, int64_t bytes, int64_t align, const char *what, bool written)
-    {
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-        if (st_ != RR_OK || bytes <= 0)
-            return *this;
-        if (!p)
-            st_ = set_error(RR_EINVAL, "%s is null", what);
-        else if (lo % uintptr_t(align))
-            st_ = set_error(RR_EINVAL, "%s=%p is not aligned to %lld bytes", what, p, (long long)align);
-        else
-            b_[n_++] = Buf{lo, lo + uintptr_t(bytes), what, written};
-        return *this;
-    }
-    Buf b_[2 * RR_MAX_SHARDS + 16];
-    int n_ = 0;
-    rr_status st_ = RR_OK;
-};
-
-// The launches of one call, up to the first that fails.
-class Launches {
-public:
-    explicit Launches(void *stream) : st_(static_cast<hipStream_t>(stream)) {}
-    template <typename A>
-    void add(hipError_t (*launch)(const Op &, hipStream_t), const A &a)
-    {
-        if (err_ == hipSuccess)
-            err_ = emit_op(Op::make(launch, a), st_);
-    }
-    rr_status finish() const { return err_ == hipSuccess ? set_ok() : op_failed(err_); }
-
-private:
-    hipStream_t st_;
-    hipError_t err_ = hipSuccess;
-};
-
 Product logits_product(const rr_vocab *v, int dtype, int64_t rows, const void *x, const void *w)
 {
     return Product{w, x, v->dim, v->dim, int32_t(v->vocab), int32_t(rows), v->dim, dtype == RR_BF16};
 }
-
-// Parts of a workspace, one after the other at 256-byte boundaries.
-class Carver {
-public:
-    explicit Carver(void *base) : base_(static_cast<char *>(base)) {}
-    void *take(int64_t bytes)
-    {
-        void *p = base_ + used_;
-        used_ += round_up(bytes, 256);
-        return p;
-    }
-    int64_t used() const { return used_; }
-
-private:
-    char *base_;
-    int64_t used_ = 0;
-};
 
 // The workspace of rr_vocab_grad.  dz is held for one piece of the vocabulary
 // at a time.
@@ -177,13 +93,6 @@ GradSpace grad_space(const rr_vocab *v, int dtype, int64_t rows, void *base)
 int64_t stats_bytes(const rr_vocab *v, int dtype, int64_t rows)
 {
     return round_up(stats_parts(logits_product(v, dtype, rows, nullptr, nullptr)) * rows * 8, 256);
-}
-
-rr_status check_workspace(int64_t have, int64_t need)
-{
-    if (have < need)
-        return set_error(RR_EINVAL, "workspace of %lld bytes, needs %lld", (long long)have, (long long)need);
-    return RR_OK;
 }
 
 rr_status check_router(const rr_router *r)
