@@ -540,6 +540,229 @@ rr_status rr_route_grad(const rr_router *r, int dtype, int64_t rows, const void 
                         const int32_t *choice, const float *weight, const float *lse, const float *slope,
                         const float *grad_loss, const float *grad_weight, void *dlogits, void *stream);
 
+/*
+ * The expert layer of a sharded training step, and what stands before its
+ * weight update: routing in groups of experts, the slots of an expert layer,
+ * the experts' products in 8 bits, and the clipping of the gradients.  The rules of
+ * the sharded losses hold here too (contiguous row-major buffers that do not
+ * overlap, workspaces, results that do not depend on the launch's timing).
+ */
+
+/*
+ * A router of tokens to experts in `groups` groups of consecutive experts:
+ * first the top_groups best groups of a token are chosen, then its topk best
+ * experts in those.
+ *   score s_e: softmax or sigmoid of the logits; choice score c_e = s_e + bias_e,
+ *     so that a bias steers the choice and not the weights (`rr_route_bias`).
+ *   A group's score is the sum of its group_best largest c_e.
+ * The choice is made in 64 bits, scores within 2^-40 of each other counting as
+ * equal; the lower index comes first among equals, NaN before every number.
+ */
+typedef struct {
+    int32_t experts;      /* 1 .. RR_MAX_EXPERTS, a multiple of groups */
+    int32_t topk;         /* 1 .. min(top_groups * experts / groups, RR_MAX_ROUTE_TOPK) */
+    int32_t groups;       /* 1 .. RR_MAX_GROUPS */
+    int32_t top_groups;   /* 1 .. groups */
+    int32_t group_best;   /* 1 or 2, at most experts / groups */
+    int32_t score;        /* RR_SOFTMAX or RR_SIGMOID */
+    int32_t renormalize;  /* weights divided by the sum of s over the chosen experts */
+    float scale;          /* of the weights; finite */
+} rr_group_router;
+
+#define RR_SOFTMAX 0
+#define RR_SIGMOID 1
+#define RR_MAX_GROUPS 64
+
+/* rr_group_route_workspace -- bytes of workspace for rr_group_route (may be 0);
+ * -1 for arguments that it rejects. */
+int64_t rr_group_route_workspace(const rr_group_router *r, int64_t rows);
+
+/*
+ * rr_group_route -- choices, weights and counts.
+ *   logits [rows][experts]; bias [experts] floats (null: 0; -inf: the expert is
+ *     never chosen); keep [rows] bytes, 0 leaves a token out (null: all kept).
+ *   choice [rows][topk]: the chosen experts, the largest c first; -1 for a token
+ *     left out and for places that only experts with c = -inf are left for.
+ *   weight [rows][topk]: scale * s (renormalize: over the sum of s of the
+ *     choices; 0 if that is 0); 0 where choice is -1.
+ *   logit [rows][topk]: the choices' logits; -inf where choice is -1.
+ *   lse [rows]: softmax: log sum exp of the logits, 0 for a token left out (null:
+ *     not stored); sigmoid: not used.
+ *   counts [experts + 1]: choices of each expert, then the tokens kept.
+ */
+rr_status rr_group_route(const rr_group_router *r, int dtype, int64_t rows, const void *logits,
+                         const float *bias, const uint8_t *keep, int32_t *choice, float *weight,
+                         float *logit, float *lse, int32_t *counts, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
+/*
+ * rr_route_bias -- the next step's bias, from the counts of nRanks ranks as
+ * rr_group_route writes them (1 .. RR_MAX_SHARDS): out_e = bias_e + rate *
+ * sign(mean - n_e), n_e the choices of expert e over all ranks and mean their
+ * mean over the experts.  `out` may be `bias`.  rate: finite.
+ */
+rr_status rr_route_bias(const rr_group_router *r, const int32_t *const *counts, int nRanks, float rate,
+                        const float *bias, float *out, void *stream);
+
+/*
+ * rr_group_route_grad -- the gradient of sum grad_weight * weight with respect
+ * to the logits, given what rr_group_route wrote; the choice is constant.
+ *   logits, lse: needed by softmax without renormalize, whose gradient reaches
+ *     every expert; else not read and may be null.
+ *   dlogits [rows][experts] in the call's dtype, 0 for a row without a choice.
+ */
+rr_status rr_group_route_grad(const rr_group_router *r, int dtype, int64_t rows, const void *logits,
+                              const int32_t *choice, const float *logit, const float *lse,
+                              const float *grad_weight, void *dlogits, void *stream);
+
+/*
+ * The slots of an expert layer: a rank holds the experts [first, first +
+ * experts), and the choices that name them, of topk for each of its rows (choices
+ * of other experts, -1 among them, are not its own).  Each expert has a segment
+ * of positions that starts at a multiple of RR_QUANT_BLOCK and holds the expert's
+ * choices n = row * topk + k in rising order.
+ */
+typedef struct {
+    int64_t rows;         /* 0 <= rows, rows * topk <= RR_MAX_CHOICES */
+    int32_t experts;      /* 1 .. RR_MAX_EXPERTS */
+    int32_t first;        /* 0 <= first <= 2^30 */
+    int32_t topk;         /* 1 .. RR_MAX_ROUTE_TOPK */
+    int32_t reserved;
+} rr_experts;
+
+#define RR_QUANT_BLOCK 128
+#define RR_MAX_CHOICES (INT64_C(1) << 28)
+
+/* rr_expert_capacity -- positions that hold any choices, a multiple of RR_QUANT_BLOCK;
+ * rr_expert_workspace -- bytes of workspace for rr_expert_slots (may be 0).
+ * -1 for arguments that the calls reject. */
+int64_t rr_expert_capacity(const rr_experts *e);
+int64_t rr_expert_workspace(const rr_experts *e);
+
+/*
+ * rr_expert_slots -- where each choice goes.
+ *   choice [rows][topk].
+ *   slot [rows][topk]: the position of a choice; -1 for those of other ranks.
+ *   source [capacity]: the choice at a position, -1 for none.
+ *   offset [experts + 1]: the segments' first positions, then the end of the last.
+ *   count [experts]: choices in each segment.
+ */
+rr_status rr_expert_slots(const rr_experts *e, const int32_t *choice, int32_t *slot, int32_t *source,
+                          int32_t *offset, int32_t *count, void *workspace, int64_t workspace_bytes,
+                          void *stream);
+
+/*
+ * Matrices in 8 bits: e4m3 (finite, NaN, largest 448) with one power of two for each
+ * block of RR_QUANT_BLOCK elements of a row, or of RR_QUANT_BLOCK x RR_QUANT_BLOCK for weights.
+ *   values [rows][ld]: ld = rr_quantized_ld(n), n rounded up to a multiple of
+ *     RR_QUANT_BLOCK, zeros past n; aligned to 16 bytes.
+ *   powers [rows][lds] (weights: [ceil(rows / RR_QUANT_BLOCK)][lds] for each expert):
+ *     lds = rr_quantized_lds(n); byte b stands for 2^(b - 127).  Aligned to 4 bytes.
+ * With a the largest magnitude of a block its power is the least 2^e, e >= -127,
+ * with a <= 448 * 2^e; each element is divided by it (exactly) and rounded once, to
+ * the nearest, ties to even.  A block that holds an infinity or a NaN is all NaN
+ * (byte 255).  Powers of two, as a multiplication by them rounds nothing: where
+ * a block's elements stay normal their relative error is at most 2^-4.
+ */
+int64_t rr_quantized_ld(int64_t n);
+int64_t rr_quantized_lds(int64_t n);
+#define RR_MAX_WIDTH 65536   /* of the matrices' dimensions dim, n, k */
+
+/* rr_quantize_rows -- x [rows][dim], each row in blocks.  rows < 2^31. */
+rr_status rr_quantize_rows(int dtype, int64_t rows, int32_t dim, const void *x, void *values,
+                           void *powers, void *stream);
+
+/*
+ * rr_quantize_slots -- transposed, in blocks of positions: values [dim][ld of
+ * capacity], for the weights' gradient, which sums over an expert's positions.
+ * Element [d][p] is x[row][d] * weight[n] (a 32-bit product) with n = source[p];
+ * row = n / topk (gather) or p (not gather, x then has capacity rows); weight null: 1.
+ * 0 where source is -1, whatever x holds there.  Positions from offset[experts] on
+ * are left as they were.
+ */
+rr_status rr_quantize_slots(const rr_experts *e, int dtype, int32_t dim, const void *x, int gather,
+                            const float *weight, const int32_t *source, const int32_t *offset,
+                            void *values, void *powers, void *stream);
+
+/*
+ * rr_quantize_weight -- w [experts][n][k] in blocks of 128 x 128.
+ *   values [experts][n][ld of k], powers [experts][ceil(n / 128)][lds of k]; the
+ *   transposed, tvalues [experts][k][ld of n] and tpowers [experts][ceil(k / 128)]
+ *   [lds of n], in the same blocks, if tvalues is not null.
+ */
+rr_status rr_quantize_weight(int dtype, int32_t experts, int32_t n, int32_t k, const void *w, void *values,
+                             void *powers, void *tvalues, void *tpowers, void *stream);
+
+/*
+ * rr_expert_product -- out[p][i] = weight * sum_j x[row][j] w[e][i][j] for every
+ * position p of a choice, e its expert; `dtype` is out's, [capacity][n].
+ *   x: values and powers [x_rows][..] of k columns as rr_quantize_rows writes
+ *     them; row = source[p] / topk (gather: x_rows = rows, rows * ld < 2^31 - 2^20)
+ *     or p (x_rows = capacity).
+ *   w: as rr_quantize_weight writes it (for dx = dy w: the transposed, n and k
+ *     exchanged).
+ *   weight [rows][topk]: multiplies a position's sums; null: none.
+ *   Positions without a choice are left as they were.
+ */
+rr_status rr_expert_product(const rr_experts *e, int dtype, int32_t n, int32_t k, int gather,
+                            const void *x, const void *x_powers, const void *w, const void *w_powers,
+                            const float *weight, const int32_t *source, const int32_t *offset,
+                            const int32_t *count, void *out, void *stream);
+
+/*
+ * rr_expert_weight_grad -- dw[e][i][j] = sum_p dy[i][p] x[j][p] over the positions
+ * of expert e, in the call's dtype; 0 for an expert without choices.  dy [n][..]
+ * and x [k][..]: as rr_quantize_slots writes them.
+ */
+rr_status rr_expert_weight_grad(const rr_experts *e, int dtype, int32_t n, int32_t k, const void *dy,
+                                const void *dy_powers, const void *x, const void *x_powers,
+                                const int32_t *offset, const int32_t *count, void *dw, void *stream);
+
+/*
+ * rr_expert_combine -- y[row] = sum_k weight[row][k] * values[slot[row][k]] over
+ * the row's own choices, summed in 32 bits in the order of k; weight null: 1.
+ *   values [capacity][dim] of values_dtype; y [rows][dim] of dtype.
+ */
+rr_status rr_expert_combine(const rr_experts *e, int values_dtype, int dtype, int32_t dim, const void *values,
+                            const int32_t *slot, const float *weight, void *y, void *stream);
+
+/*
+ * rr_expert_combine_grad -- grad_weight[row][k] = sum_i dy[row][i] *
+ * values[slot[row][k]][i]; 0 for choices of other ranks.  dy [rows][dim] of dtype.
+ */
+rr_status rr_expert_combine_grad(const rr_experts *e, int values_dtype, int dtype, int32_t dim,
+                                 const void *values, const int32_t *slot, const void *dy, float *grad_weight,
+                                 void *stream);
+
+/*
+ * The global gradient norm, over nTensors arrays of count[i] elements (0 <=
+ * nTensors <= RR_MAX_TENSORS, 0 <= count[i], 2^40 in all) of one dtype at any
+ * element alignment, and over calls: each call gives one sum, those of other
+ * dtypes and ranks are added by rr_grad_clip.
+ */
+#define RR_MAX_TENSORS 4096
+
+/* rr_grad_workspace -- bytes of workspace for rr_grad_square_sum; -1 for
+ * arguments that it rejects. */
+int64_t rr_grad_workspace(int dtype, int nTensors, const int64_t *count);
+
+/* rr_grad_square_sum -- sum [1], a double: the sum of all elements' squares, in 64
+ * bits (finite for all finite elements). */
+rr_status rr_grad_square_sum(int dtype, int nTensors, const void *const *in, const int64_t *count,
+                             double *sum, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * rr_grad_clip -- norm [1], a float: the root of the nSums sums' sum (1 ..
+ * RR_MAX_SHARDS); out[i] = in[i] * factor, factor = max_norm / norm rounded to
+ * a float where norm > max_norm, else 1.  A norm that is infinite or NaN leaves
+ * the values as they are: the caller decides by `norm`.
+ *   out[i] may be in[i] exactly, and then is not touched where factor is 1.
+ *   max_norm: 0 <= max_norm, finite.
+ */
+rr_status rr_grad_clip(int dtype, const double *const *sums, int nSums, double max_norm, int nTensors,
+                       const void *const *in, void *const *out, const int64_t *count, float *norm,
+                       void *stream);
+
 #ifdef __cplusplus
 }
 #endif

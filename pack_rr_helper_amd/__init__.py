@@ -499,3 +499,8 @@ from . import losses  # noqa: E402  (uses the helpers above)
 from .losses import *  # noqa: E402,F401,F403
 
 __all__ += losses.__all__
+
+from . import experts  # noqa: E402  (uses the losses' marshalling)
+from .experts import *  # noqa: E402,F401,F403
+
+__all__ += experts.__all__

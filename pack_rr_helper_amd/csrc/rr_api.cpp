@@ -916,7 +916,7 @@ hipError_t emit_op(const Op &op, hipStream_t stream)
     r.kind = kPlanOp;
     r.shifted = 0;
     r.tiles = 0;
-    memcpy(static_cast<void *>(&r.red), &op, sizeof op);
+    memcpy(static_cast<void *>(&r.red), &op, op.used());
     return hipSuccess;
 }
 
@@ -1210,8 +1210,10 @@ rr_status rr_plan_launch(const void *plan, void *stream)
         const rr::PlanRec &r = rec[i];
         hipError_t e;
         if (r.kind == kPlanOp) {
+            // a record is aligned less than an op
             rr::Op op;
-            memcpy(&op, static_cast<const void *>(&r.red), sizeof op);
+            memcpy(static_cast<void *>(&op), static_cast<const void *>(&r.red), offsetof(rr::Op, args));
+            memcpy(static_cast<void *>(&op), static_cast<const void *>(&r.red), op.used());
             e = op.launch(op, st);
         } else {
             e = r.kind == rr::kPlanReduce ? rr::launch_reduce(r.red, r.tiles, r.shifted != 0, st)

@@ -1,0 +1,179 @@
+// rr_expert.h -- what the host layer of the expert layer and the clipping
+// (rr_expert.cpp) shares with their kernels (rr_group_route.hip, rr_slots.hip,
+// rr_expert_product.hip, rr_clip.hip).  Not part of the public ABI.
+#pragma once
+
+#include "rr_loss.h"
+
+namespace rr {
+
+// ---------------------------------------------------------------------------
+// Routing in groups
+// ---------------------------------------------------------------------------
+
+struct GroupRouteArgs {
+    const void *logits;
+    const float *bias;
+    const uint8_t *keep;
+    int32_t *choice;
+    float *weight, *logit, *lse;
+    int32_t *counts;     // of one workgroup: the result; else [blocks][experts + 1]
+    int64_t rows;
+    int32_t experts, topk, groups, top_groups, group_best, sigmoid, renormalize, bf16, blocks;
+    float scale;
+};
+int32_t group_route_blocks(int64_t rows, int32_t experts, int32_t groups);
+hipError_t launch_group_route(const Op &, hipStream_t);
+
+struct CountSumArgs {
+    const int32_t *part;
+    int32_t *counts;
+    int32_t blocks, experts;
+};
+hipError_t launch_count_sum(const Op &, hipStream_t);
+
+struct RouteBiasArgs {
+    const int32_t *counts[RR_MAX_SHARDS];
+    const float *bias;
+    float *out;
+    int32_t ranks, experts;
+    float rate;
+};
+hipError_t launch_route_bias(const Op &, hipStream_t);
+
+struct GroupGradArgs {
+    const void *logits;
+    const int32_t *choice;
+    const float *logit, *lse, *grad_weight;
+    void *dlogits;
+    int64_t rows;
+    int32_t experts, topk, sigmoid, renormalize, bf16;
+    float scale;
+};
+hipError_t launch_group_grad(const Op &, hipStream_t);
+
+// ---------------------------------------------------------------------------
+// Slots of an expert layer, and what moves rows to and from them
+// ---------------------------------------------------------------------------
+
+struct SlotsArgs {
+    const int32_t *choice;
+    int32_t *slot, *source, *offset, *count;
+    int32_t *part;       // [blocks][experts], more than one workgroup only
+    int32_t choices, capacity, experts, first, blocks;
+};
+int32_t slots_blocks(int64_t choices);
+hipError_t launch_slots_count(const Op &, hipStream_t);
+hipError_t launch_slots(const Op &, hipStream_t);
+
+// One operand in 8 bits.
+struct Eight {
+    unsigned char *values, *powers;
+    int64_t ld, lds;
+};
+
+struct QuantizeRowsArgs {
+    const void *x;
+    Eight to;
+    int64_t rows;
+    int32_t dim, bf16;
+};
+hipError_t launch_quantize_rows(const Op &, hipStream_t);
+
+struct QuantizeSlotsArgs {
+    const void *x;
+    const float *weight;
+    const int32_t *source, *offset;
+    Eight to;
+    int64_t rows;
+    int32_t capacity, experts, dim, topk, gather, bf16;
+};
+hipError_t launch_quantize_slots(const Op &, hipStream_t);
+
+struct QuantizeWeightArgs {
+    const void *w;
+    Eight to, turned;    // turned.values may be null
+    int32_t experts, n, k, bf16;
+};
+hipError_t launch_quantize_weight(const Op &, hipStream_t);
+
+struct CombineRowsArgs {
+    const void *values;
+    const int32_t *slot;
+    const float *weight;
+    void *y;
+    int64_t rows;
+    int32_t capacity, topk, dim, from_bf16, bf16;
+};
+hipError_t launch_combine_rows(const Op &, hipStream_t);
+
+struct CombineGradArgs {
+    const void *values;
+    const int32_t *slot;
+    const void *dy;
+    float *grad_weight;
+    int64_t rows;
+    int32_t capacity, topk, dim, from_bf16, bf16;
+};
+hipError_t launch_combine_grad(const Op &, hipStream_t);
+
+// ---------------------------------------------------------------------------
+// Products in 8 bits
+// ---------------------------------------------------------------------------
+
+struct ExpertProductArgs {
+    Eight w, x;
+    const float *weight;
+    const int32_t *source, *offset, *count;
+    void *out;
+    int64_t rows;        // of x
+    int32_t n, k, experts, topk, capacity, gather, bf16, choices;
+};
+hipError_t launch_expert_product(const Op &, hipStream_t);
+
+struct ExpertGradArgs {
+    Eight dy, x;
+    const int32_t *offset, *count;
+    void *dw;
+    int32_t n, k, experts, capacity, bf16;
+};
+hipError_t launch_expert_grad(const Op &, hipStream_t);
+
+// ---------------------------------------------------------------------------
+// Gradient norm
+// ---------------------------------------------------------------------------
+
+// Tensors of one launch.
+constexpr int32_t kClipTensors = 90;
+
+struct ClipTensor {
+    const void *in;
+    void *out;
+    int64_t count;
+};
+
+struct SquareSumArgs {
+    double *part;        // one per workgroup of this launch
+    int32_t tensors, bf16, blocks, reserved;
+    ClipTensor t[kClipTensors];
+};
+int32_t square_blocks(const int64_t *count, int32_t tensors, int64_t es);
+hipError_t launch_square_sum(const Op &, hipStream_t);
+
+struct SumPartsArgs {
+    const double *part;
+    double *sum;
+    int32_t parts;
+};
+hipError_t launch_sum_parts(const Op &, hipStream_t);
+
+struct ClipArgs {
+    const double *sums[RR_MAX_SHARDS];
+    double max_norm;
+    float *norm;         // null: another launch's
+    int32_t n_sums, tensors, bf16, blocks;
+    ClipTensor t[kClipTensors];
+};
+hipError_t launch_clip(const Op &, hipStream_t);
+
+}  // namespace rr

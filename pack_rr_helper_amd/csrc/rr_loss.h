@@ -3,6 +3,7 @@
 // rr_api.cpp.  Not part of the public ABI.
 #pragma once
 
+#include <stddef.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -14,21 +15,24 @@
 
 namespace rr {
 
-// One launch of a loss operator: the function that enqueues it and its
-// arguments by value.  A plan records it as it is.
+// One launch of an operator: the function that enqueues it and its arguments by
+// value.  A plan records the bytes in use.
 struct Op {
     hipError_t (*launch)(const Op &, hipStream_t);
-    alignas(16) char args[496];
+    size_t bytes;            // of args in use
+    alignas(16) char args[2464];
 
     template <typename A>
     static Op make(hipError_t (*launch)(const Op &, hipStream_t), const A &a)
     {
         static_assert(sizeof(A) <= sizeof(Op::args) && std::is_trivially_copyable<A>::value, "");
-        Op op{};
+        Op op;
         op.launch = launch;
+        op.bytes = sizeof a;
         memcpy(op.args, &a, sizeof a);
         return op;
     }
+    size_t used() const { return offsetof(Op, args) + bytes; }
     template <typename A>
     A get() const
     {

@@ -1,0 +1,568 @@
+// rr_slots.hip -- gfx950 kernels around the experts' products: the slot map of the
+// choices, the matrices in 8 bits, the weighted sum back to rows and its gradient.
+// All but the slot map are bound by their bytes.
+#include "rr_expert.h"
+#include "rr_lanes.h"
+
+namespace rr {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------------------
+// Slots: a counting sort that keeps the order of the choices.  A workgroup has a
+// piece of the choices, each of its waves a contiguous part of that, 64 at a time:
+// a choice's place is its segment's start, the choices of the same expert in
+// earlier pieces, in earlier waves, before this 64 and in lower lanes.
+// ---------------------------------------------------------------------------
+
+constexpr int kSlotThreads = 1024, kSlotWaves = kSlotThreads / 64;
+constexpr int kOnePiece = 8192;  // choices that one workgroup places alone
+constexpr int kPiece = 2048;     // the least of many
+
+__host__ __device__ inline int piece_of(int choices, int blocks)
+{
+    const int64_t per = (int64_t(choices) + blocks - 1) / blocks;
+    return int((per + kSlotThreads - 1) / kSlotThreads * kSlotThreads);
+}
+
+__global__ __launch_bounds__(kThreads) void slots_count_kernel(SlotsArgs a)
+{
+    __shared__ int n[RR_MAX_EXPERTS];
+    for (int e = threadIdx.x; e < a.experts; e += kThreads)
+        n[e] = 0;
+    __syncthreads();
+    const int piece = piece_of(a.choices, a.blocks);
+    const int64_t lo = int64_t(blockIdx.x) * piece, hi = lo + piece < a.choices ? lo + piece : a.choices;
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+        const unsigned e = unsigned(a.choice[i]) - unsigned(a.first);
+        if (e < unsigned(a.experts))
+            atomicAdd(&n[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += kThreads)
+        a.part[int64_t(blockIdx.x) * a.experts + e] = n[e];
+}
+
+__global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotsArgs a)
+{
+    __shared__ int cursor[kSlotWaves][RR_MAX_EXPERTS];
+    __shared__ int all[RR_MAX_EXPERTS], start[RR_MAX_EXPERTS + 1], earlier[RR_MAX_EXPERTS];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int piece = piece_of(a.choices, a.blocks), per = piece / kSlotWaves;  // a multiple of 64
+    for (int i = threadIdx.x; i < kSlotWaves * a.experts; i += kSlotThreads)
+        cursor[i / a.experts][i % a.experts] = 0;
+    __syncthreads();
+    const int64_t lo = int64_t(blockIdx.x) * piece + int64_t(wave) * per;
+    const int64_t hi = lo + per < a.choices ? lo + per : a.choices;
+    for (int64_t i = lo + lane; i < hi; i += 64) {
+        const unsigned e = unsigned(a.choice[i]) - unsigned(a.first);
+        if (e < unsigned(a.experts))
+            atomicAdd(&cursor[wave][e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) {
+        int here = 0, total = 0, before = 0;
+        for (int w = 0; w < kSlotWaves; ++w)
+            here += cursor[w][e];
+        if (a.blocks > 1) {
+#pragma unroll 8
+            for (int b = 0; b < a.blocks; ++b) {
+                const int n = a.part[int64_t(b) * a.experts + e];
+                total += n;
+                before += b < int(blockIdx.x) ? n : 0;
+            }
+        } else {
+            total = here;
+        }
+        all[e] = total;
+        earlier[e] = before;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        int base = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 64) {
+            const int n = e0 + lane < a.experts ? (all[e0 + lane] + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK * RR_QUANT_BLOCK : 0;
+            int sum = n;
+            for (int d = 1; d < 64; d *= 2) {
+                const int o = __shfl_up(sum, d);
+                sum += lane >= d ? o : 0;
+            }
+            if (e0 + lane < a.experts)
+                start[e0 + lane] = base + sum - n;
+            base += __shfl(sum, 63);
+        }
+        if (lane == 0)
+            start[a.experts] = base;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) {
+        int at = start[e] + earlier[e];
+        for (int w = 0; w < kSlotWaves; ++w) {
+            const int n = cursor[w][e];
+            cursor[w][e] = at;
+            at += n;
+        }
+    }
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= a.experts; e += kSlotThreads) {
+            a.offset[e] = start[e];
+            if (e < a.experts)
+                a.count[e] = all[e];
+        }
+    // what no choice takes: the segments' ends, and the positions behind the last
+    for (int e = blockIdx.x; e < a.experts; e += a.blocks)
+        for (int p = start[e] + all[e] + int(threadIdx.x); p < start[e + 1]; p += kSlotThreads)
+            a.source[p] = -1;
+    for (int64_t p = start[a.experts] + int64_t(blockIdx.x) * kSlotThreads + threadIdx.x; p < a.capacity;
+         p += int64_t(a.blocks) * kSlotThreads)
+        a.source[p] = -1;
+    __syncthreads();
+    for (int64_t i0 = lo; i0 < hi; i0 += 64) {
+        const int64_t i = i0 + lane;
+        const unsigned e = i < hi ? unsigned(a.choice[i]) - unsigned(a.first) : ~0u;
+        const bool own = e < unsigned(a.experts);
+        unsigned long long same = __ballot(own);
+        for (int bit = 1; bit < a.experts; bit *= 2) {
+            const unsigned long long set = __ballot(own && (e & bit));
+            same &= (e & bit) ? set : ~set;
+        }
+        int p = -1;
+        if (own) {
+            p = cursor[wave][e] + __popcll(same & ((1ull << lane) - 1));
+            a.source[p] = int(i);
+        }
+        // one wave's LDS operations keep their order; so has the compiler to
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (own && (same >> lane) == 1)  // the highest lane of its expert
+            cursor[wave][e] = p + 1;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (i < hi)
+            a.slot[i] = p;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Eight bits
+// ---------------------------------------------------------------------------
+
+constexpr unsigned kNotFinite = 0x7f800000u;
+
+// The byte of the power for a block whose largest magnitude has these bits: the
+// least 2^e with it <= 448 * 2^e = 1.75 * 2^(e + 8), e >= -127; 255 for a block that is not
+// finite.
+__device__ __forceinline__ unsigned power_byte(unsigned largest)
+{
+    if (largest >= kNotFinite)
+        return 255;
+    const int b = int(largest >> 23) - 8 + ((largest & 0x7fffffu) > 0x600000u);
+    return b > 0 ? unsigned(b) : 0;
+}
+
+// What a block's elements are multiplied by; its bits are those of 2^(127 - byte).
+__device__ __forceinline__ float inverse_power(unsigned byte) { return __uint_as_float((254u - byte) << 23); }
+
+// Four elements to e4m3.
+__device__ __forceinline__ unsigned eight_bits(const float *v, unsigned byte)
+{
+    const float by = inverse_power(byte);
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * by, v[1] * by, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * by, v[3] * by, w, true);
+    return byte == 255 ? 0x7f7f7f7fu : unsigned(w);
+}
+
+__device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Eight elements from column `at` of a row of `dim`, zeros past it.  WHOLE: the
+// row starts at, and is, a multiple of 16 bytes.
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void load_eight(const void *row, int at, int dim, float *v)
+{
+    if constexpr (WHOLE && BF16) {
+        uint4 w{0, 0, 0, 0};
+        if (at < dim)
+            w = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(row) + at);
+        const unsigned u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    } else if constexpr (WHOLE) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            float4 w{0.0f, 0.0f, 0.0f, 0.0f};
+            if (at + i < dim)
+                w = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + at + i);
+            v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = 0.0f;
+            if (at + i < dim) {
+                if constexpr (BF16)
+                    v[i] = __uint_as_float(unsigned(static_cast<const unsigned short *>(row)[at + i]) << 16);
+                else
+                    v[i] = static_cast<const float *>(row)[at + i];
+            }
+        }
+    }
+}
+
+// The row at element `at` of a matrix.
+template <bool BF16>
+__device__ __forceinline__ const void *row_at(const void *x, int64_t at)
+{
+    return static_cast<const char *>(x) + at * (BF16 ? 2 : 4);
+}
+
+// A block of a row by sixteen lanes.
+template <bool BF16, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeRowsArgs a, int blocks)
+{
+    const int lane = threadIdx.x % 16;
+    const int64_t n = a.rows * blocks;
+    for (int64_t i = int64_t(blockIdx.x) * (kThreads / 16) + threadIdx.x / 16; i < n; i += int64_t(gridDim.x) * (kThreads / 16)) {
+        const int64_t r = i / blocks;
+        const int b = int(i - r * blocks), at = b * RR_QUANT_BLOCK + lane * 8;
+        float v[8];
+        load_eight<BF16, WHOLE>(row_at<BF16>(a.x, r * a.dim), at, a.dim, v);
+        unsigned top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            top = max(top, magnitude(v[e]));
+        const unsigned byte = power_byte(across<16>(top, [](unsigned x, unsigned y) { return x > y ? x : y; }));
+        const uint2 q{eight_bits(v, byte), eight_bits(v + 4, byte)};
+        *reinterpret_cast<uint2 *>(a.to.values + r * a.to.ld + at) = q;
+        if (lane == 0)
+            a.to.powers[r * a.to.lds + b] = (unsigned char)byte;
+    }
+}
+
+// A tile of 128 x 128 elements: sixteen lanes a row, a thread has rows
+// [8 (t / 16), + 8) and eight columns.  Transposed, its eight rows are eight bytes
+// of a column, which go through LDS at places exchanged by the column's lane.
+struct Turned {
+    unsigned char t[RR_QUANT_BLOCK * RR_QUANT_BLOCK];
+
+    __device__ uint2 *at(int column, int part) { return reinterpret_cast<uint2 *>(t + column * RR_QUANT_BLOCK + ((part ^ (column / 8)) & 15) * 8); }
+};
+
+// The transposed tile from LDS to rows [0, rows) of out.
+__device__ __forceinline__ void store_turned(Turned &t, unsigned char *out, int64_t ld, int rows)
+{
+    for (int i = threadIdx.x; i < RR_QUANT_BLOCK * 16; i += kThreads)
+        if (i / 16 < rows)
+            *reinterpret_cast<uint2 *>(out + i / 16 * ld + i % 16 * 8) = *t.at(i / 16, i % 16);
+}
+
+template <bool BF16, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void quantize_weight_kernel(QuantizeWeightArgs a, int blocks_n, int blocks_k)
+{
+    __shared__ __attribute__((aligned(16))) Turned turned;
+    __shared__ unsigned largest;
+    const int lane = threadIdx.x % 16, part = threadIdx.x / 16;
+    const int bk = blockIdx.x % blocks_k, bn = blockIdx.x / blocks_k % blocks_n, e = blockIdx.x / blocks_k / blocks_n;
+    const int n0 = bn * RR_QUANT_BLOCK, k0 = bk * RR_QUANT_BLOCK;
+    if (threadIdx.x == 0)
+        largest = 0;
+    __syncthreads();
+    float v[8][8];
+    unsigned top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = n0 + part * 8 + i;
+        load_eight<BF16, WHOLE>(row_at<BF16>(a.w, (int64_t(e) * a.n + (row < a.n ? row : 0)) * a.k), k0 + lane * 8,
+                                row < a.n ? a.k : 0, v[i]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            top = max(top, magnitude(v[i][c]));
+    }
+    top = across<64>(top, [](unsigned x, unsigned y) { return x > y ? x : y; });
+    if (threadIdx.x % 64 == 0)
+        atomicMax(&largest, top);
+    __syncthreads();
+    const unsigned byte = power_byte(largest);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = n0 + part * 8 + i;
+        if (row < a.n)
+            *reinterpret_cast<uint2 *>(a.to.values + (int64_t(e) * a.n + row) * a.to.ld + k0 + lane * 8) =
+                uint2{eight_bits(v[i], byte), eight_bits(v[i] + 4, byte)};
+    }
+    if (threadIdx.x == 0) {
+        a.to.powers[(int64_t(e) * blocks_n + bn) * a.to.lds + bk] = (unsigned char)byte;
+        if (a.turned.values)
+            a.turned.powers[(int64_t(e) * blocks_k + bk) * a.turned.lds + bn] = (unsigned char)byte;
+    }
+    if (!a.turned.values)
+        return;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        float col[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            col[i] = v[i][c];
+        *turned.at(lane * 8 + c, part) = uint2{eight_bits(col, byte), eight_bits(col + 4, byte)};
+    }
+    __syncthreads();
+    store_turned(turned, a.turned.values + (int64_t(e) * a.k + k0) * a.turned.ld + n0, a.turned.ld, a.k - k0);
+}
+
+template <bool BF16, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void quantize_slots_kernel(QuantizeSlotsArgs a, int blocks_d)
+{
+    __shared__ __attribute__((aligned(16))) Turned turned;
+    __shared__ unsigned largest[RR_QUANT_BLOCK];
+    const int lane = threadIdx.x % 16, part = threadIdx.x / 16;
+    const int bd = blockIdx.x % blocks_d, bp = blockIdx.x / blocks_d;
+    const int p0 = bp * RR_QUANT_BLOCK, d0 = bd * RR_QUANT_BLOCK;
+    if (p0 >= a.offset[a.experts])
+        return;
+    for (int i = threadIdx.x; i < RR_QUANT_BLOCK; i += kThreads)
+        largest[i] = 0;
+    __syncthreads();
+    float v[8][8];
+    unsigned top[8] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int p = p0 + part * 8 + i, n = a.source[p];
+        const int64_t row = a.gather ? n / a.topk : p;
+        const bool in = n >= 0 && n / a.topk < a.rows;
+        load_eight<BF16, WHOLE>(row_at<BF16>(a.x, (in ? row : 0) * a.dim), d0 + lane * 8, in ? a.dim : 0, v[i]);
+        const float w = in && a.weight ? a.weight[n] : 1.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            v[i][c] = in ? v[i][c] * w : 0.0f;
+            top[c] = max(top[c], magnitude(v[i][c]));
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        atomicMax(&largest[lane * 8 + c], top[c]);
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const unsigned byte = power_byte(largest[lane * 8 + c]);
+        float col[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            col[i] = v[i][c];
+        *turned.at(lane * 8 + c, part) = uint2{eight_bits(col, byte), eight_bits(col + 4, byte)};
+    }
+    for (int i = threadIdx.x; i < RR_QUANT_BLOCK && d0 + i < a.dim; i += kThreads)
+        a.to.powers[int64_t(d0 + i) * a.to.lds + bp] = (unsigned char)power_byte(largest[i]);
+    __syncthreads();
+    store_turned(turned, a.to.values + int64_t(d0) * a.to.ld + p0, a.to.ld, a.dim - d0);
+}
+
+// ---------------------------------------------------------------------------
+// Rows of sums
+// ---------------------------------------------------------------------------
+
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void store_eight(void *row, int at, int dim, const float *v)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    unsigned u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        u[i] = __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{v[2 * i], v[2 * i + 1]}, bf16x2));
+    if constexpr (WHOLE && BF16) {
+        *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(row) + at) = uint4{u[0], u[1], u[2], u[3]};
+    } else if constexpr (WHOLE) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4)
+            if (at + i < dim)
+                *reinterpret_cast<float4 *>(static_cast<float *>(row) + at + i) = float4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (at + i < dim) {
+                if constexpr (BF16)
+                    static_cast<unsigned short *>(row)[at + i] = (unsigned short)(u[i / 2] >> 16 * (i % 2));
+                else
+                    static_cast<float *>(row)[at + i] = v[i];
+            }
+    }
+}
+
+// Eight columns of a row by a thread.
+template <bool FROM, bool BF16, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs a, int chunks)
+{
+    const int64_t n = a.rows * chunks;
+    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kThreads) {
+        const int64_t r = i / chunks;
+        const int at = int(i - r * chunks) * 8;
+        float sum[8] = {};
+#pragma unroll 4
+        for (int k = 0; k < a.topk; ++k) {
+            const int p = a.slot[r * a.topk + k];
+            const bool in = unsigned(p) < unsigned(a.capacity);
+            const float w = a.weight && in ? a.weight[r * a.topk + k] : 1.0f;
+            float v[8];
+            load_eight<FROM, WHOLE>(row_at<FROM>(a.values, (in ? int64_t(p) : 0) * a.dim), at, in ? a.dim : 0, v);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                sum[c] = in ? __builtin_fmaf(w, v[c], sum[c]) : sum[c];
+        }
+        store_eight<BF16, WHOLE>(const_cast<void *>(row_at<BF16>(a.y, r * a.dim)), at, a.dim, sum);
+    }
+}
+
+// A row by a wave, eight choices at a time.
+template <bool FROM, bool BF16, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs a)
+{
+    constexpr int kWide = 8;
+    const int lane = threadIdx.x % 64;
+    for (int64_t r = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64; r < a.rows; r += int64_t(gridDim.x) * (kThreads / 64))
+        for (int k0 = 0; k0 < a.topk; k0 += kWide) {
+            int p[kWide];
+            float dot[kWide] = {};
+#pragma unroll
+            for (int k = 0; k < kWide; ++k) {
+                p[k] = k0 + k < a.topk ? a.slot[r * a.topk + k0 + k] : -1;
+                if (unsigned(p[k]) >= unsigned(a.capacity))
+                    p[k] = -1;
+            }
+            for (int at = lane * 8; at < a.dim; at += 512) {
+                float dy[8];
+                load_eight<BF16, WHOLE>(row_at<BF16>(a.dy, r * a.dim), at, a.dim, dy);
+#pragma unroll
+                for (int k = 0; k < kWide; ++k) {
+                    float v[8];
+                    load_eight<FROM, WHOLE>(row_at<FROM>(a.values, int64_t(p[k] < 0 ? 0 : p[k]) * a.dim), at, p[k] < 0 ? 0 : a.dim, v);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        dot[k] = p[k] < 0 ? 0.0f : __builtin_fmaf(dy[c], v[c], dot[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kWide; ++k) {
+                const float d = lanes_sum<64>(dot[k]);
+                if (lane == 0 && k0 + k < a.topk)
+                    a.grad_weight[r * a.topk + k0 + k] = d;
+            }
+        }
+}
+
+// Rows that start at, and are a multiple of, 16 bytes.
+bool whole(const void *p, int64_t dim, bool bf16) { return in_chunks(p, dim, bf16 ? 2 : 4); }
+
+// f(bf16, whole) as compile-time values.
+template <typename F>
+hipError_t with_form(bool bf16, bool w, F f)
+{
+    using Yes = std::true_type;
+    using No = std::false_type;
+    return bf16 ? (w ? f(Yes{}, Yes{}) : f(Yes{}, No{})) : (w ? f(No{}, Yes{}) : f(No{}, No{}));
+}
+
+unsigned grid_of(int64_t n, int64_t per, unsigned most)
+{
+    const int64_t b = (n + per - 1) / per;
+    return unsigned(b < most ? b : most);
+}
+
+}  // namespace
+
+int32_t slots_blocks(int64_t choices)
+{
+    // one workgroup and one launch as long as that is short; then enough
+    // workgroups for the compute units
+    if (choices <= kOnePiece)
+        return 1;
+    const int64_t n = (choices + kPiece - 1) / kPiece;
+    return int32_t(n < 256 ? n : 256);
+}
+
+hipError_t launch_slots_count(const Op &op, hipStream_t stream)
+{
+    const SlotsArgs a = op.get<SlotsArgs>();
+    (void)hipGetLastError();
+    slots_count_kernel<<<dim3(unsigned(a.blocks)), dim3(kThreads), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_slots(const Op &op, hipStream_t stream)
+{
+    const SlotsArgs a = op.get<SlotsArgs>();
+    (void)hipGetLastError();
+    slots_kernel<<<dim3(unsigned(a.blocks)), dim3(kSlotThreads), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_quantize_rows(const Op &op, hipStream_t stream)
+{
+    const QuantizeRowsArgs a = op.get<QuantizeRowsArgs>();
+    const int blocks = (a.dim + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK;
+    (void)hipGetLastError();
+    return with_form(a.bf16, whole(a.x, a.dim, a.bf16), [&](auto bf16, auto w) {
+        quantize_rows_kernel<decltype(bf16)::value, decltype(w)::value>
+            <<<dim3(grid_of(a.rows * blocks, kThreads / 16, 8192)), dim3(kThreads), 0, stream>>>(a, blocks);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_quantize_slots(const Op &op, hipStream_t stream)
+{
+    const QuantizeSlotsArgs a = op.get<QuantizeSlotsArgs>();
+    const int blocks = (a.dim + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK;
+    (void)hipGetLastError();
+    return with_form(a.bf16, whole(a.x, a.dim, a.bf16), [&](auto bf16, auto w) {
+        quantize_slots_kernel<decltype(bf16)::value, decltype(w)::value>
+            <<<dim3(unsigned(blocks) * unsigned(a.capacity / RR_QUANT_BLOCK)), dim3(kThreads), 0, stream>>>(a, blocks);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_quantize_weight(const Op &op, hipStream_t stream)
+{
+    const QuantizeWeightArgs a = op.get<QuantizeWeightArgs>();
+    const int n = (a.n + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK, k = (a.k + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK;
+    (void)hipGetLastError();
+    return with_form(a.bf16, whole(a.w, a.k, a.bf16), [&](auto bf16, auto w) {
+        quantize_weight_kernel<decltype(bf16)::value, decltype(w)::value>
+            <<<dim3(unsigned(n) * unsigned(k) * unsigned(a.experts)), dim3(kThreads), 0, stream>>>(a, n, k);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_combine_rows(const Op &op, hipStream_t stream)
+{
+    const CombineRowsArgs a = op.get<CombineRowsArgs>();
+    const int chunks = (a.dim + 7) / 8;
+    const bool w = whole(a.values, a.dim, a.from_bf16) && whole(a.y, a.dim, a.bf16);
+    (void)hipGetLastError();
+    return with_form(a.bf16, w, [&](auto bf16, auto all) {
+        const dim3 grid(grid_of(a.rows * chunks, kThreads, 16384));
+        if (a.from_bf16)
+            combine_rows_kernel<true, decltype(bf16)::value, decltype(all)::value><<<grid, dim3(kThreads), 0, stream>>>(a, chunks);
+        else
+            combine_rows_kernel<false, decltype(bf16)::value, decltype(all)::value><<<grid, dim3(kThreads), 0, stream>>>(a, chunks);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_combine_grad(const Op &op, hipStream_t stream)
+{
+    const CombineGradArgs a = op.get<CombineGradArgs>();
+    const bool w = whole(a.values, a.dim, a.from_bf16) && whole(a.dy, a.dim, a.bf16);
+    (void)hipGetLastError();
+    return with_form(a.bf16, w, [&](auto bf16, auto all) {
+        const dim3 grid(grid_of(a.rows, kThreads / 64, 16384));
+        if (a.from_bf16)
+            combine_grad_kernel<true, decltype(bf16)::value, decltype(all)::value><<<grid, dim3(kThreads), 0, stream>>>(a);
+        else
+            combine_grad_kernel<false, decltype(bf16)::value, decltype(all)::value><<<grid, dim3(kThreads), 0, stream>>>(a);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace rr
