@@ -3,8 +3,14 @@
 //
 // One matrix instruction multiplies 16 x 128 by 128 x 16 elements and applies the
 // operands' powers itself, so that a block of k is one instruction and costs no
-// vector instruction; sums are held in 32 bits throughout.  Which bytes of a block
+// vector instruction; sums over blocks are held in 32 bits.  Which bytes of a block
 // a lane holds does not matter as long as both operands agree, its power being one.
+//
+// Within a block that instruction keeps about 17 bits below its largest product
+// (measured: 1.6e-5 of a sum of 128 normal products, whatever is added to), less than
+// the 2^-9 of a result in bf16 and more than a result in 32 bits may be off.  Results in
+// 32 bits therefore take the operands as bf16, which holds e4m3 times a power of two
+// exactly, through the bf16 instructions (1e-8, at half the rate): FULL.
 #include "rr_expert.h"
 #include "rr_product.h"
 
@@ -18,6 +24,33 @@ template <int PA, int PB>
 __device__ __forceinline__ void multiply(const i32x8 &a, const i32x8 &b, f32x4 &c, unsigned pa, unsigned pb)
 {
     c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, PA, int(pa), PB, int(pb));
+}
+
+// A lane's 32 elements times 2^(power - 127), in bf16.
+struct Wide {
+    bf16x8 v[4];
+
+    __device__ __forceinline__ void set(const i32x8 &from, unsigned power)
+    {
+        const float by = __uint_as_float((power & 255u) << 23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u32x4 w;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                w[2 * h] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned(from[2 * i + h]), by, false));
+                w[2 * h + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(unsigned(from[2 * i + h]), by, true));
+            }
+            v[i] = __builtin_bit_cast(bf16x8, w);
+        }
+    }
+};
+
+__device__ __forceinline__ void multiply(const Wide &a, const Wide &b, f32x4 &c)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], c, 0, 0, 0);
 }
 
 struct Place {
@@ -100,7 +133,7 @@ struct Piece {
     }
 };
 
-template <int FJ>
+template <int FJ, bool FULL>
 __global__ __launch_bounds__(kNarrowThreads) void narrow_kernel(ExpertProductArgs a, int tiles_i)
 {
     constexpr int FI = kNarrowI / 16, TJ = 16 * FJ;
@@ -151,11 +184,26 @@ __global__ __launch_bounds__(kNarrowThreads) void narrow_kernel(ExpertProductArg
             x0[f] = xf[f];
         if (b + kNarrowWaves < blocks)
             load(b + kNarrowWaves);
+        if constexpr (FULL) {
+            Wide wide[FI];
 #pragma unroll
-        for (int i = 0; i < FI; ++i)
+            for (int i = 0; i < FI; ++i)
+                wide[i].set(w0[i].v, w0[i].p);
 #pragma unroll
-            for (int j = 0; j < FJ; ++j)
-                multiply<0, 0>(w0[i].v, x0[j].v, acc[i][j], w0[i].p, x0[j].p);
+            for (int j = 0; j < FJ; ++j) {
+                Wide of_x;
+                of_x.set(x0[j].v, x0[j].p);
+#pragma unroll
+                for (int i = 0; i < FI; ++i)
+                    multiply(wide[i], of_x, acc[i][j]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int j = 0; j < FJ; ++j)
+                    multiply<0, 0>(w0[i].v, x0[j].v, acc[i][j], w0[i].p, x0[j].p);
+        }
     }
 #pragma unroll
     for (int i = 0; i < FI; ++i)
@@ -176,7 +224,7 @@ __global__ __launch_bounds__(kNarrowThreads) void narrow_kernel(ExpertProductArg
 #pragma unroll
         for (int n = 0; n < 4; ++n)
             if (i + n < a.n) {
-                if (a.bf16)
+                if constexpr (!FULL)
                     static_cast<unsigned short *>(a.out)[to + n] = (unsigned short)pack_bf16(s[n], 0.0f);
                 else
                     static_cast<float *>(a.out)[to + n] = s[n];
@@ -195,26 +243,26 @@ __global__ __launch_bounds__(kNarrowThreads) void narrow_kernel(ExpertProductArg
 // second's fragments are read; into the second, one barrier says that this step has
 // been read by all and that the next one has arrived.
 // BLOCK_A: the rows of a wave share one power.
-template <int TI_, int TJ_, int WI, int WJ, bool BLOCK_A>
+template <int TI_, int TJ_, int WI, int WJ, bool BLOCK_A, bool FULL>
 struct Tile8 {
     static constexpr int TI = TI_, TJ = TJ_, kWaves = WI * WJ, kThreads = kWaves * 64;
     static constexpr int FI = TI / WI / 16, FJ = TJ / WJ / 16, H = FI / 2;
     static constexpr int kRows = 8 * kWaves, kLoadBytes = kRows * kRowBytes;
-    static constexpr int kLoadsA = TI / kRows, kLoadsB = TJ / kRows;
+    static constexpr int kLoadsA = TI / kRows, kLoadsB = TJ / kRows, kLoadsP = (TI + TJ) / kThreads;
     static constexpr int kStageBytes = (TI + TJ) * kRowBytes, kPowerBytes = (TI + TJ) * 4;
     static constexpr int kLdsBytes = 2 * kStageBytes + 2 * kPowerBytes;
-    static_assert(TI + TJ == kThreads, "a thread loads the powers of one row");
+    // waves a SIMD has room for, which the registers are divided by
+    static constexpr int kPerSimd = 160 * 1024 / kLdsBytes * kWaves / 4;
+    static_assert(kLoadsP * kThreads == TI + TJ && TI % 64 == 0, "a wave loads the powers of one operand");
     static_assert(!BLOCK_A || RR_QUANT_BLOCK % (FI * 16) == 0, "");
+    static_assert(FJ >= 4 && H >= 1, "");
+    static constexpr bool kFull = FULL;  // results in 32 bits
     // results leave as those of a product in bf16 and fp32 do
     template <bool BF16>
     using Out = Tile<BF16, TI, TJ, WI, WJ, 2, true>;
 
-    struct Side {
-        __amdgpu_buffer_rsrc_t values;
-    };
-
-    __amdgpu_buffer_rsrc_t a, b, power;
-    int off_a[kLoadsA], off_b[kLoadsB], off_power;
+    __amdgpu_buffer_rsrc_t a, b, power[kLoadsP];
+    int off_a[kLoadsA], off_b[kLoadsB], off_power[kLoadsP];
     char *lds;
     int s0, s1;
 
@@ -248,11 +296,14 @@ struct Tile8 {
             const int r = rb(l * kRows + row0);
             off_b[l] = r >= 0 ? int(r * y.ld) + chunk : kNowhere;
         }
-        // the waves of the first TI threads load A's powers
-        const bool of_a = wave < TI / 64;
-        power = of_a ? buffer(x.powers, power_a) : buffer(y.powers, power_b);
-        const int r = of_a ? pa(int(threadIdx.x)) : rb(int(threadIdx.x) - TI);
-        off_power = r >= 0 ? int(r * (of_a ? x.lds : y.lds)) : kNowhere;
+#pragma unroll
+        for (int l = 0; l < kLoadsP; ++l) {
+            const int row = l * kThreads + int(threadIdx.x);
+            const bool of_a = l * kThreads + __builtin_amdgcn_readfirstlane(wave) * 64 < TI;
+            power[l] = of_a ? buffer(x.powers, power_a) : buffer(y.powers, power_b);
+            const int r = of_a ? pa(row) : rb(row - TI);
+            off_power[l] = r >= 0 ? int(r * (of_a ? x.lds : y.lds)) : kNowhere;
+        }
         fetch_powers(s0 / 4);
         if (s0 % 4 == 3)
             fetch_powers(s0 / 4 + 1);
@@ -262,23 +313,25 @@ struct Tile8 {
     __device__ void fetch(int s) const
     {
         char *to = lds + s % 2 * kStageBytes + threadIdx.x / 64 * 1024;
-        const int k = s * kRowBytes;
         const bool in = s < s1;
+        const int k = in ? s * kRowBytes : 0;
 #pragma unroll
         for (int l = 0; l < kLoadsA; ++l)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(a, lds_pointer(to + l * kLoadBytes), 16, in ? off_a[l] : kNowhere, in ? k : 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(a, lds_pointer(to + l * kLoadBytes), 16, in ? off_a[l] : kNowhere, k, 0, 0);
 #pragma unroll
         for (int l = 0; l < kLoadsB; ++l)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(b, lds_pointer(to + (kLoadsA + l) * kLoadBytes), 16,
-                                                     in ? off_b[l] : kNowhere, in ? k : 0, 0, 0);
+                                                     in ? off_b[l] : kNowhere, k, 0, 0);
     }
     __device__ char *powers(int group) const { return lds + 2 * kStageBytes + group % 2 * kPowerBytes; }
     // Four steps' powers, from step 4 * group on.
     __device__ void fetch_powers(int group) const
     {
         const bool in = 4 * group < s1;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(power, lds_pointer(powers(group) + threadIdx.x / 64 * 256), 4,
-                                                 in ? off_power : kNowhere, in ? group * 4 : 0, 0, 0);
+#pragma unroll
+        for (int l = 0; l < kLoadsP; ++l)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(power[l], lds_pointer(powers(group) + (l * kThreads + threadIdx.x / 64 * 64) * 4), 4,
+                                                     in ? off_power[l] : kNowhere, in ? group * 4 : 0, 0, 0);
     }
 
     __device__ static int wave_i() { return (threadIdx.x / 64) % WI * (FI * 16); }
@@ -314,9 +367,31 @@ struct Tile8 {
         for (int f = 0; f < FJ; ++f)
             p.b[f] = at[TI + wave_j() + f * 16];
     }
+    // The powers of step s in the low bytes.
+    __device__ static void shift(const Powers &from, int s, Powers &to)
+    {
+#pragma unroll
+        for (int f = 0; f < kPowersA; ++f)
+            to.a[f] = from.a[f] >> s % 4 * 8;
+#pragma unroll
+        for (int f = 0; f < FJ; ++f)
+            to.b[f] = from.b[f] >> s % 4 * 8;
+    }
     struct Acc {
         f32x4 c[FI][FJ];
     };
+
+    // This step has been read by all, and the next one has arrived.
+    __device__ void advance(int s, Powers &raw) const
+    {
+        wait_loads<0>();
+        __builtin_amdgcn_s_barrier();
+        fetch(s + 2);
+        if ((s + 2) % 4 == 0)
+            fetch_powers((s + 2) / 4);
+        if ((s + 1) % 4 == 0)
+            read_powers(s + 1, raw);
+    }
 
     // acc += the products of steps [s0, s1), of which there is at least one
     __device__ void finish(Acc &acc) const
@@ -329,50 +404,69 @@ struct Tile8 {
         for (int f = 0; f < FJ; ++f)
             fb[f] = read_b(s0, f);
 #pragma unroll
-        for (int f = 0; f < H; ++f)
+        for (int f = 0; f < (FULL ? FI : H); ++f)
             fa[f] = read_a(s0, f);
         read_powers(s0, raw);
-        for (int s = s0; s < s1; ++s) {
-            const int shift = s % 4 * 8;
+        if constexpr (FULL) {
+            for (int s = s0; s < s1; ++s) {
+                shift(raw, s, at);
+                Wide wb[FJ];
 #pragma unroll
-            for (int f = 0; f < kPowersA; ++f)
-                at.a[f] = raw.a[f] >> shift;
+                for (int j = 0; j < FJ; ++j)
+                    wb[j].set(fb[j], at.b[j]);
 #pragma unroll
-            for (int f = 0; f < FJ; ++f)
-                at.b[f] = raw.b[f] >> shift;
+                for (int i = 0; i < FI; ++i) {
+                    Wide wa;
+                    wa.set(fa[i], at.a[BLOCK_A ? 0 : i]);
 #pragma unroll
-            for (int j = 0; j < FJ; ++j) {
+                    for (int j = 0; j < FJ; ++j)
+                        multiply(wa, wb[j], acc.c[i][j]);
+                    if (i == 0)
+                        advance(s, raw);
+                    if (i == 0 || i == 1) {
 #pragma unroll
-                for (int i = 0; i < H; ++i)
-                    multiply<0, 0>(fa[i], fb[j], acc.c[i][j], at.a[BLOCK_A ? 0 : i], at.b[j]);
-                __builtin_amdgcn_sched_barrier(0);
-                if (j < (H + 1) / 2) {
-#pragma unroll
-                    for (int f = H + 2 * j; f < H + 2 * j + 2 && f < FI; ++f)
-                        fa[f] = read_a(s, f);
+                        for (int f = i * FJ / 2; f < (i + 1) * FJ / 2; ++f)
+                            fb[f] = read_b(s + 1, f);
+                    }
+                    fa[i] = read_a(s + 1, i);
                 }
             }
+        } else {
+            for (int s = s0; s < s1; ++s) {
+                shift(raw, s, at);
 #pragma unroll
-            for (int j = 0; j < FJ; ++j) {
+                for (int j = 0; j < FJ; ++j) {
 #pragma unroll
-                for (int i = H; i < FI; ++i)
-                    multiply<0, 0>(fa[i], fb[j], acc.c[i][j], at.a[BLOCK_A ? 0 : i], at.b[j]);
-                if (j == 0) {
-                    wait_loads<0>();
-                    __builtin_amdgcn_s_barrier();
-                    fetch(s + 2);
-                    if ((s + 2) % 4 == 0)
-                        fetch_powers((s + 2) / 4);
-                    if ((s + 1) % 4 == 0)
-                        read_powers(s + 1, raw);
+                    for (int i = 0; i < H; ++i)
+                        multiply<0, 0>(fa[i], fb[j], acc.c[i][j], at.a[BLOCK_A ? 0 : i], at.b[j]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (j < (H + 1) / 2) {
+#pragma unroll
+                        for (int f = H + 2 * j; f < H + 2 * j + 2 && f < FI; ++f)
+                            fa[f] = read_a(s, f);
+                    }
                 }
-                fb[j] = read_b(s + 1, j);
-                if (j > 0) {
+                constexpr int kAt = FJ / 4 - 1;  // the barrier: after this column of the second half
 #pragma unroll
-                    for (int f = (j - 1) * H / (FJ - 1); f < j * H / (FJ - 1); ++f)
-                        fa[f] = read_a(s + 1, f);
+                for (int j = 0; j < FJ; ++j) {
+#pragma unroll
+                    for (int i = H; i < FI; ++i)
+                        multiply<0, 0>(fa[i], fb[j], acc.c[i][j], at.a[BLOCK_A ? 0 : i], at.b[j]);
+                    if (j == kAt) {
+                        advance(s, raw);
+#pragma unroll
+                        for (int f = 0; f < kAt; ++f)
+                            fb[f] = read_b(s + 1, f);
+                    }
+                    if (j >= kAt) {
+                        fb[j] = read_b(s + 1, j);
+                        constexpr int kOver = FJ - 1 - kAt;  // a's first half over the columns left
+#pragma unroll
+                        for (int f = (j - kAt) * H / kOver; f < (j - kAt + 1) * H / kOver && f < H; ++f)
+                            fa[f] = read_a(s + 1, f);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
         }
         // the loads past s1 have written zeros: LDS is free after this
@@ -382,18 +476,18 @@ struct Tile8 {
 };
 
 // The lane's results of row j (fragment f, of the wave's) to out, the tile's first i.
-template <typename T, bool BF16>
+template <typename T>
 __device__ __forceinline__ void store(const typename T::Acc &acc, int f, void *out, int64_t at, int left, float by)
 {
     f32x4 v[T::FI];
 #pragma unroll
     for (int i = 0; i < T::FI; ++i)
         v[i] = acc.c[i][f] * by;
-    T::template Out<BF16>::store_row(static_cast<char *>(out) + at * (BF16 ? 2 : 4), v, left);
+    T::template Out<!T::kFull>::store_row(static_cast<char *>(out) + at * (T::kFull ? 4 : 2), v, left);
 }
 
 template <typename T>
-__global__ __launch_bounds__(T::kThreads) void product_kernel(ExpertProductArgs a, int tiles_i)
+__global__ __launch_bounds__(T::kThreads, T::kPerSimd) void product_kernel(ExpertProductArgs a, int tiles_i)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     Place at;
@@ -429,16 +523,13 @@ __global__ __launch_bounds__(T::kThreads) void product_kernel(ExpertProductArgs 
         const int p = first + j, left = j < live ? rows_i : 0;
         const float by = weight_of(a, p, j < live);
         const int64_t to = int64_t(p) * a.n + i0;
-        if (a.bf16)
-            store<T, true>(acc, f, a.out, to, left, by);
-        else
-            store<T, false>(acc, f, a.out, to, left, by);
+        store<T>(acc, f, a.out, to, left, by);
     }
 }
 
 // dw[e][j][i] = sum over the segment's positions of x[i][p] dy[j][p].
 template <typename T>
-__global__ __launch_bounds__(T::kThreads) void grad_kernel(ExpertGradArgs a, int tiles_i, int tiles_j)
+__global__ __launch_bounds__(T::kThreads, T::kPerSimd) void grad_kernel(ExpertGradArgs a, int tiles_i, int tiles_j)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     const int e = blockIdx.x / (tiles_i * tiles_j);
@@ -466,17 +557,14 @@ __global__ __launch_bounds__(T::kThreads) void grad_kernel(ExpertGradArgs a, int
         const int j = j0 + T::wave_j() + f * 16 + int(threadIdx.x % 16);
         const int left = j < a.n ? rows_i : 0;
         const int64_t to = (int64_t(e) * a.n + j) * a.k + i0;
-        if (a.bf16)
-            store<T, true>(acc, f, a.dw, to, left, 1.0f);
-        else
-            store<T, false>(acc, f, a.dw, to, left, 1.0f);
+        store<T>(acc, f, a.dw, to, left, 1.0f);
     }
 }
 
 int tiles(int n, int per) { return n / per + (n % per != 0); }
 
-template <bool BLOCK_A> using Big = Tile8<256, 256, 2, 4, BLOCK_A>;
-template <bool BLOCK_A> using Mid = Tile8<128, 128, 2, 2, BLOCK_A>;
+template <bool BLOCK_A> using Big = Tile8<256, 256, 2, 2, BLOCK_A, false>;
+template <bool BLOCK_A, bool FULL> using Mid = Tile8<128, 128, 2, 2, BLOCK_A, FULL>;
 
 // Tiles of segments: each expert with a choice may have one that is not full.
 unsigned grid_of(const ExpertProductArgs &a, int ti, int tj)
@@ -488,7 +576,11 @@ unsigned grid_of(const ExpertProductArgs &a, int ti, int tj)
 template <int FJ>
 hipError_t narrow(const ExpertProductArgs &a, hipStream_t stream)
 {
-    narrow_kernel<FJ><<<dim3(grid_of(a, kNarrowI, 16 * FJ)), dim3(kNarrowThreads), 0, stream>>>(a, tiles(a.n, kNarrowI));
+    const dim3 grid(grid_of(a, kNarrowI, 16 * FJ)), threads(kNarrowThreads);
+    if (a.bf16)
+        narrow_kernel<FJ, false><<<grid, threads, 0, stream>>>(a, tiles(a.n, kNarrowI));
+    else
+        narrow_kernel<FJ, true><<<grid, threads, 0, stream>>>(a, tiles(a.n, kNarrowI));
     return hipGetLastError();
 }
 
@@ -521,8 +613,10 @@ hipError_t launch_expert_product(const Op &op, hipStream_t stream)
         return narrow<2>(a, stream);
     if (per <= 64)
         return narrow<4>(a, stream);
+    if (!a.bf16)
+        return product<Mid<true, true>>(a, stream);
     if (per <= 192)
-        return product<Mid<true>>(a, stream);
+        return product<Mid<true, false>>(a, stream);
     return product<Big<true>>(a, stream);
 }
 
@@ -530,8 +624,10 @@ hipError_t launch_expert_grad(const Op &op, hipStream_t stream)
 {
     const ExpertGradArgs a = op.get<ExpertGradArgs>();
     (void)hipGetLastError();
+    if (!a.bf16)
+        return grad<Mid<false, true>>(a, stream);
     if (int64_t(a.n) * a.k * a.experts < int64_t(256) * 256 * 256)
-        return grad<Mid<false>>(a, stream);
+        return grad<Mid<false, false>>(a, stream);
     return grad<Big<false>>(a, stream);
 }
 
