@@ -438,10 +438,15 @@ rr_status rr_expert_product(const rr_experts *e, int dtype, int32_t n, int32_t k
         return st;
     if (choices == 0)
         return set_ok();
+    // division by topk: 2^shift is the least power not below it
+    uint32_t shift = 0;
+    while ((1 << shift) < e->topk)
+        ++shift;
+    const uint32_t mul = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - uint64_t(e->topk))) / uint64_t(e->topk) + 1);
     Launches l(stream);
     l.add(launch_expert_product, ExpertProductArgs{eight(w, w_powers, k), eight(x, x_powers, k), weight, source, offset,
                                                    count, out, rows, n, k, e->experts, e->topk, int32_t(capacity),
-                                                   gather ? 1 : 0, dtype == RR_BF16, int32_t(choices)});
+                                                   gather ? 1 : 0, dtype == RR_BF16, int32_t(choices), int32_t(choices), mul, shift});
     return l.finish();
 }
 

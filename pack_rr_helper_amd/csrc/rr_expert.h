@@ -127,7 +127,8 @@ struct ExpertProductArgs {
     const int32_t *source, *offset, *count;
     void *out;
     int64_t rows;        // of x
-    int32_t n, k, experts, topk, capacity, gather, bf16, choices;
+    int32_t n, k, experts, topk, capacity, gather, bf16, choices, weights;
+    uint32_t topk_mul, topk_shift;  // n / topk = (high word of topk_mul * n + n) >> topk_shift, n < 2^31
 };
 hipError_t launch_expert_product(const Op &, hipStream_t);
 

@@ -236,10 +236,52 @@ __global__ __launch_bounds__(kNarrowThreads) void narrow_kernel(ExpertProductArg
 // Tiles through LDS
 // ---------------------------------------------------------------------------
 
-// One tile of C[j][i] = sum_k A[i][k] B[j][k].  Two steps of k, of 128 elements each,
-// lie in LDS in the layout of Tile (rr_product.h); a lane's 32 bytes of a row are its
-// chunks g and g + 4.  Powers come four steps at a time, a word for each row of the
-// tile.  A step is computed in two halves of the rows i.  While the first runs, the
+// A workgroup's tile, the same in all its lanes.
+struct Span {
+    int e, i0, j0;       // expert; first row of A and of B, or of the segment
+    int first, live;     // product: first position, positions from there on
+    int s0, s1;          // steps of k
+};
+
+// Where the workgroup's tables lie in LDS: of every expert the tiles of the experts before
+// it, its first position and its choices; the choices of two tiles, the weights of four.
+struct Tables {
+    int *before, *offset, *count, *list;
+    float *weight;
+};
+
+// Fills the tables; the number of segments' tiles, `wide` positions each.
+__device__ __forceinline__ int fill_tables(const Tables &t, const int32_t *offset, const int32_t *count, int experts, int wide)
+{
+    const int lane = threadIdx.x % 64;
+    int total = 0;
+    // every wave finds the total, the first one writes
+    for (int e0 = 0; e0 < experts; e0 += 64) {
+        const int e = e0 + lane, n = e < experts ? count[e] : 0, m = (n + wide - 1) / wide;
+        int sum = m;
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_up(sum, d);
+            sum += lane >= d ? o : 0;
+        }
+        if (threadIdx.x < 64 && e < experts) {
+            t.before[e] = total + sum - m;
+            t.offset[e] = offset[e];
+            t.count[e] = n;
+        }
+        total += __shfl(sum, 63);
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(total);
+}
+
+// A workgroup computes tiles of C[j][i] = sum_k A[i][k] B[j][k] one after the other.
+// Steps of 128 elements of k, of one tile and then of the next, are loaded two ahead
+// into two places in LDS (the layout of Tile, rr_product.h; a lane's 32 bytes of a row are
+// its chunks g and g + 4), so that the matrix units do not wait where tiles change:
+// with a workgroup for each tile 8192 x 8 choices of 32 experts, 4096 x 2048, took
+// @@
+// Powers come four steps at a time, a word for each row of the tile.
+// A step is computed in two halves of the rows i.  While the first runs, the
 // second's fragments are read; into the second, one barrier says that this step has
 // been read by all and that the next one has arrived.
 // BLOCK_A: the rows of a wave share one power.
@@ -250,21 +292,23 @@ struct Tile8 {
     static constexpr int kRows = 8 * kWaves, kLoadBytes = kRows * kRowBytes;
     static constexpr int kLoadsA = TI / kRows, kLoadsB = TJ / kRows, kLoadsP = (TI + TJ) / kThreads;
     static constexpr int kStageBytes = (TI + TJ) * kRowBytes, kPowerBytes = (TI + TJ) * 4;
-    static constexpr int kLdsBytes = 2 * kStageBytes + 2 * kPowerBytes;
-    // waves a SIMD has room for, which the registers are divided by
-    static constexpr int kPerSimd = 160 * 1024 / kLdsBytes * kWaves / 4;
+    static constexpr int kFixedBytes = 2 * kStageBytes + 2 * kPowerBytes + 6 * TJ * 4;
+    // workgroups on a compute unit (of 512 experts at most), and waves on a SIMD, which
+    // its registers are divided by
+    static constexpr int kPerUnit = 160 * 1024 / (kFixedBytes + 12 * 512), kPerSimd = kPerUnit * kWaves / 4;
+    static constexpr bool kFull = FULL;  // results in 32 bits
     static_assert(kLoadsP * kThreads == TI + TJ && TI % 64 == 0, "a wave loads the powers of one operand");
     static_assert(!BLOCK_A || RR_QUANT_BLOCK % (FI * 16) == 0, "");
     static_assert(FJ >= 4 && H >= 1, "");
-    static constexpr bool kFull = FULL;  // results in 32 bits
     // results leave as those of a product in bf16 and fp32 do
-    template <bool BF16>
-    using Out = Tile<BF16, TI, TJ, WI, WJ, 2, true>;
+    using Out = Tile<!FULL, TI, TJ, WI, WJ, 2, true>;
 
-    __amdgpu_buffer_rsrc_t a, b, power[kLoadsP];
-    int off_a[kLoadsA], off_b[kLoadsB], off_power[kLoadsP];
-    char *lds;
-    int s0, s1;
+    static int lds_bytes(int experts) { return kFixedBytes + 12 * experts; }
+    __device__ static Tables tables(char *lds, int experts)
+    {
+        int *t = reinterpret_cast<int *>(lds + 2 * kStageBytes + 2 * kPowerBytes);
+        return Tables{t + 6 * TJ, t + 6 * TJ + experts, t + 6 * TJ + 2 * experts, t, reinterpret_cast<float *>(t + 2 * TJ)};
+    }
 
     // Bytes of a buffer from its first row on, below kNowhere.
     __device__ static __amdgpu_buffer_rsrc_t buffer(const void *p, int64_t bytes)
@@ -272,206 +316,269 @@ struct Tile8 {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0,
                                                  int(bytes < kNowhere ? bytes : kNowhere), kBufferFormat);
     }
+    __device__ static int wave() { return __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64); }
+    __device__ static int wave_i() { return wave() % WI * (FI * 16); }
+    __device__ static int wave_j() { return wave() / WI * (FJ * 16); }
 
-    // ra(i), rb(j): the rows in the buffers of the tile's rows, -1 for none; pa: the same in
-    // A's powers.
-    template <typename RA, typename RB, typename PA>
-    __device__ void start(const Eight &x, int64_t bytes_a, int64_t power_a, const Eight &y, int64_t bytes_b,
-                          int64_t power_b, RA ra, RB rb, PA pa, int first, int last, char *buffer_lds)
-    {
-        const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-        lds = buffer_lds;
-        s0 = first;
-        s1 = last;
-        a = buffer(x.values, bytes_a);
-        b = buffer(y.values, bytes_b);
-        const int row0 = wave * 8 + lane / 8, chunk = ((lane % 8) ^ ((row0 >> 1) & 7)) * 16;
-#pragma unroll
-        for (int l = 0; l < kLoadsA; ++l) {
-            const int r = ra(l * kRows + row0);
-            off_a[l] = r >= 0 ? int(r * x.ld) + chunk : kNowhere;
-        }
-#pragma unroll
-        for (int l = 0; l < kLoadsB; ++l) {
-            const int r = rb(l * kRows + row0);
-            off_b[l] = r >= 0 ? int(r * y.ld) + chunk : kNowhere;
-        }
-#pragma unroll
-        for (int l = 0; l < kLoadsP; ++l) {
-            const int row = l * kThreads + int(threadIdx.x);
-            const bool of_a = l * kThreads + __builtin_amdgcn_readfirstlane(wave) * 64 < TI;
-            power[l] = of_a ? buffer(x.powers, power_a) : buffer(y.powers, power_b);
-            const int r = of_a ? pa(row) : rb(row - TI);
-            off_power[l] = r >= 0 ? int(r * (of_a ? x.lds : y.lds)) : kNowhere;
-        }
-        fetch_powers(s0 / 4);
-        if (s0 % 4 == 3)
-            fetch_powers(s0 / 4 + 1);
-        fetch(s0);
-        fetch(s0 + 1);
-    }
-    __device__ void fetch(int s) const
-    {
-        char *to = lds + s % 2 * kStageBytes + threadIdx.x / 64 * 1024;
-        const bool in = s < s1;
-        const int k = in ? s * kRowBytes : 0;
-#pragma unroll
-        for (int l = 0; l < kLoadsA; ++l)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(a, lds_pointer(to + l * kLoadBytes), 16, in ? off_a[l] : kNowhere, k, 0, 0);
-#pragma unroll
-        for (int l = 0; l < kLoadsB; ++l)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(b, lds_pointer(to + (kLoadsA + l) * kLoadBytes), 16,
-                                                     in ? off_b[l] : kNowhere, k, 0, 0);
-    }
-    __device__ char *powers(int group) const { return lds + 2 * kStageBytes + group % 2 * kPowerBytes; }
-    // Four steps' powers, from step 4 * group on.
-    __device__ void fetch_powers(int group) const
-    {
-        const bool in = 4 * group < s1;
-#pragma unroll
-        for (int l = 0; l < kLoadsP; ++l)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(power[l], lds_pointer(powers(group) + (l * kThreads + threadIdx.x / 64 * 64) * 4), 4,
-                                                     in ? off_power[l] : kNowhere, in ? group * 4 : 0, 0, 0);
-    }
+    // The steps of a tile that are still to be loaded.
+    struct Source {
+        __amdgpu_buffer_rsrc_t a, b, power[kLoadsP];
+        int off_a[kLoadsA], off_b[kLoadsB], off_power[kLoadsP];
+        int s, s1, group;  // group: of powers, counted over all tiles
 
-    __device__ static int wave_i() { return (threadIdx.x / 64) % WI * (FI * 16); }
-    __device__ static int wave_j() { return (threadIdx.x / 64) / WI * (FJ * 16); }
+        // ra(i), rb(j): the rows in the buffers of the tile's rows, -1 for none; pa: the same
+        // in A's powers.
+        template <typename RA, typename RB, typename PA>
+        __device__ void open(const Eight &x, int64_t bytes_a, int64_t power_a, const Eight &y, int64_t bytes_b,
+                             int64_t power_b, RA ra, RB rb, PA pa, const Span &span)
+        {
+            const int lane = threadIdx.x % 64;
+            s = span.s0;
+            s1 = span.s1;
+            group += s < s1;  // a tile without steps has no powers
+            a = buffer(x.values, bytes_a);
+            b = buffer(y.values, bytes_b);
+            const int row0 = wave() * 8 + lane / 8, chunk = ((lane % 8) ^ ((row0 >> 1) & 7)) * 16;
+#pragma unroll
+            for (int l = 0; l < kLoadsA; ++l) {
+                const int r = ra(l * kRows + row0);
+                off_a[l] = r >= 0 ? r * int(x.ld) + chunk : kNowhere;
+            }
+#pragma unroll
+            for (int l = 0; l < kLoadsB; ++l) {
+                const int r = rb(l * kRows + row0);
+                off_b[l] = r >= 0 ? r * int(y.ld) + chunk : kNowhere;
+            }
+#pragma unroll
+            for (int l = 0; l < kLoadsP; ++l) {
+                const int row = l * kThreads + int(threadIdx.x);
+                const bool of_a = l * kThreads + wave() * 64 < TI;
+                power[l] = of_a ? buffer(x.powers, power_a) : buffer(y.powers, power_b);
+                const int r = of_a ? pa(row) : rb(row - TI);
+                off_power[l] = r >= 0 ? r * int(of_a ? x.lds : y.lds) : kNowhere;
+            }
+        }
+        // No more tiles: loads give zeros.
+        __device__ void close()
+        {
+            s = 0;
+            s1 = 1 << 30;
+            ++group;
+            a = buffer(nullptr, 0);
+            b = buffer(nullptr, 0);
+#pragma unroll
+            for (int l = 0; l < kLoadsP; ++l)
+                power[l] = buffer(nullptr, 0);
+        }
+        static constexpr int kLoads = kLoadsP + kLoadsA + kLoadsB;
+        // Load l of the next step, to place `stage` in LDS.
+        __device__ void load(int l, char *lds, int stage) const
+        {
+            char *to = lds + stage * kStageBytes + wave() * 1024;
+            if (l < kLoadsA)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(a, lds_pointer(to + l * kLoadBytes), 16, off_a[l], s * kRowBytes, 0, 0);
+            else if (l < kLoadsA + kLoadsB)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(b, lds_pointer(to + l * kLoadBytes), 16, off_b[l - kLoadsA], s * kRowBytes, 0, 0);
+            else
+                // a word holds four steps: fetched again in each of them
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(power[l - kLoadsA - kLoadsB],
+                    lds_pointer(lds + 2 * kStageBytes + group % 2 * kPowerBytes + wave() * 256 + (l - kLoadsA - kLoadsB) * kThreads * 4), 4,
+                    off_power[l - kLoadsA - kLoadsB], s / 4 * 4, 0, 0);
+        }
+        __device__ void next()
+        {
+            ++s;
+            group += s % 4 == 0 && s < s1;
+        }
+    };
 
-    __device__ static i32x8 fragment(const char *stage, int f)
+    // A lane's 32 bytes of a row of 16, read in two halves.
+    struct Fragment {
+        u32x4 half[2];
+
+        __device__ void read(const char *stage, int f, int h)
+        {
+            const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
+            half[h] = *reinterpret_cast<const u32x4 *>(stage + (f + r) * kRowBytes + ((4 * h + g) ^ (r >> 1)) * 16);
+        }
+        __device__ i32x8 value() const { return __builtin_bit_cast(i32x8, half); }
+    };
+    __device__ static void read_a(Fragment *fa, const char *lds, int stage, int n)
     {
-        const int lane = threadIdx.x % 64, g = lane / 16, r = lane % 16;
-        struct {
-            u32x4 lo, hi;
-        } v;
-        v.lo = *reinterpret_cast<const u32x4 *>(stage + (f + r) * kRowBytes + (g ^ (r >> 1)) * 16);
-        v.hi = *reinterpret_cast<const u32x4 *>(stage + (f + r) * kRowBytes + ((4 + g) ^ (r >> 1)) * 16);
-        return __builtin_bit_cast(i32x8, v);
+        fa[n / 2].read(lds + stage * kStageBytes, wave_i() + n / 2 * 16, n % 2);
     }
-    __device__ i32x8 read_a(int s, int f) const { return fragment(lds + s % 2 * kStageBytes, wave_i() + f * 16); }
-    __device__ i32x8 read_b(int s, int f) const
+    __device__ static void read_b(Fragment *fb, const char *lds, int stage, int n)
     {
-        return fragment(lds + s % 2 * kStageBytes + kLoadsA * kLoadBytes, wave_j() + f * 16);
+        fb[n / 2].read(lds + stage * kStageBytes + kLoadsA * kLoadBytes, wave_j() + n / 2 * 16, n % 2);
     }
 
     static constexpr int kPowersA = BLOCK_A ? 1 : FI;
     struct Powers {
         unsigned a[kPowersA], b[FJ];
+
+        __device__ void read(const char *lds, int group)
+        {
+            const unsigned *at = reinterpret_cast<const unsigned *>(lds + 2 * kStageBytes + group % 2 * kPowerBytes) + threadIdx.x % 16;
+#pragma unroll
+            for (int f = 0; f < kPowersA; ++f)
+                a[f] = at[wave_i() + f * 16];
+#pragma unroll
+            for (int f = 0; f < FJ; ++f)
+                b[f] = at[TI + wave_j() + f * 16];
+        }
+        // Those of step s in the low bytes.
+        __device__ Powers of(int s) const
+        {
+            Powers p;
+#pragma unroll
+            for (int f = 0; f < kPowersA; ++f)
+                p.a[f] = a[f] >> s % 4 * 8;
+#pragma unroll
+            for (int f = 0; f < FJ; ++f)
+                p.b[f] = b[f] >> s % 4 * 8;
+            return p;
+        }
     };
-    __device__ void read_powers(int s, Powers &p) const
-    {
-        const unsigned *at = reinterpret_cast<const unsigned *>(powers(s / 4)) + threadIdx.x % 16;
-#pragma unroll
-        for (int f = 0; f < kPowersA; ++f)
-            p.a[f] = at[wave_i() + f * 16];
-#pragma unroll
-        for (int f = 0; f < FJ; ++f)
-            p.b[f] = at[TI + wave_j() + f * 16];
-    }
-    // The powers of step s in the low bytes.
-    __device__ static void shift(const Powers &from, int s, Powers &to)
-    {
-#pragma unroll
-        for (int f = 0; f < kPowersA; ++f)
-            to.a[f] = from.a[f] >> s % 4 * 8;
-#pragma unroll
-        for (int f = 0; f < FJ; ++f)
-            to.b[f] = from.b[f] >> s % 4 * 8;
-    }
     struct Acc {
         f32x4 c[FI][FJ];
-    };
 
-    // This step has been read by all, and the next one has arrived.
-    __device__ void advance(int s, Powers &raw) const
-    {
-        wait_loads<0>();
-        __builtin_amdgcn_s_barrier();
-        fetch(s + 2);
-        if ((s + 2) % 4 == 0)
-            fetch_powers((s + 2) / 4);
-        if ((s + 1) % 4 == 0)
-            read_powers(s + 1, raw);
-    }
-
-    // acc += the products of steps [s0, s1), of which there is at least one
-    __device__ void finish(Acc &acc) const
-    {
-        i32x8 fa[FI], fb[FJ];
-        Powers raw, at;
-        wait_loads<kLoadsA + kLoadsB>();
-        __builtin_amdgcn_s_barrier();
+        __device__ void clear()
+        {
 #pragma unroll
-        for (int f = 0; f < FJ; ++f)
-            fb[f] = read_b(s0, f);
-#pragma unroll
-        for (int f = 0; f < (FULL ? FI : H); ++f)
-            fa[f] = read_a(s0, f);
-        read_powers(s0, raw);
-        if constexpr (FULL) {
-            for (int s = s0; s < s1; ++s) {
-                shift(raw, s, at);
-                Wide wb[FJ];
+            for (int i = 0; i < FI; ++i)
 #pragma unroll
                 for (int j = 0; j < FJ; ++j)
-                    wb[j].set(fb[j], at.b[j]);
-#pragma unroll
-                for (int i = 0; i < FI; ++i) {
-                    Wide wa;
-                    wa.set(fa[i], at.a[BLOCK_A ? 0 : i]);
-#pragma unroll
-                    for (int j = 0; j < FJ; ++j)
-                        multiply(wa, wb[j], acc.c[i][j]);
-                    if (i == 0)
-                        advance(s, raw);
-                    if (i == 0 || i == 1) {
-#pragma unroll
-                        for (int f = i * FJ / 2; f < (i + 1) * FJ / 2; ++f)
-                            fb[f] = read_b(s + 1, f);
-                    }
-                    fa[i] = read_a(s + 1, i);
+                    c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    };
+
+    // Tiles t0, t0 + stride, .. below `tiles`.  job.span(t): tile t; job.open(source, t, n):
+    // the source of the n-th; job.first(t): before it is opened; job.end(span, n, acc):
+    // its results.
+    template <typename Job>
+    __device__ static void run(const Job &job, int t0, int stride, int tiles, char *lds)
+    {
+        Source source;
+        source.s = source.s1 = 0;
+        source.group = -1;
+        int to_open = t0, opened = 0, stage = 0, group = 0;
+        const auto refill = [&] {
+            while (source.s == source.s1) {
+                if (to_open >= tiles) {
+                    source.close();
+                    return;
                 }
+                job.open(source, to_open, to_open + stride < tiles ? to_open + stride : -1, opened++);
+                to_open += stride;
             }
-        } else {
-            for (int s = s0; s < s1; ++s) {
-                shift(raw, s, at);
+        };
+        if (t0 >= tiles)
+            return;
+        job.first(t0);
+        Acc acc;
+        Fragment fa[FI], fb[FJ];
+        Powers raw;
 #pragma unroll
-                for (int j = 0; j < FJ; ++j) {
+        for (int f = 0; f < 2; ++f) {
+            refill();
 #pragma unroll
-                    for (int i = 0; i < H; ++i)
-                        multiply<0, 0>(fa[i], fb[j], acc.c[i][j], at.a[BLOCK_A ? 0 : i], at.b[j]);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (j < (H + 1) / 2) {
-#pragma unroll
-                        for (int f = H + 2 * j; f < H + 2 * j + 2 && f < FI; ++f)
-                            fa[f] = read_a(s, f);
-                    }
-                }
-                constexpr int kAt = FJ / 4 - 1;  // the barrier: after this column of the second half
-#pragma unroll
-                for (int j = 0; j < FJ; ++j) {
-#pragma unroll
-                    for (int i = H; i < FI; ++i)
-                        multiply<0, 0>(fa[i], fb[j], acc.c[i][j], at.a[BLOCK_A ? 0 : i], at.b[j]);
-                    if (j == kAt) {
-                        advance(s, raw);
-#pragma unroll
-                        for (int f = 0; f < kAt; ++f)
-                            fb[f] = read_b(s + 1, f);
-                    }
-                    if (j >= kAt) {
-                        fb[j] = read_b(s + 1, j);
-                        constexpr int kOver = FJ - 1 - kAt;  // a's first half over the columns left
-#pragma unroll
-                        for (int f = (j - kAt) * H / kOver; f < (j - kAt + 1) * H / kOver && f < H; ++f)
-                            fa[f] = read_a(s + 1, f);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+            for (int l = 0; l < Source::kLoads; ++l)
+                source.load(l, lds, f);
+            source.next();
+            if (f == 0) {
+                // what the next tile's source needs is there
+                wait_loads<0>();
+                __builtin_amdgcn_s_barrier();
             }
         }
-        // the loads past s1 have written zeros: LDS is free after this
+#pragma unroll
+        for (int n = 0; n < 2 * FJ; ++n)
+            read_b(fb, lds, 0, n);
+#pragma unroll
+        for (int n = 0; n < 2 * (FULL ? FI : H); ++n)
+            read_a(fa, lds, 0, n);
+        raw.read(lds, 0);
+        int turn = 0;
+        for (int t = t0; t < tiles; t += stride, ++turn) {
+            const Span span = job.span(t);
+            acc.clear();
+            for (int s = span.s0; s < span.s1; ++s, stage ^= 1) {
+                refill();
+                // one block without branches from here on: memory operations in the
+                // shadow of matrix instructions, a few at a time
+                const Powers at = raw.of(s);
+                group += (s + 1) % 4 == 0 || s + 1 == span.s1;
+                if constexpr (FULL) {
+                    Wide wb[FJ];
+#pragma unroll
+                    for (int j = 0; j < FJ; ++j)
+                        wb[j].set(fb[j].value(), at.b[j]);
+#pragma unroll
+                    for (int i = 0; i < FI; ++i) {
+                        Wide wa;
+                        wa.set(fa[i].value(), at.a[BLOCK_A ? 0 : i]);
+                        if (i == 0) {
+                            // this step has been read by all, and the next one has arrived
+                            wait_loads<0>();
+                            __builtin_amdgcn_s_barrier();
+                        }
+#pragma unroll
+                        for (int j = 0; j < FJ; ++j) {
+                            multiply(wa, wb[j], acc.c[i][j]);
+                            constexpr int kPer = (Source::kLoads + FJ - 1) / FJ;
+                            if (i == 0)
+#pragma unroll
+                                for (int l = j * kPer; l < j * kPer + kPer && l < Source::kLoads; ++l)
+                                    source.load(l, lds, stage);
+                            if (i == 1)
+#pragma unroll
+                                for (int n = j * 2; n < j * 2 + 2; ++n)
+                                    read_b(fb, lds, stage ^ 1, n);
+                            if (i >= FI / 2 && j < 4) {
+                                constexpr int kRead = FI / (FI - FI / 2);
+#pragma unroll
+                                for (int n = ((i - FI / 2) * 4 + j) * kRead / 2; n < ((i - FI / 2) * 4 + j + 1) * kRead / 2; ++n)
+                                    if (n < 2 * i)
+                                        read_a(fa, lds, stage ^ 1, n);
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+                    read_a(fa, lds, stage ^ 1, 2 * FI - 2);
+                    read_a(fa, lds, stage ^ 1, 2 * FI - 1);
+                    raw.read(lds, group);
+                } else {
+                    constexpr int kHalf = H * FJ, kBarrier = kHalf - kHalf / 8;
+#pragma unroll
+                    for (int m = 0; m < 2 * kHalf; ++m) {
+                        const int j = m % kHalf / H, i = m / kHalf * H + m % H;
+                        multiply<0, 0>(fa[i].value(), fb[j].value(), acc.c[i][j], at.a[BLOCK_A ? 0 : i], at.b[j]);
+                        // a's second half, every other time
+                        if (m % 2 == 1 && m / 2 < 2 * (FI - H))
+                            read_a(fa, lds, stage, 2 * H + m / 2);
+                        if (m == kBarrier) {
+                            // this step has been read by all, and the next one has arrived
+                            wait_loads<0>();
+                            __builtin_amdgcn_s_barrier();
+                        }
+                        if (m >= kBarrier && m - kBarrier < Source::kLoads)
+                            source.load(m - kBarrier, lds, stage);
+                        // b's columns once they have been used, with them a's first half
+                        if (m >= kHalf && m % H == H - 1) {
+                            read_b(fb, lds, stage ^ 1, 2 * j);
+                            read_b(fb, lds, stage ^ 1, 2 * j + 1);
+                        }
+                        if (m >= kHalf && m % H < 2 && (m - kHalf) / H * 2 + m % H < 2 * H)
+                            read_a(fa, lds, stage ^ 1, (m - kHalf) / H * 2 + m % H);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    raw.read(lds, group);
+                }
+                source.next();
+            }
+            job.end(span, turn, acc);
+        }
         wait_loads<0>();
-        __syncthreads();
     }
 };
 
@@ -483,82 +590,158 @@ __device__ __forceinline__ void store(const typename T::Acc &acc, int f, void *o
 #pragma unroll
     for (int i = 0; i < T::FI; ++i)
         v[i] = acc.c[i][f] * by;
-    T::template Out<!T::kFull>::store_row(static_cast<char *>(out) + at * (T::kFull ? 4 : 2), v, left);
+    T::Out::store_row(static_cast<char *>(out) + at * (T::kFull ? 4 : 2), v, left);
 }
+
+template <typename T>
+struct ProductJob {
+    const ExpertProductArgs &a;
+    Tables tables;
+    int tiles_i, tiles_j;
+
+    __device__ Span span(int t) const
+    {
+        int i, j;
+        tile_at(t, tiles_i * tiles_j, tiles_i, tiles_j, i, j);
+        int e = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 64) {
+            const int at = e0 + int(threadIdx.x % 64);
+            const int n = __popcll(__ballot(at < a.experts && tables.before[at] <= j));
+            e = e0 + n - 1;
+            if (n < 64)
+                break;
+        }
+        e = __builtin_amdgcn_readfirstlane(e);
+        Span s;
+        s.e = e;
+        s.i0 = __builtin_amdgcn_readfirstlane(i * T::TI);
+        s.j0 = __builtin_amdgcn_readfirstlane((j - tables.before[e]) * T::TJ);
+        s.first = __builtin_amdgcn_readfirstlane(tables.offset[e]) + s.j0;
+        s.live = __builtin_amdgcn_readfirstlane(tables.count[e]) - s.j0;
+        s.s0 = 0;
+        s.s1 = int(a.w.ld / RR_QUANT_BLOCK);
+        return s;
+    }
+    // Row of x, of choice n.
+    __device__ int row_of(int n) const { return n < 0 ? -1 : int((__umulhi(a.topk_mul, unsigned(n)) + unsigned(n)) >> a.topk_shift); }
+    // The choices of a tile, to list n; a wave for 64 of them.
+    __device__ void fetch_list(const Span &s, int n) const
+    {
+        if (T::wave() * 64 < T::TJ)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                T::buffer(a.source + s.first, int64_t(s.live) * 4),
+                lds_pointer(reinterpret_cast<char *>(tables.list + n % 2 * T::TJ + T::wave() * 64)), 4, int(threadIdx.x) * 4, 0, 0, 0);
+    }
+    __device__ bool listed() const { return a.gather || a.weight; }
+    __device__ void first(int t) const
+    {
+        if (listed()) {
+            fetch_list(span(t), 0);
+            wait_loads<0>();
+            __syncthreads();
+        }
+    }
+    __device__ void open(typename T::Source &source, int t, int next, int n) const
+    {
+        const Span s = span(t);
+        const int *list = tables.list + n % 2 * T::TJ;
+        const int blocks_n = (a.n + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK, rows_i = a.n - s.i0;
+        // from the tile's first row on; gathered rows may be anywhere
+        const Eight w{a.w.values + (int64_t(s.e) * a.n + s.i0) * a.w.ld,
+                      a.w.powers + (int64_t(s.e) * blocks_n + s.i0 / RR_QUANT_BLOCK) * a.w.lds, a.w.ld, a.w.lds};
+        const int base = a.gather ? 0 : s.first;
+        const Eight x{a.x.values + base * a.x.ld, a.x.powers + base * a.x.lds, a.x.ld, a.x.lds};
+        const int64_t rows_x = a.gather ? a.rows : s.live;
+        source.open(w, rows_i * w.ld, (blocks_n - s.i0 / RR_QUANT_BLOCK) * w.lds, x, rows_x * x.ld, rows_x * x.lds,
+                    [&](int i) { return i < rows_i ? i : -1; },
+                    [&](int j) {
+                        if (j >= s.live)
+                            return -1;
+                        if (!a.gather)
+                            return j;
+                        const int r = row_of(list[j]);
+                        return r < a.rows ? r : -1;
+                    },
+                    [&](int i) { return i < rows_i ? i / RR_QUANT_BLOCK : -1; }, s);
+        if (a.weight && T::wave() * 64 < T::TJ) {
+            const int j = int(threadIdx.x), at = j < s.live ? list[j] : -1;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                T::buffer(a.weight, int64_t(a.weights) * 4),
+                lds_pointer(reinterpret_cast<char *>(tables.weight + n % 4 * T::TJ + T::wave() * 64)), 4, at >= 0 ? at * 4 : kNowhere, 0, 0, 0);
+        }
+        if (listed() && next >= 0)
+            fetch_list(span(next), n + 1);
+    }
+    __device__ void end(const Span &s, int n, const typename T::Acc &acc) const
+    {
+#pragma unroll
+        for (int f = 0; f < T::FJ; ++f) {
+            const int j = T::wave_j() + f * 16 + int(threadIdx.x % 16);
+            const float by = a.weight ? tables.weight[n % 4 * T::TJ + j] : 1.0f;
+            store<T>(acc, f, a.out, int64_t(s.first + j) * a.n + s.i0, j < s.live ? a.n - s.i0 : 0, by);
+        }
+    }
+};
 
 template <typename T>
 __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void product_kernel(ExpertProductArgs a, int tiles_i)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    Place at;
-    if (!place_of(a.count, a.experts, T::TJ, tiles_i, at))
-        return;
-    const int blocks_n = (a.n + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK;
-    const int i0 = at.i * T::TI, j0 = at.j * T::TJ, live = a.count[at.e] - j0, first = a.offset[at.e] + j0;
-    const int rows_i = a.n - i0;
-    // from the tile's first row on; gathered rows may be anywhere
-    const Eight w{a.w.values + (int64_t(at.e) * a.n + i0) * a.w.ld,
-                  a.w.powers + (int64_t(at.e) * blocks_n + i0 / RR_QUANT_BLOCK) * a.w.lds, a.w.ld, a.w.lds};
-    const int base = a.gather ? 0 : first;
-    const Eight x{a.x.values + base * a.x.ld, a.x.powers + base * a.x.lds, a.x.ld, a.x.lds};
-    const int64_t rows_x = a.gather ? a.rows : live;
-    T t;
-    t.start(w, rows_i * w.ld, (blocks_n - i0 / RR_QUANT_BLOCK) * w.lds, x, rows_x * x.ld, rows_x * x.lds,
-            [&](int i) { return i < rows_i ? i : -1; },
-            [&](int j) {
-                const int r = row_of(a, first + j, j < live);
-                return r < 0 ? -1 : r - base;
-            },
-            [&](int i) { return i < rows_i ? i / RR_QUANT_BLOCK : -1; }, 0, int(a.w.ld / RR_QUANT_BLOCK), lds);
-    typename T::Acc acc;
-#pragma unroll
-    for (int i = 0; i < T::FI; ++i)
-#pragma unroll
-        for (int j = 0; j < T::FJ; ++j)
-            acc.c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    t.finish(acc);
-#pragma unroll
-    for (int f = 0; f < T::FJ; ++f) {
-        const int j = T::wave_j() + f * 16 + int(threadIdx.x % 16);
-        const int p = first + j, left = j < live ? rows_i : 0;
-        const float by = weight_of(a, p, j < live);
-        const int64_t to = int64_t(p) * a.n + i0;
-        store<T>(acc, f, a.out, to, left, by);
-    }
+    const Tables tables = T::tables(lds, a.experts);
+    const int tiles_j = fill_tables(tables, a.offset, a.count, a.experts, T::TJ);
+    const ProductJob<T> job{a, tables, tiles_i, tiles_j};
+    T::run(job, int(blockIdx.x), int(gridDim.x), tiles_i * tiles_j, lds);
 }
 
 // dw[e][j][i] = sum over the segment's positions of x[i][p] dy[j][p].
 template <typename T>
+struct GradJob {
+    const ExpertGradArgs &a;
+    Tables tables;
+    int tiles_i, tiles_j;
+
+    __device__ Span span(int t) const
+    {
+        const int e = t / (tiles_i * tiles_j);
+        int i, j;
+        tile_at(t - e * tiles_i * tiles_j, tiles_i * tiles_j, tiles_i, tiles_j, i, j);
+        Span s{};
+        s.e = e;
+        s.i0 = i * T::TI;
+        s.j0 = j * T::TJ;
+        s.s0 = __builtin_amdgcn_readfirstlane(tables.offset[e]) / RR_QUANT_BLOCK;
+        s.s1 = s.s0 + (__builtin_amdgcn_readfirstlane(tables.count[e]) + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK;
+        return s;
+    }
+    __device__ void first(int) const {}
+    __device__ void open(typename T::Source &source, int t, int, int) const
+    {
+        const Span s = span(t);
+        const int rows_i = a.k - s.i0, rows_j = a.n - s.j0;
+        const Eight x{a.x.values + s.i0 * a.x.ld, a.x.powers + s.i0 * a.x.lds, a.x.ld, a.x.lds};
+        const Eight dy{a.dy.values + s.j0 * a.dy.ld, a.dy.powers + s.j0 * a.dy.lds, a.dy.ld, a.dy.lds};
+        source.open(x, rows_i * x.ld, rows_i * x.lds, dy, rows_j * dy.ld, rows_j * dy.lds,
+                    [&](int i) { return i < rows_i ? i : -1; }, [&](int j) { return j < rows_j ? j : -1; },
+                    [&](int i) { return i < rows_i ? i : -1; }, s);
+    }
+    __device__ void end(const Span &s, int, const typename T::Acc &acc) const
+    {
+#pragma unroll
+        for (int f = 0; f < T::FJ; ++f) {
+            const int j = s.j0 + T::wave_j() + f * 16 + int(threadIdx.x % 16);
+            store<T>(acc, f, a.dw, (int64_t(s.e) * a.n + j) * a.k + s.i0, j < a.n ? a.k - s.i0 : 0, 1.0f);
+        }
+    }
+};
+
+template <typename T>
 __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void grad_kernel(ExpertGradArgs a, int tiles_i, int tiles_j)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const int e = blockIdx.x / (tiles_i * tiles_j);
-    int ti, tj;
-    tile_at(int(blockIdx.x) - e * tiles_i * tiles_j, tiles_i * tiles_j, tiles_i, tiles_j, ti, tj);
-    const int i0 = ti * T::TI, j0 = tj * T::TJ, rows_i = a.k - i0, rows_j = a.n - j0;
-    const int s0 = a.offset[e] / RR_QUANT_BLOCK, steps = (a.count[e] + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK;
-    typename T::Acc acc;
-#pragma unroll
-    for (int i = 0; i < T::FI; ++i)
-#pragma unroll
-        for (int j = 0; j < T::FJ; ++j)
-            acc.c[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (steps > 0) {
-        const Eight x{a.x.values + i0 * a.x.ld, a.x.powers + i0 * a.x.lds, a.x.ld, a.x.lds};
-        const Eight dy{a.dy.values + j0 * a.dy.ld, a.dy.powers + j0 * a.dy.lds, a.dy.ld, a.dy.lds};
-        T t;
-        t.start(x, rows_i * x.ld, rows_i * x.lds, dy, rows_j * dy.ld, rows_j * dy.lds,
-                [&](int i) { return i < rows_i ? i : -1; }, [&](int j) { return j < rows_j ? j : -1; },
-                [&](int i) { return i < rows_i ? i : -1; }, s0, s0 + steps, lds);
-        t.finish(acc);
-    }
-#pragma unroll
-    for (int f = 0; f < T::FJ; ++f) {
-        const int j = j0 + T::wave_j() + f * 16 + int(threadIdx.x % 16);
-        const int left = j < a.n ? rows_i : 0;
-        const int64_t to = (int64_t(e) * a.n + j) * a.k + i0;
-        store<T>(acc, f, a.dw, to, left, 1.0f);
-    }
+    const Tables tables = T::tables(lds, a.experts);
+    fill_tables(tables, a.offset, a.count, a.experts, T::TJ);
+    const GradJob<T> job{a, tables, tiles_i, tiles_j};
+    T::run(job, int(blockIdx.x), int(gridDim.x), tiles_i * tiles_j * a.experts, lds);
 }
 
 int tiles(int n, int per) { return n / per + (n % per != 0); }
@@ -566,17 +749,23 @@ int tiles(int n, int per) { return n / per + (n % per != 0); }
 template <bool BLOCK_A> using Big = Tile8<256, 256, 2, 2, BLOCK_A, false>;
 template <bool BLOCK_A, bool FULL> using Mid = Tile8<128, 128, 2, 2, BLOCK_A, FULL>;
 
-// Tiles of segments: each expert with a choice may have one that is not full.
-unsigned grid_of(const ExpertProductArgs &a, int ti, int tj)
+// Tiles of segments, at most: each expert with a choice may have one that is not full.
+int64_t most_tiles(const ExpertProductArgs &a, int ti, int tj)
 {
-    const int64_t j = a.choices / tj + (a.experts < a.choices ? a.experts : a.choices);
-    return unsigned(j * tiles(a.n, ti));
+    return (a.choices / tj + (a.experts < a.choices ? a.experts : a.choices)) * int64_t(tiles(a.n, ti));
+}
+
+// As many workgroups as the 256 compute units hold at a time.
+template <typename T>
+unsigned grid_for(int64_t n)
+{
+    return unsigned(n < 256 * T::kPerUnit ? n : 256 * T::kPerUnit);
 }
 
 template <int FJ>
 hipError_t narrow(const ExpertProductArgs &a, hipStream_t stream)
 {
-    const dim3 grid(grid_of(a, kNarrowI, 16 * FJ)), threads(kNarrowThreads);
+    const dim3 grid(unsigned(most_tiles(a, kNarrowI, 16 * FJ))), threads(kNarrowThreads);
     if (a.bf16)
         narrow_kernel<FJ, false><<<grid, threads, 0, stream>>>(a, tiles(a.n, kNarrowI));
     else
@@ -587,7 +776,7 @@ hipError_t narrow(const ExpertProductArgs &a, hipStream_t stream)
 template <typename T>
 hipError_t product(const ExpertProductArgs &a, hipStream_t stream)
 {
-    product_kernel<T><<<dim3(grid_of(a, T::TI, T::TJ)), dim3(T::kThreads), T::kLdsBytes, stream>>>(a, tiles(a.n, T::TI));
+    product_kernel<T><<<dim3(grid_for<T>(most_tiles(a, T::TI, T::TJ))), dim3(T::kThreads), T::lds_bytes(a.experts), stream>>>(a, tiles(a.n, T::TI));
     return hipGetLastError();
 }
 
@@ -595,7 +784,7 @@ template <typename T>
 hipError_t grad(const ExpertGradArgs &a, hipStream_t stream)
 {
     const int ti = tiles(a.k, T::TI), tj = tiles(a.n, T::TJ);
-    grad_kernel<T><<<dim3(unsigned(ti) * unsigned(tj) * unsigned(a.experts)), dim3(T::kThreads), T::kLdsBytes, stream>>>(a, ti, tj);
+    grad_kernel<T><<<dim3(grid_for<T>(int64_t(ti) * tj * a.experts)), dim3(T::kThreads), T::lds_bytes(a.experts), stream>>>(a, ti, tj);
     return hipGetLastError();
 }
 
