@@ -244,11 +244,14 @@ struct Span {
 };
 
 // Where the workgroup's tables lie in LDS: of every expert the tiles of the experts before
-// it, its first position and its choices; the choices of two tiles, the weights of four.
+// it, its first position and its choices; the choices of two tiles, the weights of four;
+// what the workgroup's tiles are, as finding that out takes longer than looking it up.
 struct Tables {
     int *before, *offset, *count, *list;
     float *weight;
+    int4 *span;          // the workgroup's first kSpans tiles: e, i0, then j0 or first, live
 };
+constexpr int kSpans = 256;
 
 // Fills the tables; the number of segments' tiles, `wide` positions each.
 __device__ __forceinline__ int fill_tables(const Tables &t, const int32_t *offset, const int32_t *count, int experts, int wide)
@@ -292,7 +295,7 @@ struct Tile8 {
     static constexpr int kRows = 8 * kWaves, kLoadBytes = kRows * kRowBytes;
     static constexpr int kLoadsA = TI / kRows, kLoadsB = TJ / kRows, kLoadsP = (TI + TJ) / kThreads;
     static constexpr int kStageBytes = (TI + TJ) * kRowBytes, kPowerBytes = (TI + TJ) * 4;
-    static constexpr int kFixedBytes = 2 * kStageBytes + 2 * kPowerBytes + 6 * TJ * 4;
+    static constexpr int kFixedBytes = 2 * kStageBytes + 3 * kPowerBytes + 6 * TJ * 4 + kSpans * 16;
     // workgroups on a compute unit (of 512 experts at most), and waves on a SIMD, which
     // its registers are divided by
     static constexpr int kPerUnit = 160 * 1024 / (kFixedBytes + 12 * 512), kPerSimd = kPerUnit * kWaves / 4;
@@ -306,8 +309,8 @@ struct Tile8 {
     static int lds_bytes(int experts) { return kFixedBytes + 12 * experts; }
     __device__ static Tables tables(char *lds, int experts)
     {
-        int *t = reinterpret_cast<int *>(lds + 2 * kStageBytes + 2 * kPowerBytes);
-        return Tables{t + 6 * TJ, t + 6 * TJ + experts, t + 6 * TJ + 2 * experts, t, reinterpret_cast<float *>(t + 2 * TJ)};
+        int *t = reinterpret_cast<int *>(lds + 2 * kStageBytes + 3 * kPowerBytes), *e = t + 6 * TJ + 4 * kSpans;
+        return Tables{e, e + experts, e + 2 * experts, t, reinterpret_cast<float *>(t + 2 * TJ), reinterpret_cast<int4 *>(t + 6 * TJ)};
     }
 
     // Bytes of a buffer from its first row on, below kNowhere.
@@ -325,6 +328,7 @@ struct Tile8 {
         __amdgpu_buffer_rsrc_t a, b, power[kLoadsP];
         int off_a[kLoadsA], off_b[kLoadsB], off_power[kLoadsP];
         int s, s1, group;  // group: of powers, counted over all tiles
+        bool words;        // this step's powers begin a word, or a tile
 
         // ra(i), rb(j): the rows in the buffers of the tile's rows, -1 for none; pa: the same
         // in A's powers.
@@ -336,6 +340,7 @@ struct Tile8 {
             s = span.s0;
             s1 = span.s1;
             group += s < s1;  // a tile without steps has no powers
+            words = true;
             a = buffer(x.values, bytes_a);
             b = buffer(y.values, bytes_b);
             const int row0 = wave() * 8 + lane / 8, chunk = ((lane % 8) ^ ((row0 >> 1) & 7)) * 16;
@@ -364,6 +369,7 @@ struct Tile8 {
             s = 0;
             s1 = 1 << 30;
             ++group;
+            words = false;
             a = buffer(nullptr, 0);
             b = buffer(nullptr, 0);
 #pragma unroll
@@ -380,15 +386,18 @@ struct Tile8 {
             else if (l < kLoadsA + kLoadsB)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(b, lds_pointer(to + l * kLoadBytes), 16, off_b[l - kLoadsA], s * kRowBytes, 0, 0);
             else
-                // a word holds four steps: fetched again in each of them
+                // a word holds four steps.  In the other three the load reads nothing (64
+                // rows of 4 bytes cost as much as 64 rows of 128) and leaves zeros where
+                // nothing lies.
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(power[l - kLoadsA - kLoadsB],
-                    lds_pointer(lds + 2 * kStageBytes + group % 2 * kPowerBytes + wave() * 256 + (l - kLoadsA - kLoadsB) * kThreads * 4), 4,
-                    off_power[l - kLoadsA - kLoadsB], s / 4 * 4, 0, 0);
+                    lds_pointer(lds + 2 * kStageBytes + (words ? group % 2 : 2) * kPowerBytes + wave() * 256 + (l - kLoadsA - kLoadsB) * kThreads * 4), 4,
+                    words ? off_power[l - kLoadsA - kLoadsB] : kNowhere, s / 4 * 4, 0, 0);
         }
         __device__ void next()
         {
             ++s;
-            group += s % 4 == 0 && s < s1;
+            words = s % 4 == 0;
+            group += words && s < s1;
         }
     };
 
@@ -452,29 +461,28 @@ struct Tile8 {
         }
     };
 
-    // Tiles t0, t0 + stride, .. below `tiles`.  job.span(t): tile t; job.open(source, t, n):
-    // the source of the n-th; job.first(t): before it is opened; job.end(span, n, acc):
-    // its results.
+    // A workgroup's tiles, `tiles` of them.  job.span(n): the n-th; job.first(): before it
+    // is opened; job.open(source, n, last): its source; job.end(span, n, acc): its results.
     template <typename Job>
-    __device__ static void run(const Job &job, int t0, int stride, int tiles, char *lds)
+    __device__ static void run(const Job &job, int tiles, char *lds)
     {
         Source source;
         source.s = source.s1 = 0;
         source.group = -1;
-        int to_open = t0, opened = 0, stage = 0, group = 0;
+        int opened = 0, stage = 0, group = 0;
         const auto refill = [&] {
             while (source.s == source.s1) {
-                if (to_open >= tiles) {
+                if (opened >= tiles) {
                     source.close();
                     return;
                 }
-                job.open(source, to_open, to_open + stride < tiles ? to_open + stride : -1, opened++);
-                to_open += stride;
+                job.open(source, opened, opened + 1 == tiles);
+                ++opened;
             }
         };
-        if (t0 >= tiles)
+        if (tiles <= 0)
             return;
-        job.first(t0);
+        job.first();
         Acc acc;
         Fragment fa[FI], fb[FJ];
         Powers raw;
@@ -492,15 +500,14 @@ struct Tile8 {
             }
         }
 #pragma unroll
-        for (int n = 0; n < 2 * FJ; ++n)
-            read_b(fb, lds, 0, n);
+        for (int h = 0; h < 2 * FJ; ++h)
+            read_b(fb, lds, 0, h);
 #pragma unroll
-        for (int n = 0; n < 2 * (FULL ? FI : H); ++n)
-            read_a(fa, lds, 0, n);
+        for (int h = 0; h < 2 * (FULL ? FI : H); ++h)
+            read_a(fa, lds, 0, h);
         raw.read(lds, 0);
-        int turn = 0;
-        for (int t = t0; t < tiles; t += stride, ++turn) {
-            const Span span = job.span(t);
+        for (int n = 0; n < tiles; ++n) {
+            const Span span = job.span(n);
             acc.clear();
             for (int s = span.s0; s < span.s1; ++s, stage ^= 1) {
                 refill();
@@ -532,14 +539,14 @@ struct Tile8 {
                                     source.load(l, lds, stage);
                             if (i == 1)
 #pragma unroll
-                                for (int n = j * 2; n < j * 2 + 2; ++n)
-                                    read_b(fb, lds, stage ^ 1, n);
+                                for (int h = j * 2; h < j * 2 + 2; ++h)
+                                    read_b(fb, lds, stage ^ 1, h);
                             if (i >= FI / 2 && j < 4) {
                                 constexpr int kRead = FI / (FI - FI / 2);
 #pragma unroll
-                                for (int n = ((i - FI / 2) * 4 + j) * kRead / 2; n < ((i - FI / 2) * 4 + j + 1) * kRead / 2; ++n)
-                                    if (n < 2 * i)
-                                        read_a(fa, lds, stage ^ 1, n);
+                                for (int h = ((i - FI / 2) * 4 + j) * kRead / 2; h < ((i - FI / 2) * 4 + j + 1) * kRead / 2; ++h)
+                                    if (h < 2 * i)
+                                        read_a(fa, lds, stage ^ 1, h);
                             }
                             __builtin_amdgcn_sched_barrier(0);
                         }
@@ -576,21 +583,65 @@ struct Tile8 {
                 }
                 source.next();
             }
-            job.end(span, turn, acc);
+            job.end(span, n, acc);
         }
         wait_loads<0>();
     }
 };
 
-// The lane's results of row j (fragment f, of the wave's) to out, the tile's first i.
-template <typename T>
-__device__ __forceinline__ void store(const typename T::Acc &acc, int f, void *out, int64_t at, int left, float by)
+// A tile's results times by(column of the tile) to out, from its first row and column on:
+// `rows` and `left` columns of them, ld elements a row.  Where rows lie in 16-byte chunks
+// a chunk is stored or not as a whole, without branches.
+template <typename T, typename BY>
+__device__ __forceinline__ void store(const typename T::Acc &acc, void *out, int64_t ld, int rows, int left, BY by)
 {
-    f32x4 v[T::FI];
+    constexpr int es = T::kFull ? 4 : 2, kChunks = T::kFull ? T::FI : T::FI / 2, kPer = 16 / es;
+    const int g = threadIdx.x % 64 / 16;
+    if (in_chunks(out, ld, es)) {
+        const __amdgpu_buffer_rsrc_t to = T::buffer(out, kNowhere);
+        int at[kChunks];
 #pragma unroll
-    for (int i = 0; i < T::FI; ++i)
-        v[i] = acc.c[i][f] * by;
-    T::Out::store_row(static_cast<char *>(out) + at * (T::kFull ? 4 : 2), v, left);
+        for (int c = 0; c < kChunks; ++c) {
+            // the columns that store_row gives a lane
+            const int i = T::wave_i() + (T::kFull ? c * 16 + g * 4 : (2 * c + g % 2) * 16 + g / 2 * 8);
+            at[c] = i < left ? i * es : kNowhere;
+        }
+        static_assert(kPer == (T::kFull ? 4 : 8), "");
+#pragma unroll
+        for (int f = 0; f < T::FJ; ++f) {
+            const int j = T::wave_j() + f * 16 + int(threadIdx.x % 16);
+            const int row = j < rows ? j * int(ld * es) : kNowhere;
+            const float w = by(j);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                u32x4 v;
+                if constexpr (T::kFull) {
+                    v = __builtin_bit_cast(u32x4, f32x4(acc.c[c][f] * w));
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const f32x4 lo = acc.c[2 * c][f] * w, hi = acc.c[2 * c + 1][f] * w;
+                        const auto s = __builtin_amdgcn_permlane16_swap(pack_bf16(lo[2 * n], lo[2 * n + 1]),
+                                                                        pack_bf16(hi[2 * n], hi[2 * n + 1]), false, false);
+                        v[n] = s[0];
+                        v[2 + n] = s[1];
+                    }
+                }
+                __builtin_amdgcn_raw_buffer_store_b128(v, to, int(unsigned(row) + unsigned(at[c])), 0, 0);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int f = 0; f < T::FJ; ++f) {
+        const int j = T::wave_j() + f * 16 + int(threadIdx.x % 16);
+        const float w = by(j);
+        f32x4 v[T::FI];
+#pragma unroll
+        for (int i = 0; i < T::FI; ++i)
+            v[i] = acc.c[i][f] * w;
+        T::Out::store_row(static_cast<char *>(out) + j * ld * es, v, j < rows ? left : 0);
+    }
 }
 
 template <typename T>
@@ -599,28 +650,25 @@ struct ProductJob {
     Tables tables;
     int tiles_i, tiles_j;
 
-    __device__ Span span(int t) const
+    // The n-th tile of the workgroup, by its thread: expert, first column, first position,
+    // positions from there on.
+    __device__ int4 find(int n) const
     {
         int i, j;
-        tile_at(t, tiles_i * tiles_j, tiles_i, tiles_j, i, j);
+        tile_at(int(blockIdx.x) + n * int(gridDim.x), tiles_i * tiles_j, tiles_i, tiles_j, i, j);
+        // the last expert with at most j tiles before it
         int e = 0;
-        for (int e0 = 0; e0 < a.experts; e0 += 64) {
-            const int at = e0 + int(threadIdx.x % 64);
-            const int n = __popcll(__ballot(at < a.experts && tables.before[at] <= j));
-            e = e0 + n - 1;
-            if (n < 64)
-                break;
-        }
-        e = __builtin_amdgcn_readfirstlane(e);
-        Span s;
-        s.e = e;
-        s.i0 = __builtin_amdgcn_readfirstlane(i * T::TI);
-        s.j0 = __builtin_amdgcn_readfirstlane((j - tables.before[e]) * T::TJ);
-        s.first = __builtin_amdgcn_readfirstlane(tables.offset[e]) + s.j0;
-        s.live = __builtin_amdgcn_readfirstlane(tables.count[e]) - s.j0;
-        s.s0 = 0;
-        s.s1 = int(a.w.ld / RR_QUANT_BLOCK);
-        return s;
+        for (int step = 512; step > 0; step /= 2)
+            if (e + step < a.experts && tables.before[e + step] <= j)
+                e += step;
+        const int j0 = (j - tables.before[e]) * T::TJ;
+        return int4{e, i * T::TI, tables.offset[e] + j0, tables.count[e] - j0};
+    }
+    __device__ Span span(int n) const
+    {
+        const int4 v = n < kSpans ? tables.span[n] : find(n);
+        return Span{__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y), 0,
+                    __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w), 0, int(a.w.ld / RR_QUANT_BLOCK)};
     }
     // Row of x, of choice n.
     __device__ int row_of(int n) const { return n < 0 ? -1 : int((__umulhi(a.topk_mul, unsigned(n)) + unsigned(n)) >> a.topk_shift); }
@@ -633,17 +681,17 @@ struct ProductJob {
                 lds_pointer(reinterpret_cast<char *>(tables.list + n % 2 * T::TJ + T::wave() * 64)), 4, int(threadIdx.x) * 4, 0, 0, 0);
     }
     __device__ bool listed() const { return a.gather || a.weight; }
-    __device__ void first(int t) const
+    __device__ void first() const
     {
         if (listed()) {
-            fetch_list(span(t), 0);
+            fetch_list(span(0), 0);
             wait_loads<0>();
             __syncthreads();
         }
     }
-    __device__ void open(typename T::Source &source, int t, int next, int n) const
+    __device__ void open(typename T::Source &source, int n, bool last) const
     {
-        const Span s = span(t);
+        const Span s = span(n);
         const int *list = tables.list + n % 2 * T::TJ;
         const int blocks_n = (a.n + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK, rows_i = a.n - s.i0;
         // from the tile's first row on; gathered rows may be anywhere
@@ -669,19 +717,27 @@ struct ProductJob {
                 T::buffer(a.weight, int64_t(a.weights) * 4),
                 lds_pointer(reinterpret_cast<char *>(tables.weight + n % 4 * T::TJ + T::wave() * 64)), 4, at >= 0 ? at * 4 : kNowhere, 0, 0, 0);
         }
-        if (listed() && next >= 0)
-            fetch_list(span(next), n + 1);
+        if (listed() && !last)
+            fetch_list(span(n + 1), n + 1);
     }
     __device__ void end(const Span &s, int n, const typename T::Acc &acc) const
     {
-#pragma unroll
-        for (int f = 0; f < T::FJ; ++f) {
-            const int j = T::wave_j() + f * 16 + int(threadIdx.x % 16);
-            const float by = a.weight ? tables.weight[n % 4 * T::TJ + j] : 1.0f;
-            store<T>(acc, f, a.out, int64_t(s.first + j) * a.n + s.i0, j < s.live ? a.n - s.i0 : 0, by);
-        }
+        void *out = static_cast<char *>(a.out) + (int64_t(s.first) * a.n + s.i0) * (T::kFull ? 4 : 2);
+        const float *by = a.weight ? tables.weight + n % 4 * T::TJ : nullptr;
+        store<T>(acc, out, a.n, s.live, a.n - s.i0, [=](int j) { return by ? by[j] : 1.0f; });
     }
 };
+
+// Tiles of the workgroup, of n in all; their spans to the table.
+template <typename Job>
+__device__ __forceinline__ int own_tiles(const Job &job, int n)
+{
+    const int own = int(blockIdx.x) < n ? (n - int(blockIdx.x) - 1) / int(gridDim.x) + 1 : 0;
+    for (int i = threadIdx.x; i < kSpans && i < own; i += blockDim.x)
+        job.tables.span[i] = job.find(i);
+    __syncthreads();
+    return own;
+}
 
 template <typename T>
 __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void product_kernel(ExpertProductArgs a, int tiles_i)
@@ -690,7 +746,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void product_kernel(Exper
     const Tables tables = T::tables(lds, a.experts);
     const int tiles_j = fill_tables(tables, a.offset, a.count, a.experts, T::TJ);
     const ProductJob<T> job{a, tables, tiles_i, tiles_j};
-    T::run(job, int(blockIdx.x), int(gridDim.x), tiles_i * tiles_j, lds);
+    T::run(job, own_tiles(job, tiles_i * tiles_j), lds);
 }
 
 // dw[e][j][i] = sum over the segment's positions of x[i][p] dy[j][p].
@@ -700,23 +756,26 @@ struct GradJob {
     Tables tables;
     int tiles_i, tiles_j;
 
-    __device__ Span span(int t) const
+    __device__ int4 find(int n) const
     {
-        const int e = t / (tiles_i * tiles_j);
+        const int t = int(blockIdx.x) + n * int(gridDim.x), e = t / (tiles_i * tiles_j);
         int i, j;
         tile_at(t - e * tiles_i * tiles_j, tiles_i * tiles_j, tiles_i, tiles_j, i, j);
-        Span s{};
-        s.e = e;
-        s.i0 = i * T::TI;
-        s.j0 = j * T::TJ;
-        s.s0 = __builtin_amdgcn_readfirstlane(tables.offset[e]) / RR_QUANT_BLOCK;
-        s.s1 = s.s0 + (__builtin_amdgcn_readfirstlane(tables.count[e]) + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK;
-        return s;
+        const int s0 = tables.offset[e] / RR_QUANT_BLOCK;
+        return int4{e, i * T::TI | j * T::TJ << 16, s0, s0 + (tables.count[e] + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK};
     }
-    __device__ void first(int) const {}
-    __device__ void open(typename T::Source &source, int t, int, int) const
+    __device__ Span span(int n) const
     {
-        const Span s = span(t);
+        static_assert(RR_MAX_WIDTH <= 1 << 16, "a tile's first row and column take a word");
+        const int4 v = n < kSpans ? tables.span[n] : find(n);
+        const unsigned ij = unsigned(__builtin_amdgcn_readfirstlane(v.y));
+        return Span{__builtin_amdgcn_readfirstlane(v.x), int(ij & 0xffff), int(ij >> 16), 0, 0,
+                    __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w)};
+    }
+    __device__ void first() const {}
+    __device__ void open(typename T::Source &source, int n, bool) const
+    {
+        const Span s = span(n);
         const int rows_i = a.k - s.i0, rows_j = a.n - s.j0;
         const Eight x{a.x.values + s.i0 * a.x.ld, a.x.powers + s.i0 * a.x.lds, a.x.ld, a.x.lds};
         const Eight dy{a.dy.values + s.j0 * a.dy.ld, a.dy.powers + s.j0 * a.dy.lds, a.dy.ld, a.dy.lds};
@@ -726,11 +785,8 @@ struct GradJob {
     }
     __device__ void end(const Span &s, int, const typename T::Acc &acc) const
     {
-#pragma unroll
-        for (int f = 0; f < T::FJ; ++f) {
-            const int j = s.j0 + T::wave_j() + f * 16 + int(threadIdx.x % 16);
-            store<T>(acc, f, a.dw, (int64_t(s.e) * a.n + j) * a.k + s.i0, j < a.n ? a.k - s.i0 : 0, 1.0f);
-        }
+        void *out = static_cast<char *>(a.dw) + ((int64_t(s.e) * a.n + s.j0) * a.k + s.i0) * (T::kFull ? 4 : 2);
+        store<T>(acc, out, a.k, a.n - s.j0, a.k - s.i0, [](int) { return 1.0f; });
     }
 };
 
@@ -741,7 +797,7 @@ __global__ __launch_bounds__(T::kThreads, T::kPerSimd) void grad_kernel(ExpertGr
     const Tables tables = T::tables(lds, a.experts);
     fill_tables(tables, a.offset, a.count, a.experts, T::TJ);
     const GradJob<T> job{a, tables, tiles_i, tiles_j};
-    T::run(job, int(blockIdx.x), int(gridDim.x), tiles_i * tiles_j * a.experts, lds);
+    T::run(job, own_tiles(job, tiles_i * tiles_j * a.experts), lds);
 }
 
 int tiles(int n, int per) { return n / per + (n % per != 0); }

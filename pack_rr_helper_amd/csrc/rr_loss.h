@@ -63,7 +63,7 @@ struct Product {
 };
 
 // Rows that start at, and are a multiple of, 16 bytes.
-inline bool in_chunks(const void *p, int64_t ld, int64_t es)
+__host__ __device__ inline bool in_chunks(const void *p, int64_t ld, int64_t es)
 {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0;
 }
