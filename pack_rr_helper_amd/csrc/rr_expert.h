@@ -144,22 +144,32 @@ hipError_t launch_expert_grad(const Op &, hipStream_t);
 // Gradient norm
 // ---------------------------------------------------------------------------
 
-// Tensors of one launch.
+// Tensors of one launch; those without elements are left out.
 constexpr int32_t kClipTensors = 90;
 
-struct ClipTensor {
-    const void *in;
-    void *out;
-    int64_t count;
+struct ClipTable {
+    int32_t tile0[kClipTensors];  // tiles of the tensors before
+    int32_t tensors, tiles, bf16, vectors;  // vectors: of 16 bytes, of a thread in a tile
+    const void *in[kClipTensors];
+    void *out[kClipTensors];
+    int64_t count[kClipTensors];
+
+    // Adds a tensor; false if there is no room.
+    bool add(const void *in, void *out, int64_t count);
+    // The launch's workgroups, one for each tile.
+    int32_t blocks() const { return tiles > 0 ? tiles : 1; }
 };
+// Tiles of 32 KiB to sum, of 8 KiB to scale, of 4 KiB where one workgroup sums them.
+constexpr int32_t kSquareVectors = 8, kClipVectors = 2, kSmallVectors = 1;
 
 struct SquareSumArgs {
     double *part;        // one per workgroup of this launch
-    int32_t tensors, bf16, blocks, reserved;
-    ClipTensor t[kClipTensors];
+    int32_t stream, reserved;  // more than the last level cache holds
+    ClipTable t;
 };
-int32_t square_blocks(const int64_t *count, int32_t tensors, int64_t es);
 hipError_t launch_square_sum(const Op &, hipStream_t);
+// All by one workgroup; part: the sum.
+hipError_t launch_square_small(const Op &, hipStream_t);
 
 struct SumPartsArgs {
     const double *part;
@@ -172,8 +182,8 @@ struct ClipArgs {
     const double *sums[RR_MAX_SHARDS];
     double max_norm;
     float *norm;         // null: another launch's
-    int32_t n_sums, tensors, bf16, blocks;
-    ClipTensor t[kClipTensors];
+    int32_t n_sums, reserved;
+    ClipTable t;
 };
 hipError_t launch_clip(const Op &, hipStream_t);
 

@@ -20,7 +20,7 @@ namespace rr {
 struct Op {
     hipError_t (*launch)(const Op &, hipStream_t);
     size_t bytes;            // of args in use
-    alignas(16) char args[2464];
+    alignas(16) char args[2704];
 
     template <typename A>
     static Op make(hipError_t (*launch)(const Op &, hipStream_t), const A &a)

@@ -230,7 +230,7 @@ class Clip:
     def __init__(self, L):
         self.L = L
 
-    def sum(self, dtype=F32, ins=(ptr(0), ptr(1)), counts=(100, 50), total=ptr(2), ws=ptr(3), n=1 << 20):
+    def sum(self, dtype=F32, ins=(ptr(0), ptr(1)), counts=(100000, 50), total=ptr(2), ws=ptr(3), n=1 << 20):
         i, c, _ = arrays(ins, counts)
         return self.L.rr_grad_square_sum(dtype, len(counts), i, c, total, ws, n, None)
 
@@ -244,6 +244,7 @@ def test_square_sum(L):
     c = Clip(L)
     assert recorded(L, c.sum) == (OK, 2) and recorded(L, lambda: c.sum(ins=(), counts=()))[0] == OK
     assert recorded(L, lambda: c.sum(ins=(ptr(0), None), counts=(5, 0)))[0] == OK
+    assert recorded(L, lambda: c.sum(counts=(100, 50), ws=None, n=0)) == (OK, 1)
     # read twice is no fault; overlaps with what is written are
     assert recorded(L, lambda: c.sum(ins=(ptr(0), ptr(0) + 4)))[0] == OK
     for bad in (dict(dtype=2), dict(counts=(-1, 5)), dict(counts=(1 << 40, 1)), dict(ins=(None, ptr(1))), dict(ins=(ptr(0) + 2, ptr(1))),
