@@ -113,49 +113,57 @@ __device__ __forceinline__ float weight_of(const ExpertProductArgs &a, int p, bo
 }
 
 // ---------------------------------------------------------------------------
-// Few positions a segment: each of eight waves streams its share of k for 32 rows of
-// the weights from memory to registers, and the sums are joined in LDS.
+// Few positions a segment: KS waves stream FI * 16 rows of the weights from memory to
+// registers, past all positions of the tile, a block of k each in turns.  Bound by the
+// weights' bytes, and by how many are under way: x is read again for every 16 rows, so
+// that four such per wave take 32 us where one takes 47 us (96 x 6 choices of 64 experts,
+// 2048 x 1408, 5.8 TB/s); two waves to a workgroup 32 us, four 34 us.
 // ---------------------------------------------------------------------------
 
-constexpr int kNarrowWaves = 8, kNarrowThreads = kNarrowWaves * 64, kNarrowI = 32;
-
-struct Piece {
+// Block b of a row of k; a lane has its chunks g and g + 4.
+struct Block {
     i32x8 v;
-    unsigned p;
+    unsigned p;   // its power in the low byte
 
-    __device__ __forceinline__ void load(const unsigned char *at, const unsigned char *power)
+    __device__ __forceinline__ void load(const unsigned char *row, const unsigned char *powers, int b)
     {
-        u32x4 lo, hi;
-        __builtin_memcpy(&lo, __builtin_assume_aligned(at, 16), 16);
-        __builtin_memcpy(&hi, __builtin_assume_aligned(at + 16, 16), 16);
+        typedef u32x4 Half __attribute__((aligned(16)));
+        const unsigned char *at = row + int64_t(b) * RR_QUANT_BLOCK;
+        const u32x4 lo = *reinterpret_cast<const Half *>(at), hi = *reinterpret_cast<const Half *>(at + 64);
         v = i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
-        p = *power;
+        p = powers[b];
     }
 };
 
-template <int FJ, bool FULL>
-__global__ __launch_bounds__(kNarrowThreads) void narrow_kernel(ExpertProductArgs a, int tiles_i)
+template <int FJ, bool FULL, int KS, int FI>
+__global__ __launch_bounds__(KS * 64) void narrow_kernel(ExpertProductArgs a, int tiles_i)
 {
-    constexpr int FI = kNarrowI / 16, TJ = 16 * FJ;
-    __shared__ __attribute__((aligned(16))) f32x4 sums[kNarrowWaves][FI * FJ][64];
+    constexpr int TJ = 16 * FJ;
+    __shared__ __attribute__((aligned(16))) f32x4 sums[KS][FI * FJ][64];
     Place at;
     if (!place_of(a.count, a.experts, TJ, tiles_i, at))
         return;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
     const int blocks = int(a.w.ld / RR_QUANT_BLOCK), blocks_n = (a.n + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK;
-    const int i0 = at.i * kNarrowI, j0 = at.j * TJ, live = a.count[at.e] - j0, first = a.offset[at.e] + j0;
-    const unsigned char *wv[FI], *wp[FI], *xv[FJ], *xp[FJ];
+    const int i0 = at.i * 16 * FI, k0 = wave < blocks ? wave : blocks - 1;
+    const unsigned char *wv[FI], *wp[FI];
+    Block w[FI], x[FJ];
+    // the weights are what takes long: on their way before the rows of x are known
 #pragma unroll
     for (int f = 0; f < FI; ++f) {
-        const int i = i0 + f * 16 + r < a.n ? i0 + f * 16 + r : a.n - 1;
-        wv[f] = a.w.values + (int64_t(at.e) * a.n + i) * a.w.ld + g * 32;
-        wp[f] = a.w.powers + (int64_t(at.e) * blocks_n + i / RR_QUANT_BLOCK) * a.w.lds;
+        const int i = i0 + f * 16 + r, row_i = i < a.n ? i : a.n - 1;
+        wv[f] = a.w.values + (int64_t(at.e) * a.n + row_i) * a.w.ld + g * 16;
+        wp[f] = a.w.powers + (int64_t(at.e) * blocks_n + row_i / RR_QUANT_BLOCK) * a.w.lds;
+        w[f].load(wv[f], wp[f], k0);
     }
+    const int j0 = at.j * TJ, live = a.count[at.e] - j0, first = a.offset[at.e] + j0;
+    const unsigned char *xv[FJ], *xp[FJ];
 #pragma unroll
     for (int f = 0; f < FJ; ++f) {
         const int j = f * 16 + r, row = row_of(a, first + j, j < live), in = row < 0 ? 0 : row;
-        xv[f] = a.x.values + int64_t(in) * a.x.ld + g * 32;
+        xv[f] = a.x.values + int64_t(in) * a.x.ld + g * 16;
         xp[f] = a.x.powers + int64_t(in) * a.x.lds;
+        x[f].load(xv[f], xp[f], k0);
     }
     f32x4 acc[FI][FJ];
 #pragma unroll
@@ -163,27 +171,21 @@ __global__ __launch_bounds__(kNarrowThreads) void narrow_kernel(ExpertProductArg
 #pragma unroll
         for (int j = 0; j < FJ; ++j)
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    Piece wf[FI], xf[FJ];
-    const auto load = [&](int b) {
+    for (int b = wave; b < blocks; b += KS) {
+        Block w0[FI], x0[FJ];
 #pragma unroll
         for (int f = 0; f < FI; ++f)
-            wf[f].load(wv[f] + int64_t(b) * RR_QUANT_BLOCK, wp[f] + b);
+            w0[f] = w[f];
 #pragma unroll
         for (int f = 0; f < FJ; ++f)
-            xf[f].load(xv[f] + int64_t(b) * RR_QUANT_BLOCK, xp[f] + b);
-    };
-    if (wave < blocks)
-        load(wave);
-    for (int b = wave; b < blocks; b += kNarrowWaves) {
-        Piece w0[FI], x0[FJ];
+            x0[f] = x[f];
+        const int next = b + KS < blocks ? b + KS : b;
 #pragma unroll
         for (int f = 0; f < FI; ++f)
-            w0[f] = wf[f];
+            w[f].load(wv[f], wp[f], next);
 #pragma unroll
         for (int f = 0; f < FJ; ++f)
-            x0[f] = xf[f];
-        if (b + kNarrowWaves < blocks)
-            load(b + kNarrowWaves);
+            x[f].load(xv[f], xp[f], next);
         if constexpr (FULL) {
             Wide wide[FI];
 #pragma unroll
@@ -206,29 +208,33 @@ __global__ __launch_bounds__(kNarrowThreads) void narrow_kernel(ExpertProductArg
         }
     }
 #pragma unroll
-    for (int i = 0; i < FI; ++i)
-#pragma unroll
-        for (int j = 0; j < FJ; ++j)
-            sums[wave][i * FJ + j][lane] = acc[i][j];
+    for (int n = 0; n < FI * FJ; ++n)
+        sums[wave][n][lane] = acc[n / FJ][n % FJ];
     __syncthreads();
-    for (int t = threadIdx.x; t < FI * FJ * 64; t += kNarrowThreads) {
-        const int f = t / 64, l = t % 64, j = f % FJ * 16 + l % 16, i = i0 + f / FJ * 16 + l / 16 * 4;
+    for (int f = wave; f < FI * FJ; f += KS) {
+        f32x4 s = sums[0][f][lane];
+#pragma unroll
+        for (int n = 1; n < KS; ++n)
+            s += sums[n][f][lane];
+        const int j = f % FJ * 16 + r, i = i0 + f / FJ * 16 + g * 4;
         if (j >= live || i >= a.n)
             continue;
-        f32x4 s = sums[0][f][l];
-#pragma unroll
-        for (int w = 1; w < kNarrowWaves; ++w)
-            s += sums[w][f][l];
         s *= weight_of(a, first + j, true);
         const int64_t to = int64_t(first + j) * a.n + i;
+        if constexpr (FULL) {
+            store_chunk<4>(static_cast<char *>(a.out) + to * 4, __builtin_bit_cast(u32x4, s), (a.n - i) * 4);
+        } else {
+            auto *out = static_cast<unsigned short *>(a.out) + to;
+            const u32x2 v{pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
+            if (i + 3 < a.n) {
+                __builtin_memcpy(out, &v, 8);
+            } else {
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-            if (i + n < a.n) {
-                if constexpr (!FULL)
-                    static_cast<unsigned short *>(a.out)[to + n] = (unsigned short)pack_bf16(s[n], 0.0f);
-                else
-                    static_cast<float *>(a.out)[to + n] = s[n];
+                for (int n = 0; n < 3; ++n)
+                    if (i + n < a.n)
+                        out[n] = (unsigned short)(v[n / 2] >> 16 * (n % 2));
             }
+        }
     }
 }
 
@@ -818,15 +824,24 @@ unsigned grid_for(int64_t n)
     return unsigned(n < 256 * T::kPerUnit ? n : 256 * T::kPerUnit);
 }
 
+template <int FJ, int KS, int FI>
+hipError_t narrow(const ExpertProductArgs &a, hipStream_t stream)
+{
+    const dim3 grid(unsigned(most_tiles(a, 16 * FI, 16 * FJ))), threads(KS * 64);
+    if (a.bf16)
+        narrow_kernel<FJ, false, KS, FI><<<grid, threads, 0, stream>>>(a, tiles(a.n, 16 * FI));
+    else
+        narrow_kernel<FJ, true, KS, FI><<<grid, threads, 0, stream>>>(a, tiles(a.n, 16 * FI));
+    return hipGetLastError();
+}
+
 template <int FJ>
 hipError_t narrow(const ExpertProductArgs &a, hipStream_t stream)
 {
-    const dim3 grid(unsigned(most_tiles(a, kNarrowI, 16 * FJ))), threads(kNarrowThreads);
-    if (a.bf16)
-        narrow_kernel<FJ, false><<<grid, threads, 0, stream>>>(a, tiles(a.n, kNarrowI));
-    else
-        narrow_kernel<FJ, true><<<grid, threads, 0, stream>>>(a, tiles(a.n, kNarrowI));
-    return hipGetLastError();
+    // where that would leave compute units idle, smaller tiles and more parts of k (8
+    // experts, 2048 x 1024: 6.8 us against 9 us)
+    const int used = a.experts < a.choices ? a.experts : a.choices;
+    return int64_t(used) * tiles(a.n, 64) >= 512 ? narrow<FJ, 2, 4>(a, stream) : narrow<FJ, 4, 2>(a, stream);
 }
 
 template <typename T>

@@ -16,8 +16,8 @@ constexpr int kThreads = 256;
 // earlier pieces, in earlier waves, before this 64 and in lower lanes.
 // ---------------------------------------------------------------------------
 
-constexpr int kSlotThreads = 1024, kSlotWaves = kSlotThreads / 64;
-constexpr int kOnePiece = 8192;  // choices that one workgroup places alone
+constexpr int kSlotThreads = 1024;
+constexpr int kFew = 1024, kOnePiece = 8192;  // choices that a small workgroup, or a large one, places alone
 constexpr int kPiece = 2048;     // the least of many
 
 __host__ __device__ inline int piece_of(int choices, int blocks)
@@ -44,14 +44,16 @@ __global__ __launch_bounds__(kThreads) void slots_count_kernel(SlotsArgs a)
         a.part[int64_t(blockIdx.x) * a.experts + e] = n[e];
 }
 
-__global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotsArgs a)
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void slots_kernel(SlotsArgs a)
 {
-    __shared__ int cursor[kSlotWaves][RR_MAX_EXPERTS];
+    constexpr int kWaves = THREADS / 64;
+    __shared__ int cursor[kWaves][RR_MAX_EXPERTS];
     __shared__ int all[RR_MAX_EXPERTS], start[RR_MAX_EXPERTS + 1], earlier[RR_MAX_EXPERTS];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int piece = piece_of(a.choices, a.blocks), per = piece / kSlotWaves;  // a multiple of 64
-    for (int i = threadIdx.x; i < kSlotWaves * a.experts; i += kSlotThreads)
-        cursor[i / a.experts][i % a.experts] = 0;
+    const int piece = piece_of(a.choices, a.blocks), per = piece / kWaves;  // a multiple of 64
+    for (int e = lane; e < a.experts; e += 64)
+        cursor[wave][e] = 0;
     __syncthreads();
     const int64_t lo = int64_t(blockIdx.x) * piece + int64_t(wave) * per;
     const int64_t hi = lo + per < a.choices ? lo + per : a.choices;
@@ -61,9 +63,9 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotsArgs a)
             atomicAdd(&cursor[wave][e], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) {
+    for (int e = threadIdx.x; e < a.experts; e += THREADS) {
         int here = 0, total = 0, before = 0;
-        for (int w = 0; w < kSlotWaves; ++w)
+        for (int w = 0; w < kWaves; ++w)
             here += cursor[w][e];
         if (a.blocks > 1) {
 #pragma unroll 8
@@ -96,26 +98,26 @@ __global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotsArgs a)
             start[a.experts] = base;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) {
+    for (int e = threadIdx.x; e < a.experts; e += THREADS) {
         int at = start[e] + earlier[e];
-        for (int w = 0; w < kSlotWaves; ++w) {
+        for (int w = 0; w < kWaves; ++w) {
             const int n = cursor[w][e];
             cursor[w][e] = at;
             at += n;
         }
     }
     if (blockIdx.x == 0)
-        for (int e = threadIdx.x; e <= a.experts; e += kSlotThreads) {
+        for (int e = threadIdx.x; e <= a.experts; e += THREADS) {
             a.offset[e] = start[e];
             if (e < a.experts)
                 a.count[e] = all[e];
         }
     // what no choice takes: the segments' ends, and the positions behind the last
-    for (int e = blockIdx.x; e < a.experts; e += a.blocks)
-        for (int p = start[e] + all[e] + int(threadIdx.x); p < start[e + 1]; p += kSlotThreads)
+    for (int e = int(blockIdx.x) * kWaves + wave; e < a.experts; e += a.blocks * kWaves)
+        for (int p = start[e] + all[e] + lane; p < start[e + 1]; p += 64)
             a.source[p] = -1;
-    for (int64_t p = start[a.experts] + int64_t(blockIdx.x) * kSlotThreads + threadIdx.x; p < a.capacity;
-         p += int64_t(a.blocks) * kSlotThreads)
+    for (int64_t p = start[a.experts] + int64_t(blockIdx.x) * THREADS + threadIdx.x; p < a.capacity;
+         p += int64_t(a.blocks) * THREADS)
         a.source[p] = -1;
     __syncthreads();
     for (int64_t i0 = lo; i0 < hi; i0 += 64) {
@@ -494,7 +496,11 @@ hipError_t launch_slots(const Op &op, hipStream_t stream)
 {
     const SlotsArgs a = op.get<SlotsArgs>();
     (void)hipGetLastError();
-    slots_kernel<<<dim3(unsigned(a.blocks)), dim3(kSlotThreads), 0, stream>>>(a);
+    // few choices have less to wait for with fewer waves
+    if (a.choices <= kFew)
+        slots_kernel<256><<<dim3(1), dim3(256), 0, stream>>>(a);
+    else
+        slots_kernel<kSlotThreads><<<dim3(unsigned(a.blocks)), dim3(kSlotThreads), 0, stream>>>(a);
     return hipGetLastError();
 }
 
