@@ -95,6 +95,15 @@ Eight eight(const void *values, const void *powers, int64_t n)
                  static_cast<unsigned char *>(const_cast<void *>(powers)), quantized_ld(n), quantized_lds(n)};
 }
 
+// A division by d as a multiplication: 2^shift is the least power not below d.
+void divide_by(int32_t d, uint32_t *mul, uint32_t *shift)
+{
+    *shift = 0;
+    while ((1 << *shift) < d)
+        ++*shift;
+    *mul = uint32_t((uint64_t(1) << 32) * ((uint64_t(1) << *shift) - uint64_t(d)) / uint64_t(d) + 1);
+}
+
 // What one buffer resource can address: a little less than 2^31 bytes, as offsets
 // past the end stand for rows that are not there.
 constexpr int64_t kReach = (INT64_C(1) << 31) - (INT64_C(1) << 20);
@@ -412,10 +421,12 @@ rr_status rr_quantize_slots(const rr_experts *e, int dtype, int32_t dim, const v
         return st;
     if (n == 0)
         return set_ok();
+    uint32_t mul, shift;
+    divide_by(e->topk, &mul, &shift);
     Launches l(stream);
     l.add(launch_quantize_slots, QuantizeSlotsArgs{x, weight, source, offset, eight(values, powers, capacity), e->rows,
-                                                   int32_t(capacity), e->experts, dim, e->topk, gather ? 1 : 0,
-                                                   dtype == RR_BF16});
+                                                   int32_t(capacity), e->experts, dim, gather ? 1 : 0, dtype == RR_BF16,
+                                                   mul, shift});
     return l.finish();
 }
 
@@ -474,11 +485,8 @@ rr_status rr_expert_product(const rr_experts *e, int dtype, int32_t n, int32_t k
         return st;
     if (choices == 0)
         return set_ok();
-    // division by topk: 2^shift is the least power not below it
-    uint32_t shift = 0;
-    while ((1 << shift) < e->topk)
-        ++shift;
-    const uint32_t mul = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - uint64_t(e->topk))) / uint64_t(e->topk) + 1);
+    uint32_t mul, shift;
+    divide_by(e->topk, &mul, &shift);
     Launches l(stream);
     l.add(launch_expert_product, ExpertProductArgs{eight(w, w_powers, k), eight(x, x_powers, k), weight, source, offset,
                                                    count, out, rows, n, k, e->experts, e->topk, int32_t(capacity),

@@ -86,7 +86,8 @@ struct QuantizeSlotsArgs {
     const int32_t *source, *offset;
     Eight to;
     int64_t rows;
-    int32_t capacity, experts, dim, topk, gather, bf16;
+    int32_t capacity, experts, dim, gather, bf16;
+    uint32_t topk_mul, topk_shift;  // n / topk = (high word of topk_mul * n + n) >> topk_shift, n < 2^31
 };
 hipError_t launch_quantize_slots(const Op &, hipStream_t);
 
@@ -128,7 +129,7 @@ struct ExpertProductArgs {
     void *out;
     int64_t rows;        // of x
     int32_t n, k, experts, topk, capacity, gather, bf16, choices, weights;
-    uint32_t topk_mul, topk_shift;  // n / topk = (high word of topk_mul * n + n) >> topk_shift, n < 2^31
+    uint32_t topk_mul, topk_shift;  // as above
 };
 hipError_t launch_expert_product(const Op &, hipStream_t);
 

@@ -178,38 +178,35 @@ __device__ __forceinline__ unsigned eight_bits(const float *v, unsigned byte)
 __device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // Eight elements from column `at` of a row of `dim`, zeros past it.  WHOLE: the
-// row starts at, and is, a multiple of 16 bytes.
+// row starts at, and is, a multiple of 16 bytes.  The loads themselves are under no
+// condition, as one is waited for where its condition ends: what is not wanted is
+// read at the row's start.
 template <bool BF16, bool WHOLE>
 __device__ __forceinline__ void load_eight(const void *row, int at, int dim, float *v)
 {
     if constexpr (WHOLE && BF16) {
-        uint4 w{0, 0, 0, 0};
-        if (at < dim)
-            w = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(row) + at);
+        const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(row) + (at < dim ? at : 0));
         const unsigned u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            v[2 * i] = __uint_as_float(at < dim ? u[i] << 16 : 0);
+            v[2 * i + 1] = __uint_as_float(at < dim ? u[i] & 0xffff0000u : 0);
         }
     } else if constexpr (WHOLE) {
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
-            float4 w{0.0f, 0.0f, 0.0f, 0.0f};
-            if (at + i < dim)
-                w = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + at + i);
-            v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
+            const bool in = at + i < dim;
+            const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + (in ? at + i : 0));
+            v[i] = in ? w.x : 0.0f, v[i + 1] = in ? w.y : 0.0f, v[i + 2] = in ? w.z : 0.0f, v[i + 3] = in ? w.w : 0.0f;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[i] = 0.0f;
-            if (at + i < dim) {
-                if constexpr (BF16)
-                    v[i] = __uint_as_float(unsigned(static_cast<const unsigned short *>(row)[at + i]) << 16);
-                else
-                    v[i] = static_cast<const float *>(row)[at + i];
-            }
+            const bool in = at + i < dim;
+            if constexpr (BF16)
+                v[i] = __uint_as_float(in ? unsigned(static_cast<const unsigned short *>(row)[in ? at + i : 0]) << 16 : 0);
+            else
+                v[i] = in ? static_cast<const float *>(row)[in ? at + i : 0] : 0.0f;
         }
     }
 }
@@ -278,11 +275,15 @@ __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(QuantizeWeigh
     for (int i = 0; i < 8; ++i) {
         const int row = n0 + part * 8 + i;
         load_eight<BF16, WHOLE>(row_at<BF16>(a.w, (int64_t(e) * a.n + (row < a.n ? row : 0)) * a.k), k0 + lane * 8,
-                                row < a.n ? a.k : 0, v[i]);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            top = max(top, magnitude(v[i][c]));
+                                a.k, v[i]);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            v[i][c] = n0 + part * 8 + i < a.n ? v[i][c] : 0.0f;
+            top = max(top, magnitude(v[i][c]));
+        }
     top = across<64>(top, [](unsigned x, unsigned y) { return x > y ? x : y; });
     if (threadIdx.x % 64 == 0)
         atomicMax(&largest, top);
@@ -327,21 +328,24 @@ __global__ __launch_bounds__(kThreads) void quantize_slots_kernel(QuantizeSlotsA
     for (int i = threadIdx.x; i < RR_QUANT_BLOCK; i += kThreads)
         largest[i] = 0;
     __syncthreads();
-    float v[8][8];
+    float v[8][8], w[8];
+    bool in[8];
     unsigned top[8] = {};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int p = p0 + part * 8 + i, n = a.source[p];
-        const int64_t row = a.gather ? n / a.topk : p;
-        const bool in = n >= 0 && n / a.topk < a.rows;
-        load_eight<BF16, WHOLE>(row_at<BF16>(a.x, (in ? row : 0) * a.dim), d0 + lane * 8, in ? a.dim : 0, v[i]);
-        const float w = in && a.weight ? a.weight[n] : 1.0f;
+        const int of = n < 0 ? -1 : int((__umulhi(a.topk_mul, unsigned(n)) + unsigned(n)) >> a.topk_shift);
+        in[i] = of >= 0 && of < a.rows;
+        load_eight<BF16, WHOLE>(row_at<BF16>(a.x, int64_t(!in[i] ? 0 : a.gather ? of : p) * a.dim), d0 + lane * 8, a.dim, v[i]);
+        w[i] = a.weight ? a.weight[in[i] ? n : 0] : 1.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            v[i][c] = in ? v[i][c] * w : 0.0f;
+            v[i][c] = in[i] ? v[i][c] * w[i] : 0.0f;
             top[c] = max(top[c], magnitude(v[i][c]));
         }
-    }
 #pragma unroll
     for (int c = 0; c < 8; ++c)
         atomicMax(&largest[lane * 8 + c], top[c]);
@@ -393,6 +397,24 @@ __device__ __forceinline__ void store_eight(void *row, int at, int dim, const fl
     }
 }
 
+// Choices whose rows are on their way at a time.
+constexpr int kWide = 8;
+
+// The positions of a row's choices from k0 on, -1 for none, and eight elements of each.
+template <bool FROM, bool WHOLE>
+__device__ __forceinline__ void load_slots(const void *values, const int32_t *slot, int k0, int topk, int capacity, int dim,
+                                           int at, int *p, float (*v)[8])
+{
+#pragma unroll
+    for (int k = 0; k < kWide; ++k) {
+        p[k] = slot[k0 + k < topk ? k0 + k : 0];
+        p[k] = k0 + k < topk && unsigned(p[k]) < unsigned(capacity) ? p[k] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kWide; ++k)
+        load_eight<FROM, WHOLE>(row_at<FROM>(values, int64_t(p[k] < 0 ? 0 : p[k]) * dim), at, dim, v[k]);
+}
+
 // Eight columns of a row by a thread.
 template <bool FROM, bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs a, int chunks)
@@ -402,16 +424,18 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs 
         const int64_t r = i / chunks;
         const int at = int(i - r * chunks) * 8;
         float sum[8] = {};
-#pragma unroll 4
-        for (int k = 0; k < a.topk; ++k) {
-            const int p = a.slot[r * a.topk + k];
-            const bool in = unsigned(p) < unsigned(a.capacity);
-            const float w = a.weight && in ? a.weight[r * a.topk + k] : 1.0f;
-            float v[8];
-            load_eight<FROM, WHOLE>(row_at<FROM>(a.values, (in ? int64_t(p) : 0) * a.dim), at, in ? a.dim : 0, v);
+        for (int k0 = 0; k0 < a.topk; k0 += kWide) {
+            int p[kWide];
+            float w[kWide], v[kWide][8];
+            load_slots<FROM, WHOLE>(a.values, a.slot + r * a.topk, k0, a.topk, a.capacity, a.dim, at, p, v);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                sum[c] = in ? __builtin_fmaf(w, v[c], sum[c]) : sum[c];
+            for (int k = 0; k < kWide; ++k)
+                w[k] = a.weight ? a.weight[r * a.topk + (k0 + k < a.topk ? k0 + k : 0)] : 1.0f;
+#pragma unroll
+            for (int k = 0; k < kWide; ++k)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    sum[c] = p[k] >= 0 ? __builtin_fmaf(w[k], v[k][c], sum[c]) : sum[c];
         }
         store_eight<BF16, WHOLE>(const_cast<void *>(row_at<BF16>(a.y, r * a.dim)), at, a.dim, sum);
     }
@@ -421,29 +445,20 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs 
 template <bool FROM, bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs a)
 {
-    constexpr int kWide = 8;
     const int lane = threadIdx.x % 64;
     for (int64_t r = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64; r < a.rows; r += int64_t(gridDim.x) * (kThreads / 64))
         for (int k0 = 0; k0 < a.topk; k0 += kWide) {
-            int p[kWide];
             float dot[kWide] = {};
-#pragma unroll
-            for (int k = 0; k < kWide; ++k) {
-                p[k] = k0 + k < a.topk ? a.slot[r * a.topk + k0 + k] : -1;
-                if (unsigned(p[k]) >= unsigned(a.capacity))
-                    p[k] = -1;
-            }
             for (int at = lane * 8; at < a.dim; at += 512) {
-                float dy[8];
+                int p[kWide];
+                float v[kWide][8], dy[8];
+                load_slots<FROM, WHOLE>(a.values, a.slot + r * a.topk, k0, a.topk, a.capacity, a.dim, at, p, v);
                 load_eight<BF16, WHOLE>(row_at<BF16>(a.dy, r * a.dim), at, a.dim, dy);
 #pragma unroll
-                for (int k = 0; k < kWide; ++k) {
-                    float v[8];
-                    load_eight<FROM, WHOLE>(row_at<FROM>(a.values, int64_t(p[k] < 0 ? 0 : p[k]) * a.dim), at, p[k] < 0 ? 0 : a.dim, v);
+                for (int k = 0; k < kWide; ++k)
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
-                        dot[k] = p[k] < 0 ? 0.0f : __builtin_fmaf(dy[c], v[c], dot[k]);
-                }
+                        dot[k] = p[k] < 0 ? 0.0f : __builtin_fmaf(dy[c], v[k][c], dot[k]);
             }
 #pragma unroll
             for (int k = 0; k < kWide; ++k) {
