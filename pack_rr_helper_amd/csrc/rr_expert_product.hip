@@ -14,6 +14,8 @@
 #include "rr_expert.h"
 #include "rr_product.h"
 
+#include <math.h>
+
 namespace rr {
 namespace {
 
@@ -117,7 +119,7 @@ __device__ __forceinline__ float weight_of(const ExpertProductArgs &a, int p, bo
 // registers, past all positions of the tile, a block of k each in turns.  Bound by the
 // weights' bytes, and by how many are under way: x is read again for every 16 rows, so
 // that four such per wave take 32 us where one takes 47 us (96 x 6 choices of 64 experts,
-// 2048 x 1408, 5.8 TB/s); two waves to a workgroup 32 us, four 34 us.
+// 2048 x 1408); two waves to a workgroup 32 us, four 34 us.
 // ---------------------------------------------------------------------------
 
 // Block b of a row of k; a lane has its chunks g and g + 4.
@@ -865,19 +867,25 @@ hipError_t launch_expert_product(const Op &op, hipStream_t stream)
 {
     const ExpertProductArgs a = op.get<ExpertProductArgs>();
     // choices of an expert, were they even
-    const int per = a.choices / (a.experts < a.choices ? a.experts : a.choices);
+    const int used = a.experts < a.choices ? a.experts : a.choices, per = a.choices / used;
     (void)hipGetLastError();
-    if (per <= 16)
-        return narrow<1>(a, stream);
-    if (per <= 32)
-        return narrow<2>(a, stream);
-    if (per <= 64)
-        return narrow<4>(a, stream);
+    // Streaming wins where tiles through LDS would be too few for the 256 compute units:
+    // 8 experts of 2048 x 1024, one choice each: 6.5 us and 15.2 us; 576 choices of 64 experts,
+    // 2048 x 1408: 31 us and 22 us; with more choices each it reads them too often: 64 of each
+    // of 8, 2048 x 2048: 35 us and 17 us, of 2, 2048 x 1024: 9.5 us and 13.9 us.
+    if (per <= 64 && int64_t(used) * tiles(a.n, 128) <= (per <= 16 ? 512 : 96))
+        return per <= 16 ? narrow<1>(a, stream) : per <= 32 ? narrow<2>(a, stream) : narrow<4>(a, stream);
     if (!a.bf16)
         return product<Mid<true, true>>(a, stream);
-    if (per <= 192)
-        return product<Mid<true, false>>(a, stream);
-    return product<Big<true>>(a, stream);
+    // The busiest of 256 compute units has so many tiles; segments end in the middle of
+    // one.  A large tile takes as long as 3.4 small ones, of which two share a unit: one alone
+    // takes as long as 1.6 (65536 x 4096 x 2048 in 32 segments: 611 us with large tiles, 702 us
+    // with small; 16384 x 2048 x 1408 in 16: 67 us and 59 us).
+    const auto busy = [&](int t) {
+        return ceil((double(a.choices) / t + 0.5 * used) * tiles(a.n, t) / 256);
+    };
+    const double large = 3.4 * busy(256), small = busy(128) > 1 ? busy(128) : 1.6;
+    return large < small ? product<Big<true>>(a, stream) : product<Mid<true, false>>(a, stream);
 }
 
 hipError_t launch_expert_grad(const Op &op, hipStream_t stream)
@@ -886,7 +894,10 @@ hipError_t launch_expert_grad(const Op &op, hipStream_t stream)
     (void)hipGetLastError();
     if (!a.bf16)
         return grad<Mid<false, true>>(a, stream);
-    if (int64_t(a.n) * a.k * a.experts < int64_t(256) * 256 * 256)
+    // Large tiles where each compute unit has eight or more: 65536 x 4096 x 2048 for 32 experts
+    // 631 us, with small ones 794 us; for 16 experts of 2048 x 1408, three a unit, 81 us and
+    // 69 us.
+    if (int64_t(tiles(a.n, 256)) * tiles(a.k, 256) * a.experts < 2048)
         return grad<Mid<false, false>>(a, stream);
     return grad<Big<false>>(a, stream);
 }

@@ -596,3 +596,64 @@ def test_weights_past_2_31_bytes():
     rr.rr_expert_weight_grad(e, BF16, s.place, xt, xt, dw)
     torch.cuda.synchronize()
     assert not dw[0].any() and not dw[experts - 2].any() and (dw[experts - 1] == 300).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_many_large_tiles(dt):
+    """Workgroups with several tiles in turn, of the largest kind, segments that end inside one."""
+    check_product(Layer(4000, 2, 2, 136, 4096, skew=0.5, check=False), dt, weighted=True)
+    check_product(Layer(4000, 2, 3, 300, 4000, skew=0.5, check=False), dt, gather=False)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("rows", [500, 40])
+def test_weight_grad_large_tiles(dt, rows):
+    """The same of the weights' gradient, with experts that have no choice among the others."""
+    l = Layer(rows, 1, 17, 3900, 2048, masked=0.0, skew=0.6, check=False)
+    e, s = l.e, l.s
+    xt, dyt = rr.Quantized(3900, s.n), rr.Quantized(2048, s.n)
+    rr.rr_quantize_slots(e, BF16, s.place, l.x, xt, gather=True)
+    rr.rr_quantize_slots(e, BF16, s.place, l.dy, dyt, gather=True)
+    dw = Out(DT[dt], 17, 2048, 3900)
+    rr.rr_expert_weight_grad(e, dt, s.place, dyt, xt, dw.t)
+    torch.cuda.synchronize()
+    for i in range(17):
+        lo, hi = s.place.offset[i].item(), s.place.offset[i + 1].item()
+        a = ref.values(dyt.values, dyt.powers, s.n)[:, lo:hi]
+        b = ref.values(xt.values, xt.powers, s.n)[:, lo:hi]
+        want = a @ b.t()
+        assert ((dw.t[i].double() - want).abs() <= ref.product_bound(a, b, want, DT[dt])).all(), i
+    assert dw.untouched()
+
+
+def test_more_tiles_than_a_table_holds():
+    """Over 256 tiles for each workgroup, of products and of gradients, in whole numbers."""
+    experts, n, k = 1024, 16512, 128
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    e = rr.Experts(experts, 1, experts)
+    choice = torch.randperm(experts, generator=gen, device="cuda").to(torch.int32)[:, None].contiguous()
+    s = Slots(e, choice, check=False)
+    w = torch.randint(-4, 5, (experts, n, k), generator=gen, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    x = torch.randint(-4, 5, (experts, k), generator=gen, device="cuda").to(torch.bfloat16)
+    q, xq = rr.QuantizedWeight(experts, n, k), rr.Quantized(experts, k)
+    rr.rr_quantize_weight(BF16, w, q)
+    rr.rr_quantize_rows(BF16, x, xq)
+    held, y = torch.empty(s.n, n, dtype=torch.bfloat16, device="cuda"), torch.empty(experts, n, dtype=torch.bfloat16, device="cuda")
+    rr.rr_expert_product(e, BF16, s.place, xq, q, held, gather=True)
+    rr.rr_expert_combine(e, BF16, BF16, s.place, held, None, y)
+    torch.cuda.synchronize()
+    for r in list(range(0, experts, 97)) + [experts - 1]:
+        want = (w[choice[r, 0].item()].float() @ x[r].float()).to(torch.bfloat16)
+        assert torch.equal(y[r], want), r
+    del w, q, held, y
+    n, k = 2048, 2300
+    x = torch.randint(-4, 5, (experts, k), generator=gen, device="cuda").to(torch.bfloat16)
+    dy = torch.randint(-4, 5, (experts, n), generator=gen, device="cuda").to(torch.bfloat16)
+    xt, dyt = rr.Quantized(k, s.n), rr.Quantized(n, s.n)
+    rr.rr_quantize_slots(e, BF16, s.place, x, xt, gather=True)
+    rr.rr_quantize_slots(e, BF16, s.place, dy, dyt, gather=True)
+    dw = torch.empty(experts, n, k, dtype=torch.bfloat16, device="cuda")
+    rr.rr_expert_weight_grad(e, BF16, s.place, dyt, xt, dw)
+    torch.cuda.synchronize()
+    for r in list(range(0, experts, 97)) + [experts - 1]:
+        assert torch.equal(dw[choice[r, 0].item()], dy[r][:, None] * x[r][None, :]), r
