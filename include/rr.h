@@ -703,6 +703,10 @@ rr_status rr_quantize_weight(int dtype, int32_t experts, int32_t n, int32_t k, c
  *     exchanged).
  *   weight [rows][topk]: multiplies a position's sums; null: none.
  *   Positions without a choice are left as they were.
+ * Here and in rr_expert_weight_grad, sums over blocks are held in 32 bits.  Results in bf16:
+ * within a block, products are summed to 2^-16 of the largest of them.  In fp32: an
+ * element times its power is rounded where it lies below 2^-126, to multiples of 2^-133, and
+ * must lie below 2^128.
  */
 rr_status rr_expert_product(const rr_experts *e, int dtype, int32_t n, int32_t k, int gather,
                             const void *x, const void *x_powers, const void *w, const void *w_powers,

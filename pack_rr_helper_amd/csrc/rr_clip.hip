@@ -241,19 +241,18 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a)
 
 }  // namespace
 
-bool ClipTable::add(const void *from, void *to, int64_t n)
+int64_t ClipTable::add(const void *from, void *to, int64_t n)
 {
-    if (n == 0)
-        return true;
-    if (tensors == kClipTensors)
-        return false;
+    const int64_t per = int64_t(kThreads) * vectors * (bf16 ? 8 : 4), room = (kClipTiles - tiles) * per;
+    n = n < room ? n : room;
+    if (n == 0 || tensors == kClipTensors)
+        return 0;
     tile0[tensors] = tiles;
     in[tensors] = from;
     out[tensors] = to;
     count[tensors++] = n;
-    const int64_t bytes = int64_t(kThreads) * vectors * 16;
-    tiles += int32_t((n * (bf16 ? 2 : 4) + bytes - 1) / bytes);
-    return true;
+    tiles += int32_t((n + per - 1) / per);
+    return n;
 }
 
 hipError_t launch_square_sum(const Op &op, hipStream_t stream)

@@ -137,21 +137,29 @@ constexpr int64_t kCacheBytes = INT64_C(256) << 20;
 template <typename F>
 void each_launch(int32_t vectors, int dtype, int nTensors, const void *const *in, void *const *out, const int64_t *count, F f)
 {
+    const auto from = [&](auto *const *p, int i, int64_t done) { return p ? p[i] + done * elem_size(dtype) : nullptr; };
+    const char *const *src = reinterpret_cast<const char *const *>(in);
+    char *const *dst = reinterpret_cast<char *const *>(out);
+    bool first = true;
     int i = 0;
+    int64_t done = 0;    // of tensor i, of which one launch may take a part
     do {
         ClipTable t{};
         t.bf16 = dtype == RR_BF16;
         t.vectors = vectors;
-        const bool first = i == 0;
-        while (i < nTensors && t.add(in ? in[i] : nullptr, out ? out[i] : nullptr, count[i]))
-            ++i;
+        for (; i < nTensors; ++i, done = 0) {
+            done += t.add(from(src, i, done), from(dst, i, done), count[i] - done);
+            if (done < count[i])
+                break;
+        }
         f(t, first);
+        first = false;
     } while (i < nTensors);
 }
 
 // Whether one workgroup sums a call's tensors, which saves a launch: up to 64 tiles of
-// 4 KiB, four for each of its waves (40000 fp32 elements in 14 tensors with the clipping
-// @@).
+// 4 KiB, four for each of its waves (40000 fp32 elements in 14 tensors, with the
+// clipping, 12.7 us instead of 14.5 us).
 bool small(int dtype, int nTensors, const int64_t *count)
 {
     int32_t launches = 0, tiles = 0;
@@ -490,7 +498,7 @@ rr_status rr_expert_product(const rr_experts *e, int dtype, int32_t n, int32_t k
     Launches l(stream);
     l.add(launch_expert_product, ExpertProductArgs{eight(w, w_powers, k), eight(x, x_powers, k), weight, source, offset,
                                                    count, out, rows, n, k, e->experts, e->topk, int32_t(capacity),
-                                                   gather ? 1 : 0, dtype == RR_BF16, int32_t(choices), int32_t(choices), mul, shift});
+                                                   gather ? 1 : 0, dtype == RR_BF16, int32_t(choices), mul, shift});
     return l.finish();
 }
 

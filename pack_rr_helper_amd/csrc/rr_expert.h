@@ -128,7 +128,7 @@ struct ExpertProductArgs {
     const int32_t *source, *offset, *count;
     void *out;
     int64_t rows;        // of x
-    int32_t n, k, experts, topk, capacity, gather, bf16, choices, weights;
+    int32_t n, k, experts, topk, capacity, gather, bf16, choices;
     uint32_t topk_mul, topk_shift;  // as above
 };
 hipError_t launch_expert_product(const Op &, hipStream_t);
@@ -145,8 +145,9 @@ hipError_t launch_expert_grad(const Op &, hipStream_t);
 // Gradient norm
 // ---------------------------------------------------------------------------
 
-// Tensors of one launch; those without elements are left out.
-constexpr int32_t kClipTensors = 90;
+// Tensors of one launch; those without elements are left out.  And its tiles: a launch
+// has less than 2^32 threads.
+constexpr int32_t kClipTensors = 90, kClipTiles = 1 << 23;
 
 struct ClipTable {
     int32_t tile0[kClipTensors];  // tiles of the tensors before
@@ -155,8 +156,8 @@ struct ClipTable {
     void *out[kClipTensors];
     int64_t count[kClipTensors];
 
-    // Adds a tensor; false if there is no room.
-    bool add(const void *in, void *out, int64_t count);
+    // Adds a tensor, or as much of its start as there is room for; the elements added.
+    int64_t add(const void *in, void *out, int64_t count);
     // The launch's workgroups, one for each tile.
     int32_t blocks() const { return tiles > 0 ? tiles : 1; }
 };

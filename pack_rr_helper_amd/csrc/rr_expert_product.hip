@@ -10,7 +10,8 @@
 // (measured: 1.6e-5 of a sum of 128 normal products, whatever is added to), less than
 // the 2^-9 of a result in bf16 and more than a result in 32 bits may be off.  Results in
 // 32 bits therefore take the operands as bf16, which holds e4m3 times a power of two
-// exactly, through the bf16 instructions (1e-8, at half the rate): FULL.
+// exactly from 2^-117 on (below 2^-126 it has multiples of 2^-133), through the bf16
+// instructions (1e-8, at half the rate: 1060 us, 1030 TFLOP/s, for the product below): FULL.
 #include "rr_expert.h"
 #include "rr_product.h"
 
@@ -102,8 +103,8 @@ __device__ __forceinline__ int row_of(const ExpertProductArgs &a, int p, bool in
         return -1;
     if (!a.gather)
         return p;
-    const int r = a.source[p] / a.topk;
-    return r >= 0 && r < a.rows ? r : -1;
+    const int n = a.source[p];
+    return unsigned(n) < unsigned(a.choices) ? n / a.topk : -1;
 }
 
 __device__ __forceinline__ float weight_of(const ExpertProductArgs &a, int p, bool in)
@@ -111,7 +112,7 @@ __device__ __forceinline__ float weight_of(const ExpertProductArgs &a, int p, bo
     if (!in || !a.weight)
         return 1.0f;
     const int n = a.source[p];
-    return n >= 0 && n / a.topk < a.rows ? a.weight[n] : 0.0f;
+    return unsigned(n) < unsigned(a.choices) ? a.weight[n] : 0.0f;
 }
 
 // ---------------------------------------------------------------------------
@@ -289,8 +290,11 @@ __device__ __forceinline__ int fill_tables(const Tables &t, const int32_t *offse
 // Steps of 128 elements of k, of one tile and then of the next, are loaded two ahead
 // into two places in LDS (the layout of Tile, rr_product.h; a lane's 32 bytes of a row are
 // its chunks g and g + 4), so that the matrix units do not wait where tiles change:
-// with a workgroup for each tile 8192 x 8 choices of 32 experts, 4096 x 2048, took
-// @@
+// 8192 x 8 choices of 32 experts, 4096 x 2048, took 712 us with a workgroup for each tile
+// and the memory operations at the steps' ends, 594 us as it is (1850 TFLOP/s; one
+// dense product of 8192^3 2600).  What is left is the power that the matrix units draw: a
+// loop of nothing but their instructions reaches 4650 TFLOP/s on constant and 3630 on random
+// data; and a fifth of a tile's time, its results' way out between two tiles.
 // Powers come four steps at a time, a word for each row of the tile.
 // A step is computed in two halves of the rows i.  While the first runs, the
 // second's fragments are read; into the second, one barrier says that this step has
@@ -722,7 +726,7 @@ struct ProductJob {
         if (a.weight && T::wave() * 64 < T::TJ) {
             const int j = int(threadIdx.x), at = j < s.live ? list[j] : -1;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                T::buffer(a.weight, int64_t(a.weights) * 4),
+                T::buffer(a.weight, int64_t(a.choices) * 4),
                 lds_pointer(reinterpret_cast<char *>(tables.weight + n % 4 * T::TJ + T::wave() * 64)), 4, at >= 0 ? at * 4 : kNowhere, 0, 0, 0);
         }
         if (listed() && !last)

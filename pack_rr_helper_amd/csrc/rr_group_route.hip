@@ -8,7 +8,7 @@
 // scores are ordered in 32 bits first, and if no decision of the wave's rows was closer
 // than their roundings, those decisions stand.  Else, one wave in a hundred or fewer
 // with a bias, it starts again in 64 bits (every wave: 65536 x 256, top 8 of 4 of 8 groups,
-// in bf16 in 78 us instead of @@ us).
+// in bf16 in 78 us instead of 45 us).
 // Either way a score's low bits give way to the expert's index, so that one maximum
 // orders both.
 #include "rr_expert.h"

@@ -82,9 +82,9 @@ def pointers(name):
     return [k for k, v in CALLS[name].items() if isinstance(v, int) and v >= BASE]
 
 
-def recorded(L, fn):
+def recorded(L, fn, most=16):
     """The status of a call recorded into a plan, which enqueues nothing."""
-    n = L.rr_plan_bytes(16)
+    n = L.rr_plan_bytes(most)
     plan = (ctypes.c_uint64 * (n // 8 + 1))()
     assert L.rr_plan_begin(plan, n) == OK
     st = fn()
@@ -271,6 +271,21 @@ def test_clip(L):
     for bad in (dict(outs=(ptr(0) + 4, ptr(3))), dict(outs=(ptr(1), ptr(3))), dict(outs=(ptr(2), ptr(2) + 396)), dict(norm=ptr(2)),
                 dict(norm=ptr(0)), dict(sums=(ptr(2),)), dict(norm=ptr(4)), dict(outs=(ptr(1), ptr(0))), dict(outs=(ptr(2), ptr(4) - 196))):
         assert c.clip(**bad) == EALIAS, bad
+
+
+def test_largest_tensors(L):
+    """More tiles than one launch has workgroups: a tensor's parts in several launches."""
+    c, n = Clip(L), 1 << 40
+    far = dict(total=1 << 44, ws=1 << 45, n=1 << 31)
+    assert recorded(L, lambda: c.sum(ins=(BASE,), counts=(n,), **far), 100) == (OK, 16 + 1)
+    far = dict(sums=(1 << 44,), norm=1 << 45)
+    assert recorded(L, lambda: c.clip(ins=(BASE,), outs=(BASE,), counts=(n,), **far), 100) == (OK, 64)
+    # a small one before it, so that it starts inside a launch and ends in a 65th
+    assert recorded(L, lambda: c.clip(ins=(1 << 46, BASE), outs=(1 << 46, BASE), counts=(5, n - 5), **far), 100) == (OK, 65)
+    # 2^23 tiles of 8 KiB fit one launch, one more element does not
+    half = 1 << 35
+    assert recorded(L, lambda: c.clip(dtype=BF16, ins=(BASE,), outs=(BASE,), counts=(half,), **far)) == (OK, 1)
+    assert recorded(L, lambda: c.clip(dtype=BF16, ins=(BASE,), outs=(BASE,), counts=(half + 1,), **far)) == (OK, 2)
 
 
 # --------------------------------------------------------------------------

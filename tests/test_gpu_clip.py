@@ -196,3 +196,20 @@ def test_plan_graph_and_streams():
         clear()
         issue()
         assert same()
+
+
+def test_more_tiles_than_a_launch():
+    """A tensor that takes two launches to scale, its last elements in the second."""
+    n = (1 << 35) + 5
+    if torch.cuda.mem_get_info()[0] < 2 * n + (8 << 30):
+        pytest.skip("not the memory for it")
+    t = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    t[0], t[n - 6], t[n - 5], t[n - 1] = 2, 1, 2, 4
+    total = square_sum(BF16, [t])
+    norm = torch.full((1,), -1.0, device="cuda")
+    rr.rr_grad_clip(BF16, [total], 2.5, [t], [t], norm)
+    torch.cuda.synchronize()
+    assert total.item() == 25.0 and norm.item() == 5.0
+    assert [t[i].item() for i in (0, 1, n - 6, n - 5, n - 4, n - 1)] == [1.0, 0.0, 0.5, 1.0, 0.0, 2.0]
+    del t
+    torch.cuda.empty_cache()

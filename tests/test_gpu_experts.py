@@ -657,3 +657,31 @@ def test_more_tiles_than_a_table_holds():
     torch.cuda.synchronize()
     for r in list(range(0, experts, 97)) + [experts - 1]:
         assert torch.equal(dw[choice[r, 0].item()], dy[r][:, None] * x[r][None, :]), r
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("x_by,w_by", [(-121, 110), (110, -118), (-60, -70), (110, 10)])
+@pytest.mark.parametrize("rows,out", [(40, 96), (900, 600)])
+def test_small_and_large_elements(dt, x_by, w_by, rows, out):
+    """Powers at the range's ends.  fp32 results are of operands in bf16: an element below 2^-126
+    is off by half a multiple of 2^-133."""
+    l = Layer(rows, 2, 3, 500, out)
+    l.x, l.w = l.x * 2.0 ** x_by, l.w * 2.0 ** w_by
+    rr.rr_quantize_rows(BF16, l.x, l.xq)
+    rr.rr_quantize_weight(BF16, l.w, l.wq)
+    held = Out(DT[dt], l.s.n, out)
+    rr.rr_expert_product(l.e, dt, l.s.place, l.xq, l.wq, held.t, gather=True)
+    torch.cuda.synchronize()
+    for i in range(3):
+        at, n = l.s.positions(i)
+        x, w = l.x_of(n), l.w_of(i)
+        want = x @ w.t()
+        half = 2.0 ** -134
+        more = half * (x.abs().sum(dim=1)[:, None] + w.abs().sum(dim=1)[None, :]) + 500 * half ** 2 if dt == F32 else 0.0
+        # results, and their sums, below 2^-126 may be zero
+        bound = ref.product_bound(x, w, want, DT[dt]) + more + 500 * 2.0 ** -126 * (x_by + w_by < -100)
+        # a sum in 32 bits, whatever its order, holds what is below 2^128 by magnitude
+        out_of_range = ~(x.abs() @ w.abs().t() < 2.0 ** 127)
+        assert (((held.t[at].double() - want).abs() <= bound) | out_of_range).all(), i
+        assert x_by > 0 and w_by > 0 or not out_of_range.any()
+    assert held.untouched()
