@@ -177,58 +177,80 @@ __device__ __forceinline__ unsigned eight_bits(const float *v, unsigned byte)
 
 __device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Eight elements from column `at` of a row of `dim`, zeros past it.  WHOLE: the
-// row starts at, and is, a multiple of 16 bytes.  The loads themselves are under no
-// condition, as one is waited for where its condition ends: what is not wanted is
-// read at the row's start.
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 Unaligned __attribute__((aligned(2)));
+
+// What is read where a matrix has not as many bytes.
+__device__ const u32x4 kNothing = {0, 0, 0, 0};
+
+// A matrix of rows of `dim` elements, read by eight side by side: fetch() loads, under no
+// condition, as a load under one is waited for where that ends; take() gives the elements,
+// zeros past the row.  WHOLE: rows start at, and are, multiples of 16 bytes.  Others are
+// loaded at any element, from the matrix' last 16 bytes at most; what those do not hold,
+// then loaded one by one, is its last row's end (3300 x 2211 fp32 elements summed to rows:
+// 14 us; by elements 61 us).
 template <bool BF16, bool WHOLE>
-__device__ __forceinline__ void load_eight(const void *row, int at, int dim, float *v)
-{
-    if constexpr (WHOLE && BF16) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(row) + (at < dim ? at : 0));
-        const unsigned u[4] = {w.x, w.y, w.z, w.w};
+struct Matrix {
+    static constexpr int N = BF16 ? 8 : 4, kLoads = 8 / N;
+    using Element = std::conditional_t<BF16, unsigned short, unsigned>;
+    const Element *x;
+    int64_t total;       // elements
+    int dim;
+
+    __device__ Matrix(const void *p, int64_t rows, int dim) : x(static_cast<const Element *>(p)), total(rows * dim), dim(dim) {}
+
+    // The element that load n of eight from column `at` of row r starts at; the row's first
+    // for one past the row.
+    __device__ int64_t first(int64_t r, int at, int n) const { return r * dim + (at + n * N < dim ? at + n * N : 0); }
+    __device__ void fetch(int64_t r, int at, u32x4 *w) const
+    {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(at < dim ? u[i] << 16 : 0);
-            v[2 * i + 1] = __uint_as_float(at < dim ? u[i] & 0xffff0000u : 0);
-        }
-    } else if constexpr (WHOLE) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-            const bool in = at + i < dim;
-            const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + (in ? at + i : 0));
-            v[i] = in ? w.x : 0.0f, v[i + 1] = in ? w.y : 0.0f, v[i + 2] = in ? w.z : 0.0f, v[i + 3] = in ? w.w : 0.0f;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool in = at + i < dim;
-            if constexpr (BF16)
-                v[i] = __uint_as_float(in ? unsigned(static_cast<const unsigned short *>(row)[in ? at + i : 0]) << 16 : 0);
+        for (int n = 0; n < kLoads; ++n) {
+            const int64_t e = first(r, at, n);
+            if constexpr (WHOLE)
+                w[n] = *reinterpret_cast<const u32x4 *>(x + e);
             else
-                v[i] = in ? static_cast<const float *>(row)[in ? at + i : 0] : 0.0f;
+                w[n] = *reinterpret_cast<const Unaligned *>(total < N ? reinterpret_cast<const Element *>(&kNothing)
+                                                                 : x + (e < total - N ? e : total - N));
         }
     }
-}
-
-// The row at element `at` of a matrix.
-template <bool BF16>
-__device__ __forceinline__ const void *row_at(const void *x, int64_t at)
-{
-    return static_cast<const char *>(x) + at * (BF16 ? 2 : 4);
-}
+    __device__ void take(int64_t r, int at, const u32x4 *w, float *v) const
+    {
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) {
+            // a whole row ends where a load does
+            const int left = WHOLE ? (at + n * N < dim ? N : 0) : dim - at - n * N;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const unsigned u = BF16 ? (i % 2 ? w[n][i / 2] & 0xffff0000u : w[n][i / 2] << 16) : w[n][i % 4];
+                v[n * N + i] = __uint_as_float(i < left ? u : 0);
+            }
+            if constexpr (!WHOLE) {
+                const int64_t e = first(r, at, n);
+                if (left > 0 && e > total - N)
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        v[n * N + i] = __uint_as_float(i < left ? unsigned(x[e + i]) << (BF16 ? 16 : 0) : 0);
+            }
+        }
+    }
+};
 
 // A block of a row by sixteen lanes.
 template <bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeRowsArgs a, int blocks)
 {
+    using M = Matrix<BF16, WHOLE>;
+    const M x(a.x, a.rows, a.dim);
     const int lane = threadIdx.x % 16;
     const int64_t n = a.rows * blocks;
     for (int64_t i = int64_t(blockIdx.x) * (kThreads / 16) + threadIdx.x / 16; i < n; i += int64_t(gridDim.x) * (kThreads / 16)) {
         const int64_t r = i / blocks;
         const int b = int(i - r * blocks), at = b * RR_QUANT_BLOCK + lane * 8;
         float v[8];
-        load_eight<BF16, WHOLE>(row_at<BF16>(a.x, r * a.dim), at, a.dim, v);
+        u32x4 w[M::kLoads];
+        x.fetch(r, at, w);
+        x.take(r, at, w, v);
         unsigned top = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -269,21 +291,24 @@ __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(QuantizeWeigh
     if (threadIdx.x == 0)
         largest = 0;
     __syncthreads();
+    using M = Matrix<BF16, WHOLE>;
+    const M matrix(a.w, int64_t(a.experts) * a.n, a.k);
+    const auto row_of = [&](int i) { return int64_t(e) * a.n + (n0 + part * 8 + i < a.n ? n0 + part * 8 + i : 0); };
     float v[8][8];
+    u32x4 w[8][M::kLoads];
     unsigned top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = n0 + part * 8 + i;
-        load_eight<BF16, WHOLE>(row_at<BF16>(a.w, (int64_t(e) * a.n + (row < a.n ? row : 0)) * a.k), k0 + lane * 8,
-                                a.k, v[i]);
-    }
-#pragma unroll
     for (int i = 0; i < 8; ++i)
+        matrix.fetch(row_of(i), k0 + lane * 8, w[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        matrix.take(row_of(i), k0 + lane * 8, w[i], v[i]);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             v[i][c] = n0 + part * 8 + i < a.n ? v[i][c] : 0.0f;
             top = max(top, magnitude(v[i][c]));
         }
+    }
     top = across<64>(top, [](unsigned x, unsigned y) { return x > y ? x : y; });
     if (threadIdx.x % 64 == 0)
         atomicMax(&largest, top);
@@ -328,7 +353,11 @@ __global__ __launch_bounds__(kThreads) void quantize_slots_kernel(QuantizeSlotsA
     for (int i = threadIdx.x; i < RR_QUANT_BLOCK; i += kThreads)
         largest[i] = 0;
     __syncthreads();
-    float v[8][8], w[8];
+    using M = Matrix<BF16, WHOLE>;
+    const M x(a.x, a.gather ? a.rows : a.capacity, a.dim);
+    float v[8][8], by[8];
+    u32x4 w[8][M::kLoads];
+    int row[8];
     bool in[8];
     unsigned top[8] = {};
 #pragma unroll
@@ -336,16 +365,19 @@ __global__ __launch_bounds__(kThreads) void quantize_slots_kernel(QuantizeSlotsA
         const int p = p0 + part * 8 + i, n = a.source[p];
         const int of = n < 0 ? -1 : int((__umulhi(a.topk_mul, unsigned(n)) + unsigned(n)) >> a.topk_shift);
         in[i] = of >= 0 && of < a.rows;
-        load_eight<BF16, WHOLE>(row_at<BF16>(a.x, int64_t(!in[i] ? 0 : a.gather ? of : p) * a.dim), d0 + lane * 8, a.dim, v[i]);
-        w[i] = a.weight ? a.weight[in[i] ? n : 0] : 1.0f;
+        row[i] = !in[i] ? 0 : a.gather ? of : p;
+        x.fetch(row[i], d0 + lane * 8, w[i]);
+        by[i] = a.weight ? a.weight[in[i] ? n : 0] : 1.0f;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
+        x.take(row[i], d0 + lane * 8, w[i], v[i]);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            v[i][c] = in[i] ? v[i][c] * w[i] : 0.0f;
+            v[i][c] = in[i] ? v[i][c] * by[i] : 0.0f;
             top[c] = max(top[c], magnitude(v[i][c]));
         }
+    }
 #pragma unroll
     for (int c = 0; c < 8; ++c)
         atomicMax(&largest[lane * 8 + c], top[c]);
@@ -369,30 +401,38 @@ __global__ __launch_bounds__(kThreads) void quantize_slots_kernel(QuantizeSlotsA
 // Rows of sums
 // ---------------------------------------------------------------------------
 
+// Eight elements to column `at` of a row of `dim`, at element `first` of a matrix.
 template <bool BF16, bool WHOLE>
-__device__ __forceinline__ void store_eight(void *row, int at, int dim, const float *v)
+__device__ __forceinline__ void store_eight(void *y, int64_t first, int at, int dim, const float *v)
 {
+    using Free = std::conditional_t<WHOLE, u32x4, Unaligned>;
     typedef float f32x2 __attribute__((ext_vector_type(2)));
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     unsigned u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         u[i] = __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{v[2 * i], v[2 * i + 1]}, bf16x2));
-    if constexpr (WHOLE && BF16) {
-        *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(row) + at) = uint4{u[0], u[1], u[2], u[3]};
-    } else if constexpr (WHOLE) {
+    if constexpr (BF16) {
+        auto *row = static_cast<unsigned short *>(y) + first + at;
+        if (WHOLE || at + 8 <= dim) {
+            *reinterpret_cast<Free *>(row) = u32x4{u[0], u[1], u[2], u[3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (at + i < dim)
+                    row[i] = (unsigned short)(u[i / 2] >> 16 * (i % 2));
+        }
+    } else {
+        auto *row = static_cast<float *>(y) + first + at;
 #pragma unroll
         for (int i = 0; i < 8; i += 4)
-            if (at + i < dim)
-                *reinterpret_cast<float4 *>(static_cast<float *>(row) + at + i) = float4{v[i], v[i + 1], v[i + 2], v[i + 3]};
-    } else {
+            if (at + i + (WHOLE ? 0 : 3) < dim) {
+                *reinterpret_cast<Free *>(row + i) = __builtin_bit_cast(u32x4, float4{v[i], v[i + 1], v[i + 2], v[i + 3]});
+            } else if (!WHOLE) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (at + i < dim) {
-                if constexpr (BF16)
-                    static_cast<unsigned short *>(row)[at + i] = (unsigned short)(u[i / 2] >> 16 * (i % 2));
-                else
-                    static_cast<float *>(row)[at + i] = v[i];
+                for (int c = 0; c < 3; ++c)
+                    if (at + i + c < dim)
+                        row[i + c] = v[i + c];
             }
     }
 }
@@ -400,10 +440,11 @@ __device__ __forceinline__ void store_eight(void *row, int at, int dim, const fl
 // Choices whose rows are on their way at a time.
 constexpr int kWide = 8;
 
-// The positions of a row's choices from k0 on, -1 for none, and eight elements of each.
-template <bool FROM, bool WHOLE>
-__device__ __forceinline__ void load_slots(const void *values, const int32_t *slot, int k0, int topk, int capacity, int dim,
-                                           int at, int *p, float (*v)[8])
+// The positions of a row's choices from k0 on, -1 for none, and eight elements of each
+// on their way.
+template <typename M>
+__device__ __forceinline__ void fetch_slots(const M &values, const int32_t *slot, int k0, int topk, int capacity, int at,
+                                            int *p, u32x4 (*w)[M::kLoads])
 {
 #pragma unroll
     for (int k = 0; k < kWide; ++k) {
@@ -412,13 +453,15 @@ __device__ __forceinline__ void load_slots(const void *values, const int32_t *sl
     }
 #pragma unroll
     for (int k = 0; k < kWide; ++k)
-        load_eight<FROM, WHOLE>(row_at<FROM>(values, int64_t(p[k] < 0 ? 0 : p[k]) * dim), at, dim, v[k]);
+        values.fetch(p[k] < 0 ? 0 : p[k], at, w[k]);
 }
 
 // Eight columns of a row by a thread.
 template <bool FROM, bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs a, int chunks)
 {
+    using M = Matrix<FROM, WHOLE>;
+    const M values(a.values, a.capacity, a.dim);
     const int64_t n = a.rows * chunks;
     for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kThreads) {
         const int64_t r = i / chunks;
@@ -426,18 +469,21 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs 
         float sum[8] = {};
         for (int k0 = 0; k0 < a.topk; k0 += kWide) {
             int p[kWide];
-            float w[kWide], v[kWide][8];
-            load_slots<FROM, WHOLE>(a.values, a.slot + r * a.topk, k0, a.topk, a.capacity, a.dim, at, p, v);
+            float by[kWide], v[8];
+            u32x4 w[kWide][M::kLoads];
+            fetch_slots(values, a.slot + r * a.topk, k0, a.topk, a.capacity, at, p, w);
 #pragma unroll
             for (int k = 0; k < kWide; ++k)
-                w[k] = a.weight ? a.weight[r * a.topk + (k0 + k < a.topk ? k0 + k : 0)] : 1.0f;
+                by[k] = a.weight ? a.weight[r * a.topk + (k0 + k < a.topk ? k0 + k : 0)] : 1.0f;
 #pragma unroll
-            for (int k = 0; k < kWide; ++k)
+            for (int k = 0; k < kWide; ++k) {
+                values.take(p[k] < 0 ? 0 : p[k], at, w[k], v);
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    sum[c] = p[k] >= 0 ? __builtin_fmaf(w[k], v[k][c], sum[c]) : sum[c];
+                    sum[c] = p[k] >= 0 ? __builtin_fmaf(by[k], v[c], sum[c]) : sum[c];
+            }
         }
-        store_eight<BF16, WHOLE>(const_cast<void *>(row_at<BF16>(a.y, r * a.dim)), at, a.dim, sum);
+        store_eight<BF16, WHOLE>(a.y, r * a.dim, at, a.dim, sum);
     }
 }
 
@@ -445,20 +491,28 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs 
 template <bool FROM, bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs a)
 {
+    using M = Matrix<FROM, WHOLE>;
+    using D = Matrix<BF16, WHOLE>;
+    const M values(a.values, a.capacity, a.dim);
+    const D grad(a.dy, a.rows, a.dim);
     const int lane = threadIdx.x % 64;
     for (int64_t r = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64; r < a.rows; r += int64_t(gridDim.x) * (kThreads / 64))
         for (int k0 = 0; k0 < a.topk; k0 += kWide) {
             float dot[kWide] = {};
             for (int at = lane * 8; at < a.dim; at += 512) {
                 int p[kWide];
-                float v[kWide][8], dy[8];
-                load_slots<FROM, WHOLE>(a.values, a.slot + r * a.topk, k0, a.topk, a.capacity, a.dim, at, p, v);
-                load_eight<BF16, WHOLE>(row_at<BF16>(a.dy, r * a.dim), at, a.dim, dy);
+                float v[8], dy[8];
+                u32x4 w[kWide][M::kLoads], of_dy[D::kLoads];
+                grad.fetch(r, at, of_dy);
+                fetch_slots(values, a.slot + r * a.topk, k0, a.topk, a.capacity, at, p, w);
+                grad.take(r, at, of_dy, dy);
 #pragma unroll
-                for (int k = 0; k < kWide; ++k)
+                for (int k = 0; k < kWide; ++k) {
+                    values.take(p[k] < 0 ? 0 : p[k], at, w[k], v);
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
-                        dot[k] = p[k] < 0 ? 0.0f : __builtin_fmaf(dy[c], v[k][c], dot[k]);
+                        dot[k] = p[k] < 0 ? 0.0f : __builtin_fmaf(dy[c], v[c], dot[k]);
+                }
             }
 #pragma unroll
             for (int k = 0; k < kWide; ++k) {
