@@ -127,12 +127,6 @@ rr_status check_tensors(int dtype, int nTensors, const int64_t *count, int64_t *
     return RR_OK;
 }
 
-// What the last level cache holds.  Tensors that fit are read from it when they are
-// scaled; larger ones are summed past the caches, and so is what is scaled (600 million
-// bf16 elements in 300 tensors: 596 us, with all loads kept 635 us; 50 million fp32
-// elements 97 us, summed past the caches 102 us).
-constexpr int64_t kCacheBytes = INT64_C(256) << 20;
-
 // f(table, whether it is the first) for the launches that the tensors take, at least one.
 template <typename F>
 void each_launch(int32_t vectors, int dtype, int nTensors, const void *const *in, void *const *out, const int64_t *count, F f)
@@ -626,6 +620,10 @@ try {
         return st;
     double *part = parts > 1 ? static_cast<double *>(workspace) : sum;
     Launches l(stream);
+    // tensors that the cache holds are read from it when they are scaled; larger ones are
+    // summed past the caches, and so is what is scaled (600 million bf16 elements in 300
+    // tensors: 596 us, with all loads kept 635 us; 50 million fp32 elements 97 us, summed past
+    // the caches 102 us)
     const int32_t stream_it = total * es > kCacheBytes;
     if (small(dtype, nTensors, count)) {
         each_launch(kSmallVectors, dtype, nTensors, in, nullptr, count,

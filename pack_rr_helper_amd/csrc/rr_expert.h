@@ -7,6 +7,9 @@
 
 namespace rr {
 
+// Bytes of the last level cache.
+constexpr int64_t kCacheBytes = INT64_C(256) << 20;
+
 // ---------------------------------------------------------------------------
 // Routing in groups
 // ---------------------------------------------------------------------------

@@ -178,43 +178,55 @@ __device__ __forceinline__ unsigned eight_bits(const float *v, unsigned byte)
 __device__ __forceinline__ unsigned magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 Unaligned __attribute__((aligned(2)));
 
 // What is read where a matrix has not as many bytes.
 __device__ const u32x4 kNothing = {0, 0, 0, 0};
 
-// A matrix of rows of `dim` elements, read by eight side by side: fetch() loads, under no
+// 4, 8 or 16 bytes at any element.
+template <int BYTES>
+struct Words {
+    typedef unsigned T __attribute__((ext_vector_type(BYTES / 4)));
+    typedef T Unaligned __attribute__((aligned(2)));
+};
+
+// A matrix of rows of `dim` elements, read by COLS side by side: fetch() loads, under no
 // condition, as a load under one is waited for where that ends; take() gives the elements,
 // zeros past the row.  WHOLE: rows start at, and are, multiples of 16 bytes.  Others are
-// loaded at any element, from the matrix' last 16 bytes at most; what those do not hold,
+// loaded at any element, from the matrix' last bytes at most; what those do not hold,
 // then loaded one by one, is its last row's end (3300 x 2211 fp32 elements summed to rows:
 // 14 us; by elements 61 us).
-template <bool BF16, bool WHOLE>
+template <bool BF16, bool WHOLE, int COLS = 8>
 struct Matrix {
-    static constexpr int N = BF16 ? 8 : 4, kLoads = 8 / N;
+    static constexpr int kSize = BF16 ? 2 : 4, N = COLS * kSize > 16 ? 16 / kSize : COLS, kLoads = COLS / N;
     using Element = std::conditional_t<BF16, unsigned short, unsigned>;
+    using W = Words<N * kSize>;
+    struct Raw {
+        typename W::T w[kLoads];
+    };
     const Element *x;
     int64_t total;       // elements
     int dim;
 
     __device__ Matrix(const void *p, int64_t rows, int dim) : x(static_cast<const Element *>(p)), total(rows * dim), dim(dim) {}
 
-    // The element that load n of eight from column `at` of row r starts at; the row's first
-    // for one past the row.
+    // The element that load n from column `at` of row r starts at; the row's first for one past
+    // the row.
     __device__ int64_t first(int64_t r, int at, int n) const { return r * dim + (at + n * N < dim ? at + n * N : 0); }
-    __device__ void fetch(int64_t r, int at, u32x4 *w) const
+    // STREAM: not to be kept in the caches
+    template <bool STREAM = false>
+    __device__ void fetch(int64_t r, int at, Raw &raw) const
     {
+        using P = std::conditional_t<WHOLE, typename W::T, typename W::Unaligned>;
 #pragma unroll
         for (int n = 0; n < kLoads; ++n) {
             const int64_t e = first(r, at, n);
-            if constexpr (WHOLE)
-                w[n] = *reinterpret_cast<const u32x4 *>(x + e);
-            else
-                w[n] = *reinterpret_cast<const Unaligned *>(total < N ? reinterpret_cast<const Element *>(&kNothing)
-                                                                 : x + (e < total - N ? e : total - N));
+            const auto *p = reinterpret_cast<const P *>(WHOLE ? x + e
+                                                        : total < N ? reinterpret_cast<const Element *>(&kNothing)
+                                                                    : x + (e < total - N ? e : total - N));
+            raw.w[n] = STREAM ? __builtin_nontemporal_load(p) : *p;
         }
     }
-    __device__ void take(int64_t r, int at, const u32x4 *w, float *v) const
+    __device__ void take(int64_t r, int at, const Raw &raw, float *v) const
     {
 #pragma unroll
         for (int n = 0; n < kLoads; ++n) {
@@ -222,7 +234,7 @@ struct Matrix {
             const int left = WHOLE ? (at + n * N < dim ? N : 0) : dim - at - n * N;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const unsigned u = BF16 ? (i % 2 ? w[n][i / 2] & 0xffff0000u : w[n][i / 2] << 16) : w[n][i % 4];
+                const unsigned w = raw.w[n][i * kSize / 4], u = !BF16 ? w : i % 2 ? w & 0xffff0000u : w << 16;
                 v[n * N + i] = __uint_as_float(i < left ? u : 0);
             }
             if constexpr (!WHOLE) {
@@ -248,9 +260,9 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantizeRowsArg
         const int64_t r = i / blocks;
         const int b = int(i - r * blocks), at = b * RR_QUANT_BLOCK + lane * 8;
         float v[8];
-        u32x4 w[M::kLoads];
-        x.fetch(r, at, w);
-        x.take(r, at, w, v);
+        typename M::Raw raw;
+        x.fetch(r, at, raw);
+        x.take(r, at, raw, v);
         unsigned top = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -272,15 +284,27 @@ struct Turned {
     __device__ uint2 *at(int column, int part) { return reinterpret_cast<uint2 *>(t + column * RR_QUANT_BLOCK + ((part ^ (column / 8)) & 15) * 8); }
 };
 
-// The transposed tile from LDS to rows [0, rows) of out.
+// The transposed tile from LDS to rows [0, rows) of out.  STREAM: past the caches.
+template <bool STREAM>
 __device__ __forceinline__ void store_turned(Turned &t, unsigned char *out, int64_t ld, int rows)
 {
+    using W = Words<8>::T;
     for (int i = threadIdx.x; i < RR_QUANT_BLOCK * 16; i += kThreads)
-        if (i / 16 < rows)
-            *reinterpret_cast<uint2 *>(out + i / 16 * ld + i % 16 * 8) = *t.at(i / 16, i % 16);
+        if (i / 16 < rows) {
+            const W v = __builtin_bit_cast(W, *t.at(i / 16, i % 16));
+            W *to = reinterpret_cast<W *>(out + i / 16 * ld + i % 16 * 8);
+            if constexpr (STREAM)
+                __builtin_nontemporal_store(v, to);
+            else
+                *to = v;
+        }
 }
 
-template <bool BF16, bool WHOLE>
+// STREAM: more than the last level cache holds.  What is transposed then leaves past the
+// caches, and w comes past them (32 experts of 4096 x 2048 in bf16: 146 us, 7.4 TB/s; none
+// of it past them 207 us, the loads alone 208 us, the other stores too 193 us).  What
+// the cache holds is read from it by the next product.
+template <bool BF16, bool WHOLE, bool STREAM>
 __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(QuantizeWeightArgs a, int blocks_n, int blocks_k)
 {
     __shared__ __attribute__((aligned(16))) Turned turned;
@@ -295,11 +319,11 @@ __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(QuantizeWeigh
     const M matrix(a.w, int64_t(a.experts) * a.n, a.k);
     const auto row_of = [&](int i) { return int64_t(e) * a.n + (n0 + part * 8 + i < a.n ? n0 + part * 8 + i : 0); };
     float v[8][8];
-    u32x4 w[8][M::kLoads];
+    typename M::Raw w[8];
     unsigned top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        matrix.fetch(row_of(i), k0 + lane * 8, w[i]);
+        matrix.template fetch<STREAM>(row_of(i), k0 + lane * 8, w[i]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         matrix.take(row_of(i), k0 + lane * 8, w[i], v[i]);
@@ -337,10 +361,12 @@ __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(QuantizeWeigh
         *turned.at(lane * 8 + c, part) = uint2{eight_bits(col, byte), eight_bits(col + 4, byte)};
     }
     __syncthreads();
-    store_turned(turned, a.turned.values + (int64_t(e) * a.k + k0) * a.turned.ld + n0, a.turned.ld, a.k - k0);
+    store_turned<STREAM>(turned, a.turned.values + (int64_t(e) * a.k + k0) * a.turned.ld + n0, a.turned.ld, a.k - k0);
 }
 
-template <bool BF16, bool WHOLE>
+// STREAM: as above, of what is written (65536 positions x 4096: 117 us, else 126 us; a layer of
+// 16384 choices of 16 experts, 2048 x 1408, is trained in 437 us with it, in 423 us without).
+template <bool BF16, bool WHOLE, bool STREAM>
 __global__ __launch_bounds__(kThreads) void quantize_slots_kernel(QuantizeSlotsArgs a, int blocks_d)
 {
     __shared__ __attribute__((aligned(16))) Turned turned;
@@ -356,7 +382,7 @@ __global__ __launch_bounds__(kThreads) void quantize_slots_kernel(QuantizeSlotsA
     using M = Matrix<BF16, WHOLE>;
     const M x(a.x, a.gather ? a.rows : a.capacity, a.dim);
     float v[8][8], by[8];
-    u32x4 w[8][M::kLoads];
+    typename M::Raw w[8];
     int row[8];
     bool in[8];
     unsigned top[8] = {};
@@ -394,57 +420,51 @@ __global__ __launch_bounds__(kThreads) void quantize_slots_kernel(QuantizeSlotsA
     for (int i = threadIdx.x; i < RR_QUANT_BLOCK && d0 + i < a.dim; i += kThreads)
         a.to.powers[int64_t(d0 + i) * a.to.lds + bp] = (unsigned char)power_byte(largest[i]);
     __syncthreads();
-    store_turned(turned, a.to.values + int64_t(d0) * a.to.ld + p0, a.to.ld, a.dim - d0);
+    store_turned<STREAM>(turned, a.to.values + int64_t(d0) * a.to.ld + p0, a.to.ld, a.dim - d0);
 }
 
 // ---------------------------------------------------------------------------
 // Rows of sums
 // ---------------------------------------------------------------------------
 
-// Eight elements to column `at` of a row of `dim`, at element `first` of a matrix.
-template <bool BF16, bool WHOLE>
-__device__ __forceinline__ void store_eight(void *y, int64_t first, int at, int dim, const float *v)
+// COLS elements to column `at` of a row of `dim` that starts at element `first` of y, past
+// the caches.
+template <bool BF16, bool WHOLE, int COLS>
+__device__ __forceinline__ void store_row(void *y, int64_t first, int at, int dim, const float *v)
 {
-    using Free = std::conditional_t<WHOLE, u32x4, Unaligned>;
+    using M = Matrix<BF16, WHOLE, COLS>;
+    using P = std::conditional_t<WHOLE, typename M::W::T, typename M::W::Unaligned>;
     typedef float f32x2 __attribute__((ext_vector_type(2)));
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    unsigned u[4];
+    auto *row = static_cast<typename M::Element *>(y) + first + at;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        u[i] = __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{v[2 * i], v[2 * i + 1]}, bf16x2));
-    if constexpr (BF16) {
-        auto *row = static_cast<unsigned short *>(y) + first + at;
-        if (WHOLE || at + 8 <= dim) {
-            *reinterpret_cast<Free *>(row) = u32x4{u[0], u[1], u[2], u[3]};
-        } else {
+    for (int n = 0; n < M::kLoads; ++n) {
+        const float *of = v + n * M::N;
+        typename M::W::T w;
 #pragma unroll
-            for (int i = 0; i < 7; ++i)
-                if (at + i < dim)
-                    row[i] = (unsigned short)(u[i / 2] >> 16 * (i % 2));
+        for (int i = 0; i < M::N * M::kSize / 4; ++i)
+            w[i] = BF16 ? __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{of[2 * i % M::N], of[(2 * i + 1) % M::N]}, bf16x2))
+                        : __float_as_uint(of[i]);
+        const int left = dim - at - n * M::N;
+        if (left >= M::N) {
+            __builtin_nontemporal_store(w, reinterpret_cast<P *>(row + n * M::N));
+        } else if (!WHOLE) {
+#pragma unroll
+            for (int i = 0; i < M::N - 1; ++i)
+                if (i < left)
+                    row[n * M::N + i] = typename M::Element(w[i * M::kSize / 4] >> (BF16 ? i % 2 * 16 : 0));
         }
-    } else {
-        auto *row = static_cast<float *>(y) + first + at;
-#pragma unroll
-        for (int i = 0; i < 8; i += 4)
-            if (at + i + (WHOLE ? 0 : 3) < dim) {
-                *reinterpret_cast<Free *>(row + i) = __builtin_bit_cast(u32x4, float4{v[i], v[i + 1], v[i + 2], v[i + 3]});
-            } else if (!WHOLE) {
-#pragma unroll
-                for (int c = 0; c < 3; ++c)
-                    if (at + i + c < dim)
-                        row[i + c] = v[i + c];
-            }
     }
 }
 
 // Choices whose rows are on their way at a time.
 constexpr int kWide = 8;
 
-// The positions of a row's choices from k0 on, -1 for none, and eight elements of each
-// on their way.
+// The positions of a row's choices from k0 on, -1 for none, and elements of each on their
+// way.
 template <typename M>
 __device__ __forceinline__ void fetch_slots(const M &values, const int32_t *slot, int k0, int topk, int capacity, int at,
-                                            int *p, u32x4 (*w)[M::kLoads])
+                                            int *p, typename M::Raw *w)
 {
 #pragma unroll
     for (int k = 0; k < kWide; ++k) {
@@ -456,21 +476,26 @@ __device__ __forceinline__ void fetch_slots(const M &values, const int32_t *slot
         values.fetch(p[k] < 0 ? 0 : p[k], at, w[k]);
 }
 
-// Eight columns of a row by a thread.
+// Columns of a row that a thread has: 16 bytes of the values, which lie side by side across
+// the lanes.
+template <bool FROM>
+constexpr int kCols = FROM ? 8 : 4;
+
 template <bool FROM, bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs a, int chunks)
 {
-    using M = Matrix<FROM, WHOLE>;
+    constexpr int COLS = kCols<FROM>;
+    using M = Matrix<FROM, WHOLE, COLS>;
     const M values(a.values, a.capacity, a.dim);
     const int64_t n = a.rows * chunks;
     for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kThreads) {
         const int64_t r = i / chunks;
-        const int at = int(i - r * chunks) * 8;
-        float sum[8] = {};
+        const int at = int(i - r * chunks) * COLS;
+        float sum[COLS] = {};
         for (int k0 = 0; k0 < a.topk; k0 += kWide) {
             int p[kWide];
-            float by[kWide], v[8];
-            u32x4 w[kWide][M::kLoads];
+            float by[kWide], v[COLS];
+            typename M::Raw w[kWide];
             fetch_slots(values, a.slot + r * a.topk, k0, a.topk, a.capacity, at, p, w);
 #pragma unroll
             for (int k = 0; k < kWide; ++k)
@@ -479,11 +504,11 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs 
             for (int k = 0; k < kWide; ++k) {
                 values.take(p[k] < 0 ? 0 : p[k], at, w[k], v);
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
+                for (int c = 0; c < COLS; ++c)
                     sum[c] = p[k] >= 0 ? __builtin_fmaf(by[k], v[c], sum[c]) : sum[c];
             }
         }
-        store_eight<BF16, WHOLE>(a.y, r * a.dim, at, a.dim, sum);
+        store_row<BF16, WHOLE, COLS>(a.y, r * a.dim, at, a.dim, sum);
     }
 }
 
@@ -491,18 +516,20 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(CombineRowsArgs 
 template <bool FROM, bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs a)
 {
-    using M = Matrix<FROM, WHOLE>;
-    using D = Matrix<BF16, WHOLE>;
+    constexpr int COLS = kCols<FROM>;
+    using M = Matrix<FROM, WHOLE, COLS>;
+    using D = Matrix<BF16, WHOLE, COLS>;
     const M values(a.values, a.capacity, a.dim);
     const D grad(a.dy, a.rows, a.dim);
     const int lane = threadIdx.x % 64;
     for (int64_t r = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64; r < a.rows; r += int64_t(gridDim.x) * (kThreads / 64))
         for (int k0 = 0; k0 < a.topk; k0 += kWide) {
             float dot[kWide] = {};
-            for (int at = lane * 8; at < a.dim; at += 512) {
+            for (int at = lane * COLS; at < a.dim; at += 64 * COLS) {
                 int p[kWide];
-                float v[8], dy[8];
-                u32x4 w[kWide][M::kLoads], of_dy[D::kLoads];
+                float v[COLS], dy[COLS];
+                typename M::Raw w[kWide];
+                typename D::Raw of_dy;
                 grad.fetch(r, at, of_dy);
                 fetch_slots(values, a.slot + r * a.topk, k0, a.topk, a.capacity, at, p, w);
                 grad.take(r, at, of_dy, dy);
@@ -510,7 +537,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs 
                 for (int k = 0; k < kWide; ++k) {
                     values.take(p[k] < 0 ? 0 : p[k], at, w[k], v);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
+                    for (int c = 0; c < COLS; ++c)
                         dot[k] = p[k] < 0 ? 0.0f : __builtin_fmaf(dy[c], v[c], dot[k]);
                 }
             }
@@ -591,8 +618,11 @@ hipError_t launch_quantize_slots(const Op &op, hipStream_t stream)
     const int blocks = (a.dim + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK;
     (void)hipGetLastError();
     return with_form(a.bf16, whole(a.x, a.dim, a.bf16), [&](auto bf16, auto w) {
-        quantize_slots_kernel<decltype(bf16)::value, decltype(w)::value>
-            <<<dim3(unsigned(blocks) * unsigned(a.capacity / RR_QUANT_BLOCK)), dim3(kThreads), 0, stream>>>(a, blocks);
+        const dim3 grid(unsigned(blocks) * unsigned(a.capacity / RR_QUANT_BLOCK));
+        if (int64_t(a.capacity) * a.dim > kCacheBytes)
+            quantize_slots_kernel<decltype(bf16)::value, decltype(w)::value, true><<<grid, dim3(kThreads), 0, stream>>>(a, blocks);
+        else
+            quantize_slots_kernel<decltype(bf16)::value, decltype(w)::value, false><<<grid, dim3(kThreads), 0, stream>>>(a, blocks);
         return hipGetLastError();
     });
 }
@@ -603,8 +633,11 @@ hipError_t launch_quantize_weight(const Op &op, hipStream_t stream)
     const int n = (a.n + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK, k = (a.k + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK;
     (void)hipGetLastError();
     return with_form(a.bf16, whole(a.w, a.k, a.bf16), [&](auto bf16, auto w) {
-        quantize_weight_kernel<decltype(bf16)::value, decltype(w)::value>
-            <<<dim3(unsigned(n) * unsigned(k) * unsigned(a.experts)), dim3(kThreads), 0, stream>>>(a, n, k);
+        const dim3 grid(unsigned(n) * unsigned(k) * unsigned(a.experts));
+        if (int64_t(a.experts) * a.n * a.k * (a.bf16 ? 2 : 4) > kCacheBytes)
+            quantize_weight_kernel<decltype(bf16)::value, decltype(w)::value, true><<<grid, dim3(kThreads), 0, stream>>>(a, n, k);
+        else
+            quantize_weight_kernel<decltype(bf16)::value, decltype(w)::value, false><<<grid, dim3(kThreads), 0, stream>>>(a, n, k);
         return hipGetLastError();
     });
 }
@@ -612,7 +645,7 @@ hipError_t launch_quantize_weight(const Op &op, hipStream_t stream)
 hipError_t launch_combine_rows(const Op &op, hipStream_t stream)
 {
     const CombineRowsArgs a = op.get<CombineRowsArgs>();
-    const int chunks = (a.dim + 7) / 8;
+    const int cols = a.from_bf16 ? kCols<true> : kCols<false>, chunks = (a.dim + cols - 1) / cols;
     const bool w = whole(a.values, a.dim, a.from_bf16) && whole(a.y, a.dim, a.bf16);
     (void)hipGetLastError();
     return with_form(a.bf16, w, [&](auto bf16, auto all) {
