@@ -17,8 +17,10 @@ constexpr int kThreads = 256;
 // ---------------------------------------------------------------------------
 
 constexpr int kSlotThreads = 1024;
-constexpr int kFew = 1024, kOnePiece = 8192;  // choices that a small workgroup, or a large one, places alone
-constexpr int kPiece = 2048;     // the least of many
+// Choices that one workgroup places alone, which takes one launch (3200 choices 5.1 us, by
+// two 6.9 us; 8000 choices 10.1 us, by eight 6.7 us), and else a workgroup's at the least (16384
+// choices 6.9 us, with 2048 each 7.9 us).
+constexpr int kOnePiece = 4096, kPiece = 1024;
 
 __host__ __device__ inline int piece_of(int choices, int blocks)
 {
@@ -44,10 +46,9 @@ __global__ __launch_bounds__(kThreads) void slots_count_kernel(SlotsArgs a)
         a.part[int64_t(blockIdx.x) * a.experts + e] = n[e];
 }
 
-template <int THREADS>
-__global__ __launch_bounds__(THREADS) void slots_kernel(SlotsArgs a)
+__global__ __launch_bounds__(kSlotThreads) void slots_kernel(SlotsArgs a)
 {
-    constexpr int kWaves = THREADS / 64;
+    constexpr int kWaves = kSlotThreads / 64;
     __shared__ int cursor[kWaves][RR_MAX_EXPERTS];
     __shared__ int all[RR_MAX_EXPERTS], start[RR_MAX_EXPERTS + 1], earlier[RR_MAX_EXPERTS];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -63,7 +64,7 @@ __global__ __launch_bounds__(THREADS) void slots_kernel(SlotsArgs a)
             atomicAdd(&cursor[wave][e], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += THREADS) {
+    for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) {
         int here = 0, total = 0, before = 0;
         for (int w = 0; w < kWaves; ++w)
             here += cursor[w][e];
@@ -98,7 +99,7 @@ __global__ __launch_bounds__(THREADS) void slots_kernel(SlotsArgs a)
             start[a.experts] = base;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += THREADS) {
+    for (int e = threadIdx.x; e < a.experts; e += kSlotThreads) {
         int at = start[e] + earlier[e];
         for (int w = 0; w < kWaves; ++w) {
             const int n = cursor[w][e];
@@ -107,7 +108,7 @@ __global__ __launch_bounds__(THREADS) void slots_kernel(SlotsArgs a)
         }
     }
     if (blockIdx.x == 0)
-        for (int e = threadIdx.x; e <= a.experts; e += THREADS) {
+        for (int e = threadIdx.x; e <= a.experts; e += kSlotThreads) {
             a.offset[e] = start[e];
             if (e < a.experts)
                 a.count[e] = all[e];
@@ -116,8 +117,8 @@ __global__ __launch_bounds__(THREADS) void slots_kernel(SlotsArgs a)
     for (int e = int(blockIdx.x) * kWaves + wave; e < a.experts; e += a.blocks * kWaves)
         for (int p = start[e] + all[e] + lane; p < start[e + 1]; p += 64)
             a.source[p] = -1;
-    for (int64_t p = start[a.experts] + int64_t(blockIdx.x) * THREADS + threadIdx.x; p < a.capacity;
-         p += int64_t(a.blocks) * THREADS)
+    for (int64_t p = start[a.experts] + int64_t(blockIdx.x) * kSlotThreads + threadIdx.x; p < a.capacity;
+         p += int64_t(a.blocks) * kSlotThreads)
         a.source[p] = -1;
     __syncthreads();
     for (int64_t i0 = lo; i0 < hi; i0 += 64) {
@@ -572,12 +573,11 @@ unsigned grid_of(int64_t n, int64_t per, unsigned most)
 
 int32_t slots_blocks(int64_t choices)
 {
-    // one workgroup and one launch as long as that is short; then enough
-    // workgroups for the compute units
     if (choices <= kOnePiece)
         return 1;
+    // each workgroup reads the counts of all (524288 choices 19 us, by 256 of them 23 us)
     const int64_t n = (choices + kPiece - 1) / kPiece;
-    return int32_t(n < 256 ? n : 256);
+    return int32_t(n < 128 ? n : 128);
 }
 
 hipError_t launch_slots_count(const Op &op, hipStream_t stream)
@@ -592,11 +592,7 @@ hipError_t launch_slots(const Op &op, hipStream_t stream)
 {
     const SlotsArgs a = op.get<SlotsArgs>();
     (void)hipGetLastError();
-    // few choices have less to wait for with fewer waves
-    if (a.choices <= kFew)
-        slots_kernel<256><<<dim3(1), dim3(256), 0, stream>>>(a);
-    else
-        slots_kernel<kSlotThreads><<<dim3(unsigned(a.blocks)), dim3(kSlotThreads), 0, stream>>>(a);
+    slots_kernel<<<dim3(unsigned(a.blocks)), dim3(kSlotThreads), 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -685,3 +685,10 @@ def test_small_and_large_elements(dt, x_by, w_by, rows, out):
         assert (((held.t[at].double() - want).abs() <= bound) | out_of_range).all(), i
         assert x_by > 0 and w_by > 0 or not out_of_range.any()
     assert held.untouched()
+
+
+@pytest.mark.parametrize("rows,topk,experts", [(512, 8, 64), (1366, 3, 20), (70000, 2, 11), (9000, 20, 1024)])
+def test_slots_pieces(rows, topk, experts):
+    """As many choices as one workgroup places, a few more, and more than a piece each of the most workgroups."""
+    e = rr.Experts(experts, topk, rows)
+    Slots(e, choices(e, masked=0.2, skew=0.5))
