@@ -302,9 +302,10 @@ __device__ __forceinline__ void store_turned(Turned &t, unsigned char *out, int6
 }
 
 // STREAM: more than the last level cache holds.  What is transposed then leaves past the
-// caches, and w comes past them (32 experts of 4096 x 2048 in bf16: 146 us, 7.4 TB/s; none
-// of it past them 207 us, the loads alone 208 us, the other stores too 193 us).  What
-// the cache holds is read from it by the next product.
+// caches, and w comes past them (32 experts of 4096 x 2048 in bf16 in a training step: 170 us,
+// 6.3 TB/s, and 200 us with none of it past them.  Alone, and of zeros: 146 us and 207 us, the
+// loads alone past them 208 us, the other stores too 193 us).  What the cache holds is read from
+// it by the next product.
 template <bool BF16, bool WHOLE, bool STREAM>
 __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(QuantizeWeightArgs a, int blocks_n, int blocks_k)
 {
@@ -365,9 +366,10 @@ __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(QuantizeWeigh
     store_turned<STREAM>(turned, a.turned.values + (int64_t(e) * a.k + k0) * a.turned.ld + n0, a.turned.ld, a.k - k0);
 }
 
-// STREAM: as above, of what is written (65536 positions x 4096: 117 us, else 126 us; a layer of
-// 16384 choices of 16 experts, 2048 x 1408, is trained in 437 us with it, in 423 us without).
-template <bool BF16, bool WHOLE, bool STREAM>
+// The stores past the caches, as above, gain nothing inside a layer (65536 positions x 4096: 145
+// us both ways) and cost the next product what the cache would have held (16384 choices of 16
+// experts, 2048 x 1408: forward and backward 437 us instead of 423 us).
+template <bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void quantize_slots_kernel(QuantizeSlotsArgs a, int blocks_d)
 {
     __shared__ __attribute__((aligned(16))) Turned turned;
@@ -421,7 +423,7 @@ __global__ __launch_bounds__(kThreads) void quantize_slots_kernel(QuantizeSlotsA
     for (int i = threadIdx.x; i < RR_QUANT_BLOCK && d0 + i < a.dim; i += kThreads)
         a.to.powers[int64_t(d0 + i) * a.to.lds + bp] = (unsigned char)power_byte(largest[i]);
     __syncthreads();
-    store_turned<STREAM>(turned, a.to.values + int64_t(d0) * a.to.ld + p0, a.to.ld, a.dim - d0);
+    store_turned<false>(turned, a.to.values + int64_t(d0) * a.to.ld + p0, a.to.ld, a.dim - d0);
 }
 
 // ---------------------------------------------------------------------------
@@ -614,11 +616,8 @@ hipError_t launch_quantize_slots(const Op &op, hipStream_t stream)
     const int blocks = (a.dim + RR_QUANT_BLOCK - 1) / RR_QUANT_BLOCK;
     (void)hipGetLastError();
     return with_form(a.bf16, whole(a.x, a.dim, a.bf16), [&](auto bf16, auto w) {
-        const dim3 grid(unsigned(blocks) * unsigned(a.capacity / RR_QUANT_BLOCK));
-        if (int64_t(a.capacity) * a.dim > kCacheBytes)
-            quantize_slots_kernel<decltype(bf16)::value, decltype(w)::value, true><<<grid, dim3(kThreads), 0, stream>>>(a, blocks);
-        else
-            quantize_slots_kernel<decltype(bf16)::value, decltype(w)::value, false><<<grid, dim3(kThreads), 0, stream>>>(a, blocks);
+        quantize_slots_kernel<decltype(bf16)::value, decltype(w)::value>
+            <<<dim3(unsigned(blocks) * unsigned(a.capacity / RR_QUANT_BLOCK)), dim3(kThreads), 0, stream>>>(a, blocks);
         return hipGetLastError();
     });
 }
