@@ -475,6 +475,7 @@ struct Tile8 {
 
     // A workgroup's tiles, `tiles` of them.  job.span(n): the n-th; job.first(): before it
     // is opened; job.open(source, n, last): its source; job.end(span, n, acc): its results.
+    // A tile of one step is opened right after the one before it.
     template <typename Job>
     __device__ static void run(const Job &job, int tiles, char *lds)
     {
@@ -505,8 +506,10 @@ struct Tile8 {
             for (int l = 0; l < Source::kLoads; ++l)
                 source.load(l, lds, f);
             source.next();
-            if (f == 0) {
-                // what the next tile's source needs is there
+            if (f == 0 || opened > 1) {
+                // between any two calls of open() stands a wait and a barrier, here as in the
+                // loop below: what the next tile's source needs, loaded by all waves, is there,
+                // and all waves have read what the next call overwrites
                 wait_loads<0>();
                 __builtin_amdgcn_s_barrier();
             }
