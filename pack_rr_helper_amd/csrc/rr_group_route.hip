@@ -96,6 +96,16 @@ __device__ __forceinline__ double exp_from64(float z, float base)
     return d >= -double(kReach) ? e : d != d ? __builtin_nan("") : 0.0;
 }
 
+// The same in either width.
+template <typename T>
+__device__ __forceinline__ T exp_from(float z, float base)
+{
+    if constexpr (std::is_same_v<T, double>)
+        return exp_from64(z, base);
+    else
+        return expf(z - base);
+}
+
 // The two largest of the lanes of a group (LANES of them, a power of two).
 template <int G, int STEP = 0>
 __device__ __forceinline__ void best_two(double &a, double &b, int lanes)
@@ -520,12 +530,17 @@ struct Chosen {
 
 // The chosen experts' terms lie in LDS, zero at every other expert, and are zeroed
 // again once read.  Only softmax that is not renormalized (WHOLE) reads the logits.
-//   sigmoid: ds/dz = s (1 - s) with 1 - s = sigmoid(-z); softmax: dz_e = p_e (d_e - sum p d).
+//   sigmoid: ds/dz = s (1 - s) with 1 - s = sigmoid(-z); softmax: dz_e = scale p_e (g_e - sum p g),
+//   g of the chosen, else 0.
+// In 64 bits, rounded once; of WHOLE only fp32 results are (65536 x 256, top 8: 27 us, in 32 bits
+// 22 us), as bf16's own rounding is 2^14 times those of 32 bits.  Softmax's p are divided by their sum over the
+// row, so that what lse lost as a float (2^-24 of it, for every p of the row) is not theirs.
 template <bool BF16, typename R, int L, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void group_grad_kernel(GroupGradArgs a)
 {
     constexpr int G = R::G, PER = R::PER, V = R::V, kGroups = kThreads / G;
     constexpr int kKeep = ((L ? L : RR_MAX_ROUTE_TOPK) + G - 1) / G;
+    using Real = std::conditional_t<BF16, float, double>;
     __shared__ __attribute__((aligned(16))) float chosen_terms[kGroups][G * PER];
     const int lane = threadIdx.x % G, of_row = threadIdx.x / G;
     float *own = chosen_terms[of_row];
@@ -545,7 +560,7 @@ __global__ __launch_bounds__(kThreads) void group_grad_kernel(GroupGradArgs a)
         Chosen<kKeep> next = of;
         if (r + step < a.rows)
             next.template load<G>(a, r + step, lane, WHOLE);
-        float term[kKeep], dot = 0.0f;
+        float term[kKeep];
         int live = 0;
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
@@ -553,13 +568,28 @@ __global__ __launch_bounds__(kThreads) void group_grad_kernel(GroupGradArgs a)
                 of.c[i] = -1;
             live |= of.c[i] >= 0;
         }
-        if (WHOLE) {
+        // WHOLE: exp(z - lse), and what makes them sum to 1
+        Real whole[WHOLE ? PER : 1], dot = 0, inv = 0;
+        if constexpr (WHOLE) {
+            const float base = of.lse == -INFINITY ? 0.0f : of.lse;
+            row.pad(lane, a.experts);
+#pragma unroll
+            for (int s = 0; s < PER; ++s) {
+                whole[s] = exp_from<Real>(row.get(s), base);
+                inv += whole[s];
+                // a few at a time: side by side they would not fit the registers
+                if (!BF16 && s % 2)
+                    __builtin_amdgcn_sched_barrier(0);
+            }
+            const auto add = [](Real x, Real y) { return x + y; };
+            inv = across<G>(inv, add);
+            inv = inv == 0 ? Real(0) : Real(1) / inv;
 #pragma unroll
             for (int i = 0; i < kKeep; ++i) {
-                term[i] = of.c[i] >= 0 ? a.scale * of.g[i] : 0.0f;
-                dot += of.c[i] >= 0 ? expf(of.z[i] - (of.lse == -INFINITY ? 0.0f : of.lse)) * term[i] : 0.0f;
+                term[i] = of.g[i];
+                dot += of.c[i] >= 0 ? exp_from<Real>(of.z[i], base) * Real(of.g[i]) : Real(0);
             }
-            dot = lanes_sum<G>(dot);
+            dot = across<G>(dot, add) * inv;
             live = lanes_max<G>(live ? 1.0f : 0.0f) > 0.0f;
         } else {
             // in 64 bits: s of logits far below 0 are small, their quotients are not
@@ -605,10 +635,9 @@ __global__ __launch_bounds__(kThreads) void group_grad_kernel(GroupGradArgs a)
         for (int s = 0; s < PER; s += V)
             __builtin_memcpy(&d[s], __builtin_assume_aligned(own + R::expert(lane, s), V % 4 ? 4 * V : 16), 4 * V);
         if constexpr (WHOLE) {
-            const float base = of.lse == -INFINITY ? 0.0f : of.lse;
 #pragma unroll
             for (int s = 0; s < PER; ++s)
-                d[s] = live ? expf(row.get(s) - base) * (d[s] - dot) : 0.0f;
+                d[s] = live ? float(Real(a.scale) * (whole[s] * inv) * (Real(d[s]) - dot)) : 0.0f;
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
