@@ -20,7 +20,7 @@ experts are matrices, multiplied in 8 bits::
     y       = x + sum_k weight_k * (experts[choice_k] x)
 
 With ``max_norm`` the gradients are clipped to that norm over all weights before an
-update.
+update; a step whose norm is not finite changes no weight and no bias (``norm`` tells).
 
     python -m pack_rr_helper_amd.sharded_step --steps 20
     python -m pack_rr_helper_amd.sharded_step --groups 4 --products --max-norm 1
@@ -149,7 +149,9 @@ class ShardedStep:
             rr_expert_weight_grad(e, dtype, place, dyt, xt, self.dexperts)
 
     def _clip(self, grads):
-        """Scales the gradients in place to the norm that they may have over all weights, and returns theirs."""
+        """Scales the gradients in place to the norm that they may have over all weights, and returns theirs and
+        whether it is finite; if not, the gradients become zeros.  The sums of squares tell, as the norm is a
+        float: infinite too where a finite norm is past fp32's range."""
         totals, kinds = [], []
         for dtype, t in TORCH.items():
             these = [g for g in grads if g.dtype == t]
@@ -161,7 +163,10 @@ class ShardedStep:
         norm = torch.empty(1, device=grads[0].device)
         for dtype, these in kinds:
             rr_grad_clip(dtype, totals, self.max_norm, these, these, norm)
-        return norm
+        finite = torch.isfinite(sum(totals))
+        for g in grads:
+            g.masked_fill_(~finite, 0)
+        return norm, finite
 
     def step(self, x, index, teacher=None, rate=0.0):
         """One step on x [rows, dim]; index [rows, k] holds the targets (below 0,
@@ -202,11 +207,15 @@ class ShardedStep:
             else:
                 dexperts = torch.zeros_like(self.scale).index_add_(
                     0, choice.flatten(), ((self.weight * keep)[:, :, None] * dgain[:, None, :]).flatten(0, 1))
+            finite = None
             if self.max_norm is not None:
-                self.norm = self._clip([drouter, dexperts, self.dhead])
+                self.norm, finite = self._clip([drouter, dexperts, self.dhead])
             self.router -= rate * drouter
             if self.move_bias is not None:
+                before = None if finite is None else self.bias.clone()
                 self.move_bias()
+                if finite is not None:
+                    self.bias.copy_(torch.where(finite, self.bias, before))
             if self.products:
                 self.experts -= (rate * dexperts.float()).to(self.experts.dtype)
             else:
