@@ -758,8 +758,11 @@ rr_status rr_grad_square_sum(int dtype, int nTensors, const void *const *in, con
 /*
  * rr_grad_clip -- norm [1], a float: the root of the nSums sums' sum (1 ..
  * RR_MAX_SHARDS); out[i] = in[i] * factor, factor = max_norm / norm rounded to
- * a float where norm > max_norm, else 1.  A norm that is infinite or NaN leaves
- * the values as they are: the caller decides by `norm`.
+ * a float where norm > max_norm, else 1.  The factor is found in 64 bits.  Sums that
+ * are infinite or NaN together leave the values as they are, and the caller decides
+ * by them.  A finite norm past the range of a float scales the values like any
+ * other and is stored as infinite: whether the values are scaled is told by the sums,
+ * which are finite for all finite elements, and not by `norm`.
  *   out[i] may be in[i] exactly, and then is not touched where factor is 1.
  *   max_norm: 0 <= max_norm, finite.
  */

@@ -412,7 +412,9 @@ def rr_grad_square_sum(dtype, tensors, total, workspace=None, stream=None, prepa
 
 def rr_grad_clip(dtype, totals, max_norm, tensors, outs, norm, stream=None, prepare=False):
     """norm [1], the root of the totals' sum (of ranks and dtypes), and outs: the tensors
-    scaled to max_norm where norm is above it.  outs may be the tensors themselves."""
+    scaled to max_norm where norm is above it.  outs may be the tensors themselves.  Totals that are
+    not finite leave the values as they are; a finite norm past fp32's range is stored as infinite
+    and scales them, so ask the totals."""
     _esize(dtype)
     tensors, outs = list(tensors), list(outs)
     if [t.numel() for t in tensors] != [t.numel() for t in outs]:
