@@ -69,7 +69,8 @@ def test_rows_of_few_live_logits(dt):
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 @pytest.mark.parametrize("sigmoid", [True, False])
 def test_scores_are_cut(sign, sigmoid):
-    """Choice scores are compared by 43 significant bits: next to 2^20 by steps of 2^-22, the lower index first in one."""
+    """Choice scores are compared by 43 significant bits: in steps of 2^-22 from 2^20 on, of 2^-23 below, the lower index
+    first in one."""
     logits = torch.full((5, 8), -20.0, device="cuda")
     # sigmoid: 1/2, 1e-7 more, 1e-6 more; softmax of these three: about a third, 1.3e-7 and 1.3e-6 apart
     logits[:, 1:4] = torch.tensor([0.0, 4e-7, 4e-6], device="cuda")
@@ -79,8 +80,9 @@ def test_scores_are_cut(sign, sigmoid):
     x.run()
     z = logits[0].double()
     c = (torch.sigmoid(z) if sigmoid else torch.softmax(z, dim=0)) + bias.double()
-    # the cut is towards zero, and no score is within 2^-44 of a border that decides
-    cut = torch.trunc(c * 2.0 ** 22)
+    # the cut is towards zero: a negative bias leaves magnitudes below 2^20, whose 43 bits reach to 2^-23
+    part, e = torch.frexp(c)
+    cut = torch.ldexp(torch.trunc(part * 2.0 ** 43), e - 43)
     want = sorted(range(8), key=lambda i: (-cut[i].item(), i))[:3]
     assert x.choice.t.tolist() == [want] * 5
     # without a bias the same scores are apart
