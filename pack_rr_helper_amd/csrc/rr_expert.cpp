@@ -426,9 +426,13 @@ rr_status rr_quantize_slots(const rr_experts *e, int dtype, int32_t dim, const v
     uint32_t mul, shift;
     divide_by(e->topk, &mul, &shift);
     Launches l(stream);
-    l.add(launch_quantize_slots, QuantizeSlotsArgs{x, weight, source, offset, eight(values, powers, capacity), e->rows,
-                                                   int32_t(capacity), e->experts, dim, gather ? 1 : 0, dtype == RR_BF16,
-                                                   mul, shift});
+    QuantizeSlotsArgs a{x, weight, source, offset, eight(values, powers, capacity), e->rows, int32_t(capacity), e->experts,
+                        dim, gather ? 1 : 0, dtype == RR_BF16, mul, shift, 0, 0};
+    const int32_t blocks = int32_t(blocks_of(capacity)), most = kSlotBlocks / int32_t(blocks_of(dim));
+    for (; a.block0 < blocks; a.block0 += a.blocks) {
+        a.blocks = std::min(blocks - a.block0, most);
+        l.add(launch_quantize_slots, a);
+    }
     return l.finish();
 }
 

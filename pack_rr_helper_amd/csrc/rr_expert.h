@@ -91,7 +91,10 @@ struct QuantizeSlotsArgs {
     int64_t rows;
     int32_t capacity, experts, dim, gather, bf16;
     uint32_t topk_mul, topk_shift;  // n / topk = (high word of topk_mul * n + n) >> topk_shift, n < 2^31
+    int32_t block0, blocks;  // this launch's blocks of positions
 };
+// Blocks of 128 x 128 in a launch: one has less than 2^32 threads.
+constexpr int32_t kSlotBlocks = 1 << 20;
 hipError_t launch_quantize_slots(const Op &, hipStream_t);
 
 struct QuantizeWeightArgs {

@@ -375,7 +375,7 @@ __global__ __launch_bounds__(kThreads) void quantize_slots_kernel(QuantizeSlotsA
     __shared__ __attribute__((aligned(16))) Turned turned;
     __shared__ unsigned largest[RR_QUANT_BLOCK];
     const int lane = threadIdx.x % 16, part = threadIdx.x / 16;
-    const int bd = blockIdx.x % blocks_d, bp = blockIdx.x / blocks_d;
+    const int bd = blockIdx.x % blocks_d, bp = a.block0 + blockIdx.x / blocks_d;
     const int p0 = bp * RR_QUANT_BLOCK, d0 = bd * RR_QUANT_BLOCK;
     if (p0 >= a.offset[a.experts])
         return;
@@ -617,7 +617,7 @@ hipError_t launch_quantize_slots(const Op &op, hipStream_t stream)
     (void)hipGetLastError();
     return with_form(a.bf16, whole(a.x, a.dim, a.bf16), [&](auto bf16, auto w) {
         quantize_slots_kernel<decltype(bf16)::value, decltype(w)::value>
-            <<<dim3(unsigned(blocks) * unsigned(a.capacity / RR_QUANT_BLOCK)), dim3(kThreads), 0, stream>>>(a, blocks);
+            <<<dim3(unsigned(blocks) * unsigned(a.blocks)), dim3(kThreads), 0, stream>>>(a, blocks);
         return hipGetLastError();
     });
 }
