@@ -718,7 +718,9 @@ rr_status rr_expert_product(const rr_experts *e, int dtype, int32_t n, int32_t k
 /*
  * rr_expert_weight_grad -- dw[e][i][j] = sum_p dy[i][p] x[j][p] over the positions
  * of expert e, in the call's dtype; 0 for an expert without choices.  dy [n][..]
- * and x [k][..]: as rr_quantize_slots writes them.
+ * and x [k][..]: as rr_quantize_slots writes them.  A capacity of at most
+ * 2^23 - 2^12 positions (larger layers: in several calls over parts of the rows, whose results
+ * the caller adds).
  */
 rr_status rr_expert_weight_grad(const rr_experts *e, int dtype, int32_t n, int32_t k, const void *dy,
                                 const void *dy_powers, const void *x, const void *x_powers,
