@@ -880,6 +880,10 @@ hipError_t launch_expert_product(const Op &op, hipStream_t stream)
     // 8 experts of 2048 x 1024, one choice each: 6.5 us and 15.2 us; 576 choices of 64 experts,
     // 2048 x 1408: 31 us and 22 us; with more choices each it reads them too often: 64 of each
     // of 8, 2048 x 2048: 35 us and 17 us, of 2, 2048 x 1024: 9.5 us and 13.9 us.
+    // Counts are known on the device only, so that the rule takes them to be even.  Others cost
+    // streaming up to 1.6 times as long (32 choices of 8 experts, 2048 x 1024: 6.4 us, half of
+    // them one expert's 10.2 us, all of them 6.9 us), tiles next to nothing (16384 of 16, 2048 x
+    // 1408: 61 us, 57 us and 56 us; 65536 of 32, 4096 x 2048: 510 us, 534 us and 459 us).
     if (per <= 64 && int64_t(used) * tiles(a.n, 128) <= (per <= 16 ? 512 : 96))
         return per <= 16 ? narrow<1>(a, stream) : per <= 32 ? narrow<2>(a, stream) : narrow<4>(a, stream);
     if (!a.bf16)
