@@ -555,10 +555,11 @@ rr_status rr_route_grad(const rr_router *r, int dtype, int64_t rows, const void 
  *   score s_e: softmax or sigmoid of the logits; choice score c_e = s_e + bias_e,
  *     so that a bias steers the choice and not the weights (`rr_route_bias`).
  *   A group's score is the sum of its group_best largest c_e.
- * The choice is made in 64 bits: s to 2^-44 of itself, c cut to 43 significant bits (steps of
- * 2^-42 of c up to 2 c: 2^-42 about 1, 2^-36 about 100), a group's score the sum of such c.  The larger
- * comes first and the lower index among equals.  NaN counts as larger than every number, and
- * infinities as numbers beyond all others: of two groups the one with fewer c = -inf among its group_best comes first.
+ * The choice is made in 64 bits: s to 2^-44 of itself, c cut to 43 significant bits towards 0
+ * (steps of 2^-42 from |c| = 1 on, of 2^-36 from 64 on), a group's score the sum of such c.
+ * The larger comes first, the lower index among equals.  NaN counts as larger than every
+ * number, and infinities as numbers beyond all others: of two groups the one with fewer
+ * c = -inf among its group_best comes first.
  */
 typedef struct {
     int32_t experts;      /* 1 .. RR_MAX_EXPERTS, a multiple of groups */

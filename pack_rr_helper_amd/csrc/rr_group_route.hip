@@ -536,8 +536,9 @@ struct Chosen {
 //   sigmoid: ds/dz = s (1 - s) with 1 - s = sigmoid(-z); softmax: dz_e = scale p_e (g_e - sum p g),
 //   g of the chosen, else 0.
 // In 64 bits, rounded once; of WHOLE only fp32 results are (65536 x 256, top 8: 27 us, in 32 bits
-// 22 us), as bf16's own rounding is 2^14 times those of 32 bits.  Softmax's p are divided by their sum over the
-// row, so that what lse lost as a float (2^-24 of it, for every p of the row) is not theirs.
+// 22 us), as bf16's own rounding is 2^16 times those of 32 bits.  Softmax's p are divided by
+// their sum over the row, so that what lse lost as a float (2^-24 of it, for every p of the row)
+// is not theirs.
 template <bool BF16, typename R, int L, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void group_grad_kernel(GroupGradArgs a)
 {

@@ -20,7 +20,7 @@ experts are matrices, multiplied in 8 bits::
     y       = x + sum_k weight_k * (experts[choice_k] x)
 
 With ``max_norm`` the gradients are clipped to that norm over all weights before an
-update; a step whose norm is not finite changes no weight and no bias (``norm`` tells).
+update; a step whose gradients have no finite sum of squares changes no weight and no bias.
 
     python -m pack_rr_helper_amd.sharded_step --steps 20
     python -m pack_rr_helper_amd.sharded_step --groups 4 --products --max-norm 1
